@@ -365,6 +365,126 @@ relay_status_t relay_allreduce_noalloc(void* const* send, void* const* recv, siz
                                        const relay_opts_t* opts, cudaStream_t stream);
 
 /*
+ * The objective of a training step over virtual ranks. The page has no counterpart: its
+ * collectives move and sum what these calls produce (gradients, per-expert counts).
+ *
+ * ---- Output projection with a vocabulary sharded on the active ranks ----
+ *
+ * logits z[n][v] = hidden[n] . weight[v]. The vocabulary is the concatenation of A shards;
+ * shard a holds rows[a] rows of the weight (and of its gradient) in rank a's memory. The
+ * hidden rows are the whole batch's, once (after an all-gather every rank holds the same).
+ * The logits are never kept: the calls work on pieces of the vocabulary of at most
+ * piece_bytes, and hold one value per logit of a piece. When the whole batch's logits are
+ * one piece, the second logits product of the gradient is saved.
+ */
+#define RELAY_HEAD_MAX_SHARDS 8
+#define RELAY_HEAD_MAX_TOP 128
+#define RELAY_HEAD_PIECE_BYTES (1ll << 30)
+typedef struct relay_head {
+  int32_t dtype;             /* RELAY_F32 or RELAY_BF16: hidden, weight and their gradients */
+  int32_t A;                 /* shards, 1..RELAY_HEAD_MAX_SHARDS */
+  int64_t tokens, dim;       /* hidden is [tokens][dim]; tokens may be 0, dim >= 1 */
+  const void* hidden;
+  int64_t hidden_stride;     /* elements between rows, >= dim (all four strides) */
+  const void* weight[RELAY_HEAD_MAX_SHARDS]; /* shard a: [rows[a]][dim] */
+  int64_t rows[RELAY_HEAD_MAX_SHARDS];       /* >= 0; the sum in [1, 2^31 - 1] */
+  int64_t weight_stride;
+  void* d_hidden;            /* [tokens][dim], or NULL: not wanted */
+  int64_t d_hidden_stride;
+  void* d_weight[RELAY_HEAD_MAX_SHARDS];     /* all NULL: not wanted; else one per shard */
+  int64_t d_weight_stride;
+  int64_t piece_bytes;       /* 0: RELAY_HEAD_PIECE_BYTES. Less memory for a smaller value; a
+                                piece is never less than 256 columns */
+} relay_head_t;
+
+/* Bytes of workspace (device memory, any alignment, contents unspecified before and after)
+ * the two calls below need. top: 0 for relay_linear_xent, else the K of
+ * relay_linear_distill. -1 on an invalid head (relay_last_error says why). */
+int64_t relay_head_workspace_size(const relay_head_t* head, int top);
+
+/*
+ * relay_linear_xent -- softmax cross entropy against one target per row.
+ *   targets[tokens] int32: index into the concatenated vocabulary. Any value outside
+ *     [0, sum of rows) ignores the row: loss 0, d_hidden 0, no part in d_weight, and
+ *     nothing its hidden row holds (NaN included) reaches any output.
+ *   loss[tokens] fp32: log(sum_v exp z[n][v]) - z[n][target].
+ *   row_weight[tokens] fp32 (NULL: 1): dL/dloss[n]. The gradients are those of
+ *     L = sum_n row_weight[n] * loss[n] and overwrite d_hidden and d_weight.
+ * Arithmetic: products of the inputs accumulate in fp32; maxima, sums and the loss are
+ * fp32. For a bf16 head the gradient of each logit is rounded to bf16 once before its two
+ * products, which accumulate in fp32 and are rounded to bf16 once. Every sum has a fixed
+ * order: equal calls give equal bits. An infinite or NaN logit gives its row NaN.
+ * All pointers device memory, element-aligned; outputs overlap nothing else.
+ * tokens == 0 writes zeros to d_weight.
+ */
+relay_status_t relay_linear_xent(const relay_head_t* head, const int32_t* targets,
+                                 const float* row_weight, float* loss, void* workspace,
+                                 int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * relay_linear_distill -- distillation from the K largest logits of a teacher.
+ *   teacher_index[tokens][top] int32: vocabulary ids, in any order. An id outside
+ *     [0, sum of rows) is an absent entry, whatever its logit. A row with no entry, or
+ *     whose entries are all -inf, is ignored as above. An id given twice counts twice.
+ *   teacher_logits[tokens][top], teacher_dtype RELAY_F32 or RELAY_BF16.
+ *   q[n] = softmax over the row's entries of teacher_logits / temperature;
+ *   loss[n] = temperature^2 * sum_k q log(q / p), p = softmax(z / temperature) over the
+ *     whole vocabulary; temperature finite and > 0; 1 <= top <= RELAY_HEAD_MAX_TOP.
+ * Everything else is as for relay_linear_xent.
+ */
+relay_status_t relay_linear_distill(const relay_head_t* head, const void* teacher_logits,
+                                    relay_dtype_t teacher_dtype, const int32_t* teacher_index,
+                                    int top, float temperature, const float* row_weight,
+                                    float* loss, void* workspace, int64_t workspace_bytes,
+                                    cudaStream_t stream);
+
+/*
+ * ---- Expert router: top-k choice, per-expert counts, balance loss ----
+ *
+ * relay_router_forward: logits[tokens][experts] (RELAY_F32 or RELAY_BF16, row_stride
+ *   elements apart). A row is counted unless mask (NULL: all counted) holds 0 for it or no
+ *   logit of it is above -inf.
+ *   index[tokens][top] int32: the top largest logits, largest first, ties to the lower
+ *     expert; -1 for a row that is not counted. (A row with fewer than `top` logits above
+ *     -inf fills up with the lowest experts left, gate 0.)
+ *   gate[tokens][top] fp32: the softmax over all experts at index, or, with normalize != 0,
+ *     the softmax over the row's chosen logits; 0 for a row that is not counted.
+ *   counts[experts] int32: rows that chose the expert. prob_sum[experts] fp32: the sum of the
+ *     rows' softmax. Both in a fixed order of summation, and both sums over ranks: with
+ *     relay_allreduce over them between this call and relay_balance_loss, the balance
+ *     loss is that of all ranks' tokens.
+ *   1 <= top <= experts, top <= RELAY_ROUTER_MAX_TOP, experts <= RELAY_ROUTER_MAX_EXPERTS.
+ *   A NaN logit makes its row's gates and prob_sum NaN; index stays in range and distinct.
+ *   Two launches at most. workspace: relay_router_workspace_size bytes, any alignment.
+ */
+#define RELAY_ROUTER_MAX_EXPERTS 1024
+#define RELAY_ROUTER_MAX_TOP 32
+int64_t relay_router_workspace_size(int64_t tokens, int experts);
+relay_status_t relay_router_forward(const void* logits, int64_t row_stride, relay_dtype_t dtype,
+                                    int64_t tokens, int experts, int top, int normalize,
+                                    const uint8_t* mask, int32_t* index, float* gate,
+                                    int32_t* counts, float* prob_sum, void* workspace,
+                                    int64_t workspace_bytes, cudaStream_t stream);
+
+/* relay_balance_loss -- with T = sum(counts) / top counted tokens:
+ *   loss[0] = coef * experts * sum_e (counts[e] / (top * T)) * (prob_sum[e] / T)
+ *   d_prob[e] = coef * experts * counts[e] / (top * T^2), its derivative by one token's
+ *     probability of e (the counts are constants). Both 0 when T = 0. */
+relay_status_t relay_balance_loss(const int32_t* counts, const float* prob_sum, int experts,
+                                  int top, float coef, float* loss, float* d_prob,
+                                  cudaStream_t stream);
+
+/* relay_router_backward -- d_logits[tokens][experts] (dtype and strides of logits' own) from
+ *   d_gate[tokens][top] (NULL: 0) and d_prob[experts] (NULL: 0, usually relay_balance_loss's).
+ *   index is relay_router_forward's; rows whose first index is negative get 0. normalize must
+ *   be the forward's. */
+relay_status_t relay_router_backward(const void* logits, int64_t row_stride, relay_dtype_t dtype,
+                                     int64_t tokens, int experts, int top, int normalize,
+                                     const int32_t* index, const float* d_gate,
+                                     const float* d_prob, void* d_logits, int64_t d_row_stride,
+                                     cudaStream_t stream);
+
+/*
  * relay_device_status -- reads and clears the device's fault word. Passes whose sources
  * sit off the 16-byte grid stage each tile's source bytes in shared memory with a bulk
  * copy and wait for it on an mbarrier (the schedule's strided pack/unpack, item 7). That

@@ -17,4 +17,7 @@ from ._binding import (  # noqa: F401
     relay_plan_passes, relay_reduce_scatter, group_ranks, relay_multi_group,
     relay_multi_group_link_bytes, alloc_multi_scratch, relay_pack_flat, relay_unpack_flat,
     relay_allreduce_noalloc, relay_helper_size, relay_active_scratch_size,
-    relay_helper_contract_size, relay_copy)
+    relay_helper_contract_size, relay_copy,
+    HEAD_MAX_SHARDS, HEAD_MAX_TOP, ROUTER_MAX_EXPERTS, ROUTER_MAX_TOP, RelayHead, make_head,
+    relay_head_workspace_size, alloc_head_workspace, relay_linear_xent, relay_linear_distill,
+    alloc_router_workspace, relay_router_forward, relay_balance_loss, relay_router_backward)

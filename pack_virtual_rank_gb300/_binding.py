@@ -63,6 +63,23 @@ class RelayPassInfo(ctypes.Structure):
                 ("bytes_read", ctypes.c_int64), ("bytes_written", ctypes.c_int64)]
 
 
+HEAD_MAX_SHARDS = 8
+HEAD_MAX_TOP = 128
+ROUTER_MAX_EXPERTS = 1024
+ROUTER_MAX_TOP = 32
+
+
+class RelayHead(ctypes.Structure):
+    """A sharded output projection (relay_head_t); build it with ``make_head``."""
+    _fields_ = [("dtype", ctypes.c_int32), ("A", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("hidden", ctypes.c_void_p),
+                ("hidden_stride", ctypes.c_int64), ("weight", ctypes.c_void_p * HEAD_MAX_SHARDS),
+                ("rows", ctypes.c_int64 * HEAD_MAX_SHARDS), ("weight_stride", ctypes.c_int64),
+                ("d_hidden", ctypes.c_void_p), ("d_hidden_stride", ctypes.c_int64),
+                ("d_weight", ctypes.c_void_p * HEAD_MAX_SHARDS),
+                ("d_weight_stride", ctypes.c_int64), ("piece_bytes", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -127,6 +144,20 @@ def lib():
     L.relay_device_status.restype = i32
     L.relay_test_staged_wait.argtypes = [vp, vp, sz, i32, i32, vp]
     L.relay_test_staged_wait.restype = i32
+    L.relay_head_workspace_size.argtypes = [P(RelayHead), i32]
+    L.relay_head_workspace_size.restype = i64
+    L.relay_linear_xent.argtypes = [P(RelayHead), vp, vp, vp, vp, i64, vp]
+    L.relay_linear_xent.restype = i32
+    L.relay_linear_distill.argtypes = [P(RelayHead), vp, i32, vp, i32, f32, vp, vp, vp, i64, vp]
+    L.relay_linear_distill.restype = i32
+    L.relay_router_workspace_size.argtypes = [i64, i32]
+    L.relay_router_workspace_size.restype = i64
+    L.relay_router_forward.argtypes = [vp, i64, i32, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.relay_router_forward.restype = i32
+    L.relay_balance_loss.argtypes = [vp, vp, i32, i32, f32, vp, vp, vp]
+    L.relay_balance_loss.restype = i32
+    L.relay_router_backward.argtypes = [vp, i64, i32, i64, i32, i32, i32, vp, vp, vp, vp, i64, vp]
+    L.relay_router_backward.restype = i32
     if L.relay_abi_version() != 1:
         raise RuntimeError("librelay.so ABI version mismatch")
     _lib = L
@@ -423,3 +454,178 @@ def relay_copy(dst, src, max_ctas: int = 0, stream=None) -> None:
         raise ValueError("relay_copy: dst and src must have the same dtype and size")
     _check(lib().relay_copy(_any_ptr(dst), _any_ptr(src), src.numel(), dtype_code(src.dtype),
                             max_ctas, _stream(stream)))
+
+
+# ------------------------------------------- training objective: losses and router --
+
+def _array(x, name: str, dtype, shape) -> Optional[int]:
+    """Address of a contiguous CUDA tensor of the given dtype and shape."""
+    if x.dtype != dtype or tuple(x.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {shape}, got {x.dtype} of {tuple(x.shape)}")
+    return _ptr(x)
+
+
+def _matrix(x, name: str) -> int:
+    """Address of a CUDA matrix whose rows are contiguous (any row stride)."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (device memory)")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    return x.data_ptr()
+
+
+def _row_stride(x) -> int:
+    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+
+
+def _common_stride(xs, name: str) -> int:
+    strides = {x.stride(0) for x in xs if x.shape[0] > 1}
+    if len(strides) > 1:
+        raise ValueError(f"the {name} shards must have one row stride")
+    return strides.pop() if strides else max(x.shape[1] for x in xs)
+
+
+def _own_workspace(alloc, stream):
+    """A workspace for one call. The allocator frees it in the order of the current stream, so a
+    call on another stream tells it so."""
+    ws = alloc()
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            raise ValueError("pass a workspace with a raw stream handle")
+        ws.record_stream(stream)
+    return ws
+
+
+def make_head(hidden, weights: Sequence, d_hidden=None, d_weights: Optional[Sequence] = None,
+              piece_bytes: int = 0) -> RelayHead:
+    """Describe an output projection for relay_linear_xent and relay_linear_distill:
+    hidden [tokens, dim], one weight shard [rows, dim] per active rank (their concatenation is
+    the vocabulary), and the gradients to write, if any. The tensors must outlive the head (it
+    keeps references) and it can be used for any number of calls."""
+    weights = list(weights)
+    if not 1 <= len(weights) <= HEAD_MAX_SHARDS:
+        raise ValueError(f"1 to {HEAD_MAX_SHARDS} weight shards, got {len(weights)}")
+    h = RelayHead()
+    h.dtype, h.A = dtype_code(hidden.dtype), len(weights)
+    h.hidden = _matrix(hidden, "hidden")
+    h.tokens, h.dim = hidden.shape
+    h.hidden_stride = _row_stride(hidden)
+    h.piece_bytes = piece_bytes
+    for a, x in enumerate(weights):
+        h.weight[a] = _matrix(x, f"weights[{a}]")
+        h.rows[a] = x.shape[0]
+        if x.dtype != hidden.dtype or x.shape[1] != h.dim:
+            raise ValueError(f"weights[{a}] must be {hidden.dtype} with rows of {h.dim}")
+    h.weight_stride = _common_stride(weights, "weight")
+    if d_hidden is not None:
+        if d_hidden.dtype != hidden.dtype or d_hidden.shape != hidden.shape:
+            raise ValueError("d_hidden must have hidden's dtype and shape")
+        h.d_hidden = _matrix(d_hidden, "d_hidden")
+        h.d_hidden_stride = _row_stride(d_hidden)
+    if d_weights is not None:
+        d_weights = list(d_weights)
+        if [tuple(x.shape) for x in d_weights] != [tuple(x.shape) for x in weights]:
+            raise ValueError("d_weights must have the weights' shapes")
+        for a, x in enumerate(d_weights):
+            if x.dtype != hidden.dtype:
+                raise ValueError(f"d_weights[{a}] must be {hidden.dtype}")
+            h.d_weight[a] = _matrix(x, f"d_weights[{a}]")
+        h.d_weight_stride = _common_stride(d_weights, "d_weight")
+    h._tensors = (hidden, weights, d_hidden, d_weights)
+    return h
+
+
+def relay_head_workspace_size(head: RelayHead, top: int = 0) -> int:
+    n = int(lib().relay_head_workspace_size(ctypes.byref(head), top))
+    if n < 0:
+        raise RelayError(ERR_INVALID_ARGUMENT, lib().relay_last_error().decode(errors="replace"))
+    return n
+
+
+def alloc_head_workspace(head: RelayHead, device, top: int = 0):
+    """Workspace of relay_linear_xent (top = 0) or of relay_linear_distill with `top` entries."""
+    import torch
+    return torch.empty(relay_head_workspace_size(head, top), dtype=torch.uint8, device=device)
+
+
+def relay_linear_xent(head: RelayHead, targets, loss, row_weight=None, workspace=None,
+                      stream=None) -> None:
+    """Cross entropy of the projection's logits against int32 targets (outside the vocabulary:
+    the row is ignored), with the gradients the head asks for (see relay.h)."""
+    import torch
+    t = (head.tokens,)
+    w = None if row_weight is None else _array(row_weight, "row_weight", torch.float32, t)
+    if workspace is None:
+        workspace = _own_workspace(lambda: alloc_head_workspace(head, loss.device), stream)
+    _check(lib().relay_linear_xent(ctypes.byref(head), _array(targets, "targets", torch.int32, t), w,
+                                   _array(loss, "loss", torch.float32, t), workspace.data_ptr(),
+                                   workspace.numel(), _stream(stream)))
+
+
+def relay_linear_distill(head: RelayHead, teacher_logits, teacher_index, temperature: float, loss,
+                         row_weight=None, workspace=None, stream=None) -> None:
+    """Distillation from a teacher's top logits [tokens, top] (fp32 or bf16) at the int32 ids
+    teacher_index (outside the vocabulary: no entry), with the gradients the head asks for."""
+    import torch
+    t, top = (head.tokens,), teacher_index.shape[1]
+    w = None if row_weight is None else _array(row_weight, "row_weight", torch.float32, t)
+    if workspace is None:
+        workspace = _own_workspace(lambda: alloc_head_workspace(head, loss.device, top), stream)
+    _check(lib().relay_linear_distill(
+        ctypes.byref(head), _array(teacher_logits, "teacher_logits", teacher_logits.dtype, t + (top,)),
+        dtype_code(teacher_logits.dtype), _array(teacher_index, "teacher_index", torch.int32, t + (top,)),
+        top, temperature, w, _array(loss, "loss", torch.float32, t), workspace.data_ptr(),
+        workspace.numel(), _stream(stream)))
+
+
+def alloc_router_workspace(tokens: int, experts: int, device):
+    import torch
+    n = int(lib().relay_router_workspace_size(tokens, experts))
+    if n < 0:
+        raise RelayError(ERR_INVALID_ARGUMENT, lib().relay_last_error().decode(errors="replace"))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def relay_router_forward(logits, index, gate, counts, prob_sum, mask=None, normalize: bool = False,
+                         workspace=None, stream=None) -> None:
+    """Top-k experts of each row of logits [tokens, experts] (k = index.shape[1]), their gates, and
+    the per-expert counts and probability sums (see relay.h). mask: bool or uint8 per row."""
+    import torch
+    t, e = logits.shape
+    k = index.shape[1]
+    if mask is not None:
+        mask = _array(mask, "mask", torch.bool if mask.dtype == torch.bool else torch.uint8, (t,))
+    if workspace is None:
+        workspace = _own_workspace(lambda: alloc_router_workspace(t, e, logits.device), stream)
+    _check(lib().relay_router_forward(
+        _matrix(logits, "logits"), _row_stride(logits), dtype_code(logits.dtype), t, e, k, int(normalize),
+        mask, _array(index, "index", torch.int32, (t, k)), _array(gate, "gate", torch.float32, (t, k)),
+        _array(counts, "counts", torch.int32, (e,)), _array(prob_sum, "prob_sum", torch.float32, (e,)),
+        workspace.data_ptr(), workspace.numel(), _stream(stream)))
+
+
+def relay_balance_loss(counts, prob_sum, top: int, coef: float, loss, d_prob, stream=None) -> None:
+    """Balance loss of (possibly all-reduced) counts and probability sums, and its derivative by
+    one token's probability of each expert."""
+    import torch
+    e = counts.shape[0]
+    _check(lib().relay_balance_loss(
+        _array(counts, "counts", torch.int32, (e,)), _array(prob_sum, "prob_sum", torch.float32, (e,)), e,
+        top, coef, _array(loss, "loss", torch.float32, (1,)), _array(d_prob, "d_prob", torch.float32, (e,)),
+        _stream(stream)))
+
+
+def relay_router_backward(logits, index, d_logits, d_gate=None, d_prob=None, normalize: bool = False,
+                          stream=None) -> None:
+    """Gradient of the router's logits from the gates' and the probabilities' (see relay.h)."""
+    import torch
+    t, e = logits.shape
+    k = index.shape[1]
+    if d_logits.dtype != logits.dtype or d_logits.shape != logits.shape:
+        raise ValueError("d_logits must have the logits' dtype and shape")
+    dg = None if d_gate is None else _array(d_gate, "d_gate", torch.float32, (t, k))
+    dp = None if d_prob is None else _array(d_prob, "d_prob", torch.float32, (e,))
+    _check(lib().relay_router_backward(
+        _matrix(logits, "logits"), _row_stride(logits), dtype_code(logits.dtype), t, e, k, int(normalize),
+        _array(index, "index", torch.int32, (t, k)), dg, dp, _matrix(d_logits, "d_logits"),
+        _row_stride(d_logits), _stream(stream)))

@@ -1,0 +1,92 @@
+// head.h -- internal: the output projection with a sharded vocabulary (relay_linear_xent,
+// relay_linear_distill): geometry, workspace and the launches behind the entry points.
+//
+// Vocabulary columns are numbered in a padded space: every shard starts at a multiple of
+// kHeadTile columns, so that a tile of columns, of the logits' gradient or of a product's
+// inner dimension lies in one shard. Padding columns have no weight row; their
+// gradient is 0.
+//
+// Rows are compacted: the rows that take part ("live") are copied, in order, to the front of
+// the workspace copy of hidden, and rows after them up to a multiple of kHeadRowTile hold 0.
+// An ignored row is therefore never multiplied by anything (NaN * 0 is NaN), and costs
+// nothing. How many rows are live is known on the device only: launches are sized for
+// all of them and leave early.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "relay.h"
+
+namespace relay {
+
+constexpr int kHeadTile = 256;     // columns a shard is padded to
+constexpr int kHeadRowTile = 128;  // rows the live rows are padded to
+
+struct HeadGeom {
+  int32_t A, top;                           // shards; entries per row (1 for cross entropy)
+  int32_t tokens, dim;
+  int32_t tile0[RELAY_HEAD_MAX_SHARDS + 1]; // first padded tile of each shard, then the total
+  int32_t rows[RELAY_HEAD_MAX_SHARDS];
+  int32_t base[RELAY_HEAD_MAX_SHARDS];      // first vocabulary id of each shard
+  int32_t vocab;
+  int32_t mpad;                             // tokens rounded up to kHeadRowTile
+  float tau, inv_tau;
+};
+
+#ifdef __CUDACC__
+__host__ __device__ __forceinline__
+#else
+inline
+#endif
+int head_shard_of_tile(const HeadGeom& g, int tile) {
+  int a = 0;
+  while (a + 1 < g.A && tile >= g.tile0[a + 1]) ++a;
+  return a;
+}
+
+// Everything a call works with on the device.
+struct HeadWork {
+  int32_t* n_live;    // [1]
+  int32_t* perm;      // [mpad] packed row -> row of hidden
+  float* wrow;        // [mpad] row weight * tau (0 past the live rows)
+  void* hid;          // [mpad][dim_pad] packed hidden
+  int32_t dim_pad;
+  uint8_t* live;      // [tokens]            (distill)
+  int32_t* ent_col;   // [tokens][top] entries' padded columns, ascending; INT32_MAX: absent
+  float* ent_q;       // [tokens][top]
+  float* ent_z;       // [tokens][top] the entries' logits / tau
+  float2* part;       // [tiles][mpad] (max, sum of exp) of a row's tile
+  float* lse;         // [mpad]
+  void* grad;         // [mpad][piece columns] gradient of the logits of one piece
+  int64_t grad_ld;    // columns per row
+  float* dh;          // [mpad][dim] fp32 sum of d_hidden over pieces
+};
+
+struct HeadShards {
+  const void* w[RELAY_HEAD_MAX_SHARDS];
+  void* dw[RELAY_HEAD_MAX_SHARDS];
+  int64_t w_ld, dw_ld;
+};
+
+// head_rows.cu
+cudaError_t head_teacher(const HeadGeom& g, const HeadWork& w, const void* teacher, int teacher_dtype,
+                         const int32_t* index, cudaStream_t s);
+cudaError_t head_pack(const HeadGeom& g, const HeadWork& w, int dtype, bool distill,
+                      const void* hidden, int64_t hidden_ld, const int32_t* targets,
+                      const float* row_weight, float* loss, void* d_hidden, int64_t d_hidden_ld,
+                      cudaStream_t s);
+cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, float* loss,
+                         cudaStream_t s);
+cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, void* d_hidden,
+                          int64_t d_hidden_ld, cudaStream_t s);
+
+// head_gemm.cu
+cudaError_t head_logits(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
+                        int tile_lo, int tile_hi, bool gradient, cudaStream_t s);
+cudaError_t head_dhidden(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
+                         int tile_lo, int tile_hi, bool first, cudaStream_t s);
+cudaError_t head_dweight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
+                         int tile_lo, int tile_hi, cudaStream_t s);
+
+}  // namespace relay
