@@ -46,6 +46,7 @@ def _stale() -> bool:
     deps = [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, "program.h"),
                                                        os.path.join(CSRC, "device.cuh"),
                                                        os.path.join(CSRC, "head.h"),
+                                                       os.path.join(CSRC, "tc.cuh"),
                                                        os.path.join(INCLUDE, "relay.h"), __file__]
     return any(os.path.getmtime(d) > t for d in deps)
 

@@ -10,6 +10,7 @@
 #include <string>
 #include <vector>
 
+#include "head.h"
 #include "program.h"
 
 namespace relay {
@@ -778,6 +779,12 @@ relay_status_t relay_device_status(void) {
     return fail(RELAY_ERR_CUDA,
                 "a bounded wait in a relay kernel gave up (a bulk copy into shared memory did "
                 "not land in time); the affected tiles were not written");
+  const cudaError_t he = head_read_fault(&fault);
+  if (he != cudaSuccess) return fail(RELAY_ERR_CUDA, cudaGetErrorString(he));
+  if (fault)
+    return fail(RELAY_ERR_CUDA,
+                "a bounded wait in a product of relay_linear_xent or relay_linear_distill gave up; "
+                "the call's outputs are unspecified");
   return RELAY_OK;
 }
 

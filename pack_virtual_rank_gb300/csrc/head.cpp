@@ -1,11 +1,15 @@
 // head.cpp -- relay_linear_xent and relay_linear_distill: validation, workspace layout and
 // the order of launches.
 //
-//   rows      the entries of a row (distill), then the live rows packed to the front
-//   logits    every piece: tile maxima and sums, and the logits at the entries
+//   rows      the entries of a row (distill), then the live rows packed to the front; the weight
+//             packed too where its rows cannot be read through tensor maps, or are fp32
+//   logits    tile maxima and sums, and the logits at the entries
 //   combine   log-sum-exp and loss of each row
 //   gradient  every piece: gradient of the logits, d_hidden += its product with the weight,
 //             d_weight of the piece's rows = its transposed product with hidden
+//
+// When all the logits of the batch make one piece, the first pass keeps their exponentials and
+// the gradient is a scaling of them; otherwise each piece multiplies its logits again.
 #include <limits.h>
 #include <string.h>
 
@@ -78,21 +82,28 @@ struct Layout {
 struct Arrangement {
   HeadWork w;
   int tiles_per_piece;
+  bool keep;  // one piece: the first pass keeps its exponentials
   int64_t bytes;
 };
 
 Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t base) {
   Arrangement ar{};
-  const int E = esize_of(h.dtype);
+  const int planes = head_planes(h.dtype);
   const int tiles = g.tile0[RELAY_HEAD_MAX_SHARDS];
   const bool dh = h.d_hidden != nullptr, dw = wants_dw(h);
+  // tensor maps want 16-byte aligned rows
+  bool pack = h.dtype == RELAY_F32;
+  for (int a = 0; a < h.A; ++a)
+    pack |= h.rows[a] > 0 && (reinterpret_cast<uintptr_t>(h.weight[a]) % 16 || h.weight_stride % 8);
   Layout l{base};
   HeadWork& w = ar.w;
-  w.dim_pad = (int32_t)up(g.dim, 16 / E);
+  w.dim_pad = (int32_t)up(g.dim, 8);
+  w.splits = 1;
   w.n_live = reinterpret_cast<int32_t*>(l.take(4));
   w.perm = reinterpret_cast<int32_t*>(l.take(4ll * g.mpad));
   w.wrow = reinterpret_cast<float*>(l.take(4ll * g.mpad));
-  w.hid = reinterpret_cast<void*>(l.take((int64_t)g.mpad * w.dim_pad * E));
+  w.hid = reinterpret_cast<uint16_t*>(l.take(2ll * planes * g.mpad * w.dim_pad));
+  if (pack) w.wpack = reinterpret_cast<uint16_t*>(l.take(2ll * planes * tiles * kHeadTile * w.dim_pad));
   if (top > 0) w.live = reinterpret_cast<uint8_t*>(l.take(g.tokens));
   const int64_t ents = (int64_t)g.tokens * g.top;
   w.ent_col = reinterpret_cast<int32_t*>(l.take(4 * ents));
@@ -103,11 +114,15 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
   ar.tiles_per_piece = tiles;
   if ((dh || dw) && g.mpad > 0) {
     const int64_t cap = h.piece_bytes > 0 ? h.piece_bytes : RELAY_HEAD_PIECE_BYTES;
-    const int64_t per_tile = (int64_t)g.mpad * kHeadTile * E;
+    const int64_t per_tile = 2ll * planes * g.mpad * kHeadTile;
     ar.tiles_per_piece = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, cap / per_tile));
+    ar.keep = ar.tiles_per_piece == tiles;
     w.grad_ld = (int64_t)ar.tiles_per_piece * kHeadTile;
-    w.grad = reinterpret_cast<void*>(l.take(per_tile * ar.tiles_per_piece));
-    if (dh) w.dh = reinterpret_cast<float*>(l.take(4ll * g.mpad * g.dim));
+    w.grad = reinterpret_cast<uint16_t*>(l.take(per_tile * ar.tiles_per_piece));
+    if (dh) {
+      w.splits = head_splits(g, ar.tiles_per_piece);
+      w.dh = reinterpret_cast<float*>(l.take(4ll * w.splits * g.mpad * g.dim));
+    }
   }
   ar.bytes = (int64_t)(l.at - base);
   return ar;
@@ -213,12 +228,16 @@ relay_status_t run_head(const relay_head_t& h, const HeadGeom& g, int top, const
   if (distill) RELAY_HEAD_TRY(head_teacher(g, w, teacher, teacher_dtype, entries, stream));
   RELAY_HEAD_TRY(head_pack(g, w, h.dtype, distill, h.hidden, h.hidden_stride, entries, row_weight, loss,
                            h.d_hidden, h.d_hidden_stride, stream));
-  RELAY_HEAD_TRY(head_logits(g, w, sh, h.dtype, 0, tiles, false, stream));
+  if (w.wpack != nullptr) RELAY_HEAD_TRY(head_pack_weight(g, w, sh, h.dtype, stream));
+  RELAY_HEAD_TRY(head_logits(g, w, sh, h.dtype, 0, tiles, ar.keep ? kHeadStatsKeep : kHeadStats, stream));
   RELAY_HEAD_TRY(head_combine(g, w, distill, loss, stream));
   if (!dh && !dw) return RELAY_OK;
   for (int t = 0; t < tiles; t += ar.tiles_per_piece) {
     const int hi = std::min(tiles, t + ar.tiles_per_piece);
-    RELAY_HEAD_TRY(head_logits(g, w, sh, h.dtype, t, hi, true, stream));
+    if (ar.keep)
+      RELAY_HEAD_TRY(head_scale(g, w, h.dtype, stream));
+    else
+      RELAY_HEAD_TRY(head_logits(g, w, sh, h.dtype, t, hi, kHeadGradient, stream));
     if (dh) RELAY_HEAD_TRY(head_dhidden(g, w, sh, h.dtype, t, hi, t == 0, stream));
     if (dw) RELAY_HEAD_TRY(head_dweight(g, w, sh, h.dtype, t, hi, stream));
   }

@@ -45,22 +45,30 @@ int head_shard_of_tile(const HeadGeom& g, int tile) {
   return a;
 }
 
+// Matrices the products read are bf16. An fp32 value is held as three bf16 parts that sum to
+// it (to 2^-26 of it), in three planes; a product of two such matrices is the sum of the six
+// products of parts above 2^-24.
+constexpr int kHeadPlanesF32 = 3;
+inline int head_planes(int dtype) { return dtype == RELAY_F32 ? kHeadPlanesF32 : 1; }
+
 // Everything a call works with on the device.
 struct HeadWork {
   int32_t* n_live;    // [1]
   int32_t* perm;      // [mpad] packed row -> row of hidden
   float* wrow;        // [mpad] row weight * tau (0 past the live rows)
-  void* hid;          // [mpad][dim_pad] packed hidden
-  int32_t dim_pad;
+  uint16_t* hid;      // [planes][mpad][dim_pad] packed hidden
+  int32_t dim_pad;    // a multiple of 8
+  uint16_t* wpack;    // [planes][tiles * kHeadTile][dim_pad] packed weight, or NULL: read in place
   uint8_t* live;      // [tokens]            (distill)
   int32_t* ent_col;   // [tokens][top] entries' padded columns, ascending; INT32_MAX: absent
   float* ent_q;       // [tokens][top]
   float* ent_z;       // [tokens][top] the entries' logits / tau
-  float2* part;       // [tiles][mpad] (max, sum of exp) of a row's tile
-  float* lse;         // [mpad]
-  void* grad;         // [mpad][piece columns] gradient of the logits of one piece
+  float2* part;       // [tiles][mpad] (max, sum of exp) of a row's tile, log2 units
+  float* lse;         // [mpad] log2 units
+  uint16_t* grad;     // [planes][mpad][grad_ld] of one piece: exponentials, then the gradient
   int64_t grad_ld;    // columns per row
-  float* dh;          // [mpad][dim] fp32 sum of d_hidden over pieces
+  float* dh;          // [splits][mpad][dim] fp32 partial sums of d_hidden
+  int32_t splits;
 };
 
 struct HeadShards {
@@ -76,17 +84,25 @@ cudaError_t head_pack(const HeadGeom& g, const HeadWork& w, int dtype, bool dist
                       const void* hidden, int64_t hidden_ld, const int32_t* targets,
                       const float* row_weight, float* loss, void* d_hidden, int64_t d_hidden_ld,
                       cudaStream_t s);
+cudaError_t head_pack_weight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
+                             cudaStream_t s);
 cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, float* loss,
                          cudaStream_t s);
+cudaError_t head_scale(const HeadGeom& g, const HeadWork& w, int dtype, cudaStream_t s);
 cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, void* d_hidden,
                           int64_t d_hidden_ld, cudaStream_t s);
 
 // head_gemm.cu
+enum HeadLogits { kHeadStats, kHeadStatsKeep, kHeadGradient };
 cudaError_t head_logits(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
-                        int tile_lo, int tile_hi, bool gradient, cudaStream_t s);
+                        int tile_lo, int tile_hi, HeadLogits mode, cudaStream_t s);
 cudaError_t head_dhidden(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
                          int tile_lo, int tile_hi, bool first, cudaStream_t s);
 cudaError_t head_dweight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
                          int tile_lo, int tile_hi, cudaStream_t s);
+// Ways to cut the vocabulary for d_hidden so that its tiles fill the GPU.
+int head_splits(const HeadGeom& g, int tiles);
+// Reads and clears the products' fault word.
+cudaError_t head_read_fault(unsigned* fault);
 
 }  // namespace relay

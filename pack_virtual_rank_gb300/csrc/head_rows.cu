@@ -39,6 +39,45 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// The three bf16 parts of an fp32 value. A value that rounds to infinity is cut instead, and an
+// infinity or NaN is its first part alone.
+__device__ __forceinline__ void parts_of(float v, uint16_t (&o)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    uint32_t r = bf16x2_rn(v, 0.0f) << 16;
+    if ((r & 0x7f800000u) == 0x7f800000u && v == v) r = __float_as_uint(v) & 0xffff0000u;
+    o[i] = (uint16_t)(r >> 16);
+    const float left = __fsub_rn(v, __uint_as_float(r));
+    v = (r & 0x7f800000u) == 0x7f800000u ? 0.0f : left;
+  }
+}
+
+// Copies one row to its packed place: bf16 as it is, fp32 in three parts, `plane` elements apart.
+// Columns from dim to pad, and all of them when from is NULL, are 0.
+__device__ __forceinline__ void pack_row(uint16_t* to, int64_t, const uint16_t* from, int dim, int pad, bool vec) {
+  const int whole_vecs = from != nullptr && vec ? dim / 8 : 0;
+  for (int v = threadIdx.x; v < whole_vecs; v += kThreadsRows)
+    reinterpret_cast<uint4*>(to)[v] = ld_stream_v4(from + v * 8);
+  for (int d = whole_vecs * 8 + threadIdx.x; d < pad; d += kThreadsRows)
+    to[d] = from != nullptr && d < dim ? from[d] : (uint16_t)0;
+}
+__device__ __forceinline__ void pack_row(uint16_t* to, int64_t plane, const float* from, int dim, int pad, bool) {
+  for (int d = threadIdx.x; d < pad; d += kThreadsRows) {
+    uint16_t o[3] = {0, 0, 0};
+    if (from != nullptr && d < dim) parts_of(from[d], o);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) to[i * plane + d] = o[i];
+  }
+}
+
+// The padded weight: one block per padded row.
+template <class T>
+__global__ void __launch_bounds__(kThreadsRows) pack_weight_kernel(const HeadGeom g, const HeadWork w, const HeadShards sh) {
+  const int row = blockIdx.x, a = head_shard_of_tile(g, row / kHeadTile), v = row - g.tile0[a] * kHeadTile;
+  const T* from = v < g.rows[a] ? static_cast<const T*>(sh.w[a]) + v * sh.w_ld : nullptr;
+  pack_row(w.wpack + (int64_t)row * w.dim_pad, (int64_t)gridDim.x * w.dim_pad, from, g.dim, w.dim_pad, false);
+}
+
 // One warp per row: the entries' columns in ascending order (by counting, each lane holds up to
 // four), and the teacher's probabilities beside them. An id given twice keeps two entries.
 template <class T>
@@ -130,7 +169,7 @@ __global__ void __launch_bounds__(kThreadsRows)
   int packed = s_before;          // live rows before row r
   const int read_end = (total + kHeadRowTile - 1) / kHeadRowTile * kHeadRowTile;
   if (blockIdx.x == 0 && threadIdx.x == 0) *w.n_live = total;
-  T* out = static_cast<T*>(w.hid);
+  const int64_t plane = (int64_t)g.mpad * w.dim_pad;
   for (int r = lo; r < hi; ++r) {
     const bool live = row_live<DISTILL>(g, w, targets, r);
     const int place = live ? packed : total + (r - packed);
@@ -147,18 +186,7 @@ __global__ void __launch_bounds__(kThreadsRows)
     if (!live && dh != nullptr)
       for (int d = threadIdx.x; d < g.dim; d += kThreadsRows) store_from_f32(dh + r * dh_ld + d, 0.0f);
     if (!live && place >= read_end) continue;
-    T* to = out + (int64_t)place * w.dim_pad;
-    const T* from = hidden + r * ld;
-    constexpr int kLanes = 16 / sizeof(T);
-    if (live && vec) {
-      for (int v = threadIdx.x; v < g.dim / kLanes; v += kThreadsRows)
-        reinterpret_cast<uint4*>(to)[v] = ld_stream_v4(from + v * kLanes);
-      for (int d = g.dim / kLanes * kLanes + threadIdx.x; d < w.dim_pad; d += kThreadsRows)
-        to[d] = d < g.dim ? from[d] : T(0);
-    } else {
-      for (int d = threadIdx.x; d < w.dim_pad; d += kThreadsRows)
-        to[d] = live && d < g.dim ? from[d] : T(0);
-    }
+    pack_row(w.hid + (int64_t)place * w.dim_pad, plane, live ? hidden + r * ld : nullptr, g.dim, w.dim_pad, vec);
   }
   // places past the last row of the batch
   if (blockIdx.x == gridDim.x - 1)
@@ -168,7 +196,7 @@ __global__ void __launch_bounds__(kThreadsRows)
         w.wrow[place] = 0.0f;
       }
       if (place < read_end)
-        for (int d = threadIdx.x; d < w.dim_pad; d += kThreadsRows) out[(int64_t)place * w.dim_pad + d] = T(0);
+        pack_row(w.hid + (int64_t)place * w.dim_pad, plane, static_cast<const T*>(nullptr), g.dim, w.dim_pad, false);
     }
 }
 
@@ -189,7 +217,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
       const float2 p = w.part[(int64_t)t * g.mpad + row];
       const float top = fmaxf(m, p.x);
       // -inf - -inf: a side that holds nothing yet adds nothing
-      s = (m > -INFINITY || s != s ? s * expf(m - top) : 0.0f) + (p.x > -INFINITY || p.y != p.y ? p.y * expf(p.x - top) : 0.0f);
+      s = (m > -INFINITY || s != s ? s * exp2f(m - top) : 0.0f) + (p.x > -INFINITY || p.y != p.y ? p.y * exp2f(p.x - top) : 0.0f);
       m = top;
     }
   s_max[warp][lane] = m;
@@ -198,11 +226,11 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
   if (warp != 0 || row >= live) return;
   for (int i = 1; i < kCombineWarps; ++i) {
     const float pm = s_max[i][lane], ps = s_sum[i][lane], top = fmaxf(m, pm);
-    s = (m > -INFINITY || s != s ? s * expf(m - top) : 0.0f) + (pm > -INFINITY || ps != ps ? ps * expf(pm - top) : 0.0f);
+    s = (m > -INFINITY || s != s ? s * exp2f(m - top) : 0.0f) + (pm > -INFINITY || ps != ps ? ps * exp2f(pm - top) : 0.0f);
     m = top;
   }
-  const float lse = m + logf(s);
-  w.lse[row] = lse;
+  const float lse2 = m + log2f(s), lse = lse2 * 0.6931471805599453f;
+  w.lse[row] = lse2;
   const int r = w.perm[row];
   const int64_t at = (int64_t)r * g.top;
   if (!DISTILL) {
@@ -218,6 +246,66 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
   }
 }
 
+// Kept exponentials to the gradient of the logits, in place: each is relative to its tile's
+// maximum, so a factor per row and tile makes it a probability times the row's weight. The
+// entries' columns are computed from their fp32 logits instead: p - 1 of a confident row
+// would otherwise be the rounding error of p. A block takes 2048 columns of a row; rows after the
+// live ones, as far as products read them, become 0.
+constexpr int kScaleCols = kThreadsRows * 8;
+template <int PLANES>
+__global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, const HeadWork w) {
+  const int live = *w.n_live, row = blockIdx.x;
+  if (row >= (live + kHeadRowTile - 1) / kHeadRowTile * kHeadRowTile) return;
+  const int col0 = blockIdx.y * kScaleCols, col = col0 + threadIdx.x * 8;
+  const int cols = g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
+  const int64_t plane = (int64_t)g.mpad * w.grad_ld;
+  uint16_t* line = w.grad + (int64_t)row * w.grad_ld;
+  const bool on = row < live;
+  const float lse = on ? w.lse[row] : 0.0f, weight = on ? w.wrow[row] : 0.0f;
+  if (col < cols) {
+    const float f = on ? weight * exp2f(w.part[(int64_t)(col / kHeadTile) * g.mpad + row].x - lse) : 0.0f;
+    uint4 in[PLANES], out[PLANES];
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < PLANES; ++i) in[i] = *reinterpret_cast<const uint4*>(line + i * plane + col);
+    TBF16::unpack(in[0], v);
+    if (PLANES > 1) {
+      float x[8], y[8];
+      TBF16::unpack(in[PLANES - 2], x);
+      TBF16::unpack(in[PLANES - 1], y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(__fadd_rn(y[j], x[j]), v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = on ? v[j] * f : 0.0f;
+#pragma unroll
+    for (int i = 0; i < PLANES; ++i) {
+      out[i] = TBF16::pack(v);
+      float r[8];
+      TBF16::unpack(out[i], r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fsub_rn(v[j], r[j]);
+      *reinterpret_cast<uint4*>(line + i * plane + col) = out[i];
+    }
+  }
+  if (!on) return;
+  __syncthreads();
+  const int64_t at = (int64_t)w.perm[row] * g.top;
+  for (int k = threadIdx.x; k < g.top; k += kThreadsRows) {
+    const int c = w.ent_col[at + k];
+    if (c < col0 || c >= col0 + kScaleCols || c >= cols || (k > 0 && w.ent_col[at + k - 1] == c)) continue;
+    float q = 0.0f;  // an id given several times: its first entry sums them
+    for (int j = k; j < g.top && w.ent_col[at + j] == c; ++j) q += w.ent_q[at + j];
+    float v = weight * (exp2f(fmaf(w.ent_z[at + k], 1.4426950408889634f, -lse)) - q);
+#pragma unroll
+    for (int i = 0; i < PLANES; ++i) {
+      const uint32_t r = bf16x2_rn(v, 0.0f) & 0xffffu;
+      line[i * plane + c] = (uint16_t)r;
+      v = __fsub_rn(v, __uint_as_float(r << 16));
+    }
+  }
+}
+
 template <class T>
 __global__ void __launch_bounds__(kThreadsRows)
     write_dh_kernel(const HeadGeom g, const HeadWork w, T* dh, int64_t ld) {
@@ -225,7 +313,11 @@ __global__ void __launch_bounds__(kThreadsRows)
   for (int row = blockIdx.x; row < live; row += gridDim.x) {
     T* to = dh + (int64_t)w.perm[row] * ld;
     const float* from = w.dh + (int64_t)row * g.dim;
-    for (int d = threadIdx.x; d < g.dim; d += kThreadsRows) store_from_f32(to + d, from[d]);
+    for (int d = threadIdx.x; d < g.dim; d += kThreadsRows) {
+      float sum = from[d];
+      for (int i = 1; i < w.splits; ++i) sum += from[(int64_t)i * g.mpad * g.dim + d];
+      store_from_f32(to + d, sum);
+    }
   }
 }
 
@@ -275,6 +367,25 @@ cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, flo
     combine_kernel<true><<<blocks, 32 * kCombineWarps, 0, s>>>(g, w, loss);
   else
     combine_kernel<false><<<blocks, 32 * kCombineWarps, 0, s>>>(g, w, loss);
+  return cudaGetLastError();
+}
+
+cudaError_t head_pack_weight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, cudaStream_t s) {
+  const int blocks = g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
+  if (dtype == RELAY_BF16)
+    pack_weight_kernel<uint16_t><<<blocks, kThreadsRows, 0, s>>>(g, w, sh);
+  else
+    pack_weight_kernel<float><<<blocks, kThreadsRows, 0, s>>>(g, w, sh);
+  return cudaGetLastError();
+}
+
+cudaError_t head_scale(const HeadGeom& g, const HeadWork& w, int dtype, cudaStream_t s) {
+  const int cols = g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
+  const dim3 grid(g.mpad, ceil_div(cols, kScaleCols));  // few column blocks: a piece is bounded
+  if (dtype == RELAY_BF16)
+    scale_kernel<1><<<grid, kThreadsRows, 0, s>>>(g, w);
+  else
+    scale_kernel<kHeadPlanesF32><<<grid, kThreadsRows, 0, s>>>(g, w);
   return cudaGetLastError();
 }
 
