@@ -379,7 +379,7 @@ relay_status_t relay_allreduce_noalloc(void* const* send, void* const* recv, siz
  */
 #define RELAY_HEAD_MAX_SHARDS 8
 #define RELAY_HEAD_MAX_TOP 128
-#define RELAY_HEAD_PIECE_BYTES (1ll << 30)
+#define RELAY_HEAD_PIECE_BYTES (2ll << 30)
 typedef struct relay_head {
   int32_t dtype;             /* RELAY_F32 or RELAY_BF16: hidden, weight and their gradients */
   int32_t A;                 /* shards, 1..RELAY_HEAD_MAX_SHARDS */

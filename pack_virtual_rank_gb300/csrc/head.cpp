@@ -109,7 +109,7 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
   w.ent_col = reinterpret_cast<int32_t*>(l.take(4 * ents));
   w.ent_q = reinterpret_cast<float*>(l.take(4 * ents));
   w.ent_z = reinterpret_cast<float*>(l.take(4 * ents));
-  w.part = reinterpret_cast<float2*>(l.take(8ll * tiles * g.mpad));
+  w.part = reinterpret_cast<float2*>(l.take(8ll * tiles * (kHeadTile / kHeadStatTile) * g.mpad));
   w.lse = reinterpret_cast<float*>(l.take(4ll * g.mpad));
   ar.tiles_per_piece = tiles;
   if ((dh || dw) && g.mpad > 0) {

@@ -22,6 +22,15 @@ namespace relay {
 
 constexpr int kHeadTile = 256;     // columns a shard is padded to
 constexpr int kHeadRowTile = 128;  // rows the live rows are padded to
+constexpr int kHeadStatTile = 128; // columns one (max, sum) of a row stands for
+
+// The form in which the exponentials of a bf16 head are kept: how far a logit lies below the
+// largest of its row's kHeadStatTile columns, in log2 units, in steps of 2^-10 and 16 bits. That is
+// within 2^-11 ln 2 = 3.4e-4 of the exponential, a sixth of bf16's step, at the same width, so
+// the gradient is as good as rounded once; bf16 exponentials would round it twice (1.7e-3 each,
+// in the mean). 65535 stands for 0 (an exponential 2^-64 of the largest).
+constexpr float kCodeSteps = 1024.0f;
+constexpr float kCodeZero = 65535.0f;
 
 struct HeadGeom {
   int32_t A, top;                           // shards; entries per row (1 for cross entropy)
@@ -63,9 +72,9 @@ struct HeadWork {
   int32_t* ent_col;   // [tokens][top] entries' padded columns, ascending; INT32_MAX: absent
   float* ent_q;       // [tokens][top]
   float* ent_z;       // [tokens][top] the entries' logits / tau
-  float2* part;       // [tiles][mpad] (max, sum of exp) of a row's tile, log2 units
+  float2* part;       // [2 tiles][mpad] (max, sum of exp) of kHeadStatTile columns, log2 units
   float* lse;         // [mpad] log2 units
-  uint16_t* grad;     // [planes][mpad][grad_ld] of one piece: exponentials, then the gradient
+  uint16_t* grad;     // [planes][mpad][grad_ld] of one piece: codes or exponentials, then the gradient
   int64_t grad_ld;    // columns per row
   float* dh;          // [splits][mpad][dim] fp32 partial sums of d_hidden
   int32_t splits;

@@ -7,7 +7,7 @@
 // One CTA per SM walks 128 x 256 tiles of the result. A producer thread brings 64 elements of the
 // inner dimension at a time into a ring of shared memory stages (tensor map loads, 128-byte
 // swizzle); one thread issues the products, whose accumulators alternate between two halves of
-// tensor memory; four warps turn one half into its result while the other fills. Operands are
+// tensor memory; eight warps turn one half into its result while the other fills. Operands are
 // read as they lie: where the outer dimension is the contiguous one (weight in d_hidden, both in
 // d_weight) the descriptors say so, and nothing is transposed in memory.
 //
@@ -32,13 +32,29 @@ __device__ unsigned g_head_fault;
 constexpr int kBM = 128, kBN = 256, kBK = 64;
 constexpr int kStages = 4;
 constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
-constexpr int kOutWarpBytes = 32 * 64 * 2;             // 32 rows x 64 columns of bf16
-constexpr int kOutBytes = 4 * 2 * kOutWarpBytes;       // four warps, two buffers each
+constexpr int kFinishWarps = 8;                        // warps that turn accumulators into results
+constexpr int kOutWarpBytes = 32 * 64 * 2;             // 32 rows x 64 columns of 16 bits, one per warp
+constexpr int kOutBytes = kFinishWarps * kOutWarpBytes;
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kOutBytes;
-constexpr int kGemmThreads = 192;
+// Three groups of four warps: one that loads and multiplies (two threads of it), two that
+// finish. The finishing threads hold 128 accumulators each, so registers move to them: at launch
+// every thread has kLaunchRegs, and 56 + 2 * 224 = 3 * 168. The launch checks that the kernel was
+// given exactly that many.
+constexpr int kGemmThreads = 128 + 32 * kFinishWarps;
+constexpr int kLaunchRegs = 168, kFeedRegs = 56, kFinishRegs = 224;
+static_assert(kFeedRegs + 2 * kFinishRegs == 3 * kLaunchRegs, "the groups' registers add up to the launch's");
+constexpr int kMine = kBN / 2;                         // columns of a tile's row one thread finishes
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum Product { kStats, kStatsKeep, kGradient, kDHidden, kDWeight };
+
+// Inner steps (of 64) summed in tensor memory before the sum moves on into registers. The tensor
+// cores cut what does not fit 24 bits at every product instead of rounding it, which drifts with
+// the length of the chain: at dim 4096 in one chain the loss was several times as far from its
+// 64-bit value as an fp32 sum. Chains of 32 products (48 for the six products of fp32 parts)
+// are as close as that sum. A result that is rounded to bf16 does not show the drift.
+template <int P, int PLANES>
+constexpr int kChain = PLANES > 1 ? 2 : P == kDHidden || P == kDWeight ? INT_MAX : 8;
 
 struct GemmArgs {
   CUtensorMap a;
@@ -196,33 +212,42 @@ __device__ void multiply(const GemmArgs& p, int live, uint32_t ring, uint32_t fu
   uint32_t phase = 0;
   const int items = item_count<P>(p, live);
   bool ok = true;
-  for (int i = blockIdx.x; ok && i < items; i += gridDim.x, ++n) {
+  for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
     const Item t = item_at<P>(p, live, i);
-    const int half = n & 1;
-    if (!(ok = bar_wait(acc_empty + 8 * half, ((n >> 1) & 1) ^ 1, gave_up))) break;
-    tc_fence_after();
-    const uint32_t acc = tmem + half * kBN;
-    bool started = false;
+    int in_chain = 0;
+    auto open = [&] {
+      const bool free = bar_wait(acc_empty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, gave_up);
+      tc_fence_after();
+      return free;
+    };
+    if (!(ok = open())) break;
     ok = for_steps<P>(p, t, [&](int, int, int) {
+      if (in_chain == kChain<P, PLANES>) {
+        tc_commit(acc_full + 8 * (n & 1));
+        ++n;
+        in_chain = 0;
+        if (!open()) return false;
+      }
+      const uint32_t acc = tmem + (n & 1) * kBN;
       for (int pair = 0; pair < kPairs<PLANES>; ++pair) {
         if (!bar_wait(full + 8 * stage, phase, gave_up)) return false;
         tc_fence_after();
         const uint32_t sa = ring + stage * kStageBytes;
         const uint64_t da = operand_desc(sa, kAOuter), db = operand_desc(sa + kABytes, kBOuter);
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k) {
-          tc_product(acc, da + k * operand_step(kAOuter), db + k * operand_step(kBOuter), kDesc, started);
-          started = true;
-        }
+        for (int k = 0; k < kBK / 16; ++k)
+          tc_product(acc, da + k * operand_step(kAOuter), db + k * operand_step(kBOuter), kDesc,
+                     in_chain > 0 || pair > 0 || k > 0);
         tc_commit(empty + 8 * stage);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
         }
       }
+      ++in_chain;
       return true;
     });
-    if (ok) tc_commit(acc_full + 8 * half);
+    if (ok) tc_commit(acc_full + 8 * (n++ & 1));
   }
   // giving up: products still running write the tensor memory that is about to be freed
   if (!ok) {
@@ -233,40 +258,29 @@ __device__ void multiply(const GemmArgs& p, int live, uint32_t ring, uint32_t fu
   }
 }
 
-// Splits v into PLANES bf16 parts; returns part `part` of each of two values, packed.
-__device__ __forceinline__ uint32_t part_pair(float a, float b, int part) {
-  uint32_t r = bf16x2_rn(a, b);
-  for (int i = 0; i < part; ++i) {
-    a = __fsub_rn(a, __uint_as_float(r << 16));
-    b = __fsub_rn(b, __uint_as_float(r & 0xffff0000u));
-    r = bf16x2_rn(a, b);
-  }
+// Two values rounded to bf16, packed; they keep what the rounding left.
+__device__ __forceinline__ uint32_t take_part(float& a, float& b) {
+  const uint32_t r = bf16x2_rn(a, b);
+  a = __fsub_rn(a, __uint_as_float(r << 16));
+  b = __fsub_rn(b, __uint_as_float(r & 0xffff0000u));
   return r;
 }
 
-// Stores 32 rows x 64 columns of bf16 through a warp's two staging buffers.
+// Stores 32 rows x 64 columns of 16-bit values through a warp's staging buffer.
 struct Stager {
-  uint32_t base;
-  int n = 0;
-  // the buffer may still be read by the store before last
-  __device__ __forceinline__ uint32_t open() {
-    if (threadIdx.x % 32 == 0) store_wait_read<1>();
+  uint32_t buf;
+  // the store before may still be reading the buffer
+  __device__ __forceinline__ void open() {
+    if (threadIdx.x % 32 == 0) store_wait_read<0>();
     __syncwarp();
-    return base + (n++ & 1) * kOutWarpBytes;
   }
-  // 32 of the row's 64 columns (half 0 or 1)
-  static __device__ __forceinline__ void put(uint32_t buf, int half, const float (&v)[32], int part) {
+  // eight of the row's columns (group 0..7)
+  __device__ __forceinline__ void put(int group, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     const int row = threadIdx.x % 32;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t at = buf + row * 128 + (((half * 4 + j) ^ (row & 7)) << 4);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(part_pair(v[8 * j], v[8 * j + 1], part)),
-                   "r"(part_pair(v[8 * j + 2], v[8 * j + 3], part)), "r"(part_pair(v[8 * j + 4], v[8 * j + 5], part)),
-                   "r"(part_pair(v[8 * j + 6], v[8 * j + 7], part))
-                   : "memory");
-    }
+    const uint32_t at = buf + row * 128 + ((group ^ (row & 7)) << 4);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
   }
-  __device__ __forceinline__ void close(uint32_t buf, const CUtensorMap* map, int x, int y) {
+  __device__ __forceinline__ void close(const CUtensorMap* map, int x, int y) {
     fence_async_smem();
     __syncwarp();
     if (threadIdx.x % 32 == 0) {
@@ -275,6 +289,23 @@ struct Stager {
     }
   }
 };
+
+// The thread's 128 values rounded to bf16, stored 64 columns at a time; v keeps the rest.
+__device__ __forceinline__ void store_part(Stager& out, float (&v)[kMine], const CUtensorMap* map,
+                                           int x, int y, int columns) {
+#pragma unroll
+  for (int c = 0; c < kMine; c += 64) {
+    if (c >= columns) break;
+    out.open();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = c + 8 * j;
+      out.put(j, take_part(v[i], v[i + 1]), take_part(v[i + 2], v[i + 3]), take_part(v[i + 4], v[i + 5]),
+              take_part(v[i + 6], v[i + 7]));
+    }
+    out.close(map, x + c, y);
+  }
+}
 
 // The entries of one row, walked in ascending column order.
 struct Entries {
@@ -300,172 +331,158 @@ struct Entries {
   __device__ __forceinline__ void step() { next = ++at < n ? col[at] : INT_MAX; }
 };
 
+// Steps of 2^-10 below the maximum, in log2 units, as the low 16 bits of the result's bits:
+// kCodeZero (2^-64 of the maximum and less) stands for 0.
+__device__ __forceinline__ uint32_t code_bits(float log2_below) {
+  return __float_as_uint(fminf(fmaf(log2_below, -kCodeSteps, 8388608.0f), 8388608.0f + kCodeZero));
+}
+
+// v: the thread's row of the accumulator, columns [part * 128, part * 128 + 128) of the tile.
 template <int P, int PLANES>
-__device__ __forceinline__ void finish_logits(const GemmArgs& p, const Item& t, int live, uint32_t acc,
-                                              int quarter, Stager& out) {
-  const int lane = threadIdx.x % 32, row = t.row0 + quarter * 32 + lane;
-  const int first = t.tile * kHeadTile;                       // padded column of the tile
-  const int valid = min(kHeadTile, p.g.rows[t.shard] - t.v0);
+__device__ __forceinline__ void finish_logits(const GemmArgs& p, const Item& t, int live, float (&v)[kMine],
+                                              int quarter, int part, const Entries& seeked, Stager& out) {
+  const int row = t.row0 + quarter * 32 + threadIdx.x % 32;
+  const int first = t.tile * kHeadTile + part * kMine;        // padded column of v[0]
+  const int valid = p.g.rows[t.shard] - t.v0 - part * kMine;  // columns with a weight row; may be <= 0
   const float scale = p.g.inv_tau * kLog2e;
-  Entries e;
-  e.seek(p.w, p.g, row, live, first);
-  float v[32];
-  float top = -INFINITY, sum = 0.0f;
-  if (P == kStatsKeep) {
-    // the exponentials are kept relative to the tile's maximum, which must be known first
-    for (int c = 0; c < valid; c += 32) {
-      tmem_load32(acc + c, v);
+  const int x = t.col0 + part * kMine, y = t.row0 + quarter * 32;
+  Entries e = seeked;
+  if (P != kGradient) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (c + j < valid) top = fmaxf(top, v[j]);
-    }
-  }
-  const float lse = P == kGradient && row < live ? p.w.lse[row] : 0.0f;
-  const float weight = P == kGradient && row < live ? p.w.wrow[row] : 0.0f;
-  uint32_t buf = 0;
-  for (int c = 0; c < kHeadTile; c += 32) {
-    if (P == kStats && c >= valid) break;
-    tmem_load32(acc + c, v);
-    if (P != kGradient && e.next < first + c + 32) {
+    for (int c = 0; c < kMine; c += 32) {
+      if (e.next >= first + c + 32) continue;
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         while (e.next == first + c + j) {
-          e.z[e.at] = v[j] * p.g.inv_tau;
+          e.z[e.at] = v[c + j] * p.g.inv_tau;
           e.step();
         }
     }
-    if (P == kStats) {
-      float m = top;
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (valid < kMine) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (c + j >= valid) v[j] = -INFINITY;
-        m = fmaxf(m, v[j]);
-      }
-      // a row of nothing but -inf so far: exponentials relative to 0 are 0, not NaN
-      const float ref = m > -INFINITY ? m * scale : 0.0f;
-      sum = top > -INFINITY || sum != sum ? sum * exp2_approx(fmaf(top, scale, -ref)) : 0.0f;
-      top = m;
-      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int j = 0; j < 32; ++j) part[j & 3] += exp2_approx(fmaf(v[j], scale, -ref));
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
-      continue;
+      for (int j = 0; j < kMine; ++j)
+        if (j >= valid) v[j] = -INFINITY;
     }
-    if (P == kStatsKeep) {
-      const float ref = top > -INFINITY ? top * scale : 0.0f;
-      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        v[j] = c + j < valid ? exp2_approx(fmaf(v[j], scale, -ref)) : 0.0f;
-        part[j & 3] += v[j];
+    for (int j = 0; j < kMine; ++j) m[j & 3] = fmaxf(m[j & 3], v[j]);
+    const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    // a row of nothing but -inf: exponentials relative to 0 are 0, not NaN
+    const float ref = top > -INFINITY ? top * scale : 0.0f;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (P == kStatsKeep && PLANES == 1) {
+#pragma unroll
+      for (int c = 0; c < kMine; c += 64) {
+        out.open();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t code[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = c + 8 * j + 2 * i;
+            const float a = fmaf(v[at], scale, -ref), b = fmaf(v[at + 1], scale, -ref);
+            sum[i] += exp2_approx(a) + exp2_approx(b);
+            code[i] = __byte_perm(code_bits(a), code_bits(b), 0x5410);
+          }
+          out.put(j, code[0], code[1], code[2], code[3]);
+        }
+        out.close(&p.c[0], x + c, y);
       }
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        v[j] = c + j < valid && row < live ? weight * exp2_approx(fmaf(v[j], scale, -lse)) : 0.0f;
-      if (e.next < first + c + 32) {
+      for (int j = 0; j < kMine; ++j) {
+        v[j] = exp2_approx(fmaf(v[j], scale, -ref));
+        sum[j & 3] += v[j];
+      }
+      if (P == kStatsKeep) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          while (e.next == first + c + j) {
-            v[j] = fmaf(-weight, e.q[e.at], v[j]);
-            e.step();
-          }
+        for (int i = 0; i < PLANES; ++i) store_part(out, v, &p.c[0], x, i * p.g.mpad + y, kMine);
       }
     }
-    // the warp's 32 rows, 64 columns to a store
-    if (c % 64 == 0) buf = out.open();
-    Stager::put(buf, c / 32 & 1, v, 0);
-    if (c % 64 == 32) out.close(buf, &p.c[0], t.col0 + c - 32, t.row0 + quarter * 32);
-    if (PLANES > 1) {
-      // the other parts of these 32 columns, straight to memory
-      const int64_t at = (int64_t)row * p.w.grad_ld + t.col0 + c;
-#pragma unroll
-      for (int part = 1; part < PLANES; ++part) {
-        uint4* to = reinterpret_cast<uint4*>(p.w.grad + part * (int64_t)p.g.mpad * p.w.grad_ld + at);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          to[j] = make_uint4(part_pair(v[8 * j], v[8 * j + 1], part), part_pair(v[8 * j + 2], v[8 * j + 3], part),
-                             part_pair(v[8 * j + 4], v[8 * j + 5], part), part_pair(v[8 * j + 6], v[8 * j + 7], part));
-      }
-    }
+    p.w.part[(int64_t)(t.tile * 2 + part) * p.g.mpad + row] =
+        make_float2(top > -INFINITY ? ref : -INFINITY, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    return;
   }
-  if (P != kGradient)
-    p.w.part[(int64_t)t.tile * p.g.mpad + row] = make_float2(top > -INFINITY ? top * scale : -INFINITY, sum);
+  const float lse = row < live ? p.w.lse[row] : 0.0f, weight = row < live ? p.w.wrow[row] : 0.0f;
+#pragma unroll
+  for (int j = 0; j < kMine; ++j)
+    v[j] = j < valid && row < live ? weight * exp2_approx(fmaf(v[j], scale, -lse)) : 0.0f;
+#pragma unroll
+  for (int c = 0; c < kMine; c += 32) {
+    if (e.next >= first + c + 32) continue;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      while (e.next == first + c + j) {
+        v[c + j] = fmaf(-weight, e.q[e.at], v[c + j]);
+        e.step();
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < PLANES; ++i) store_part(out, v, &p.c[0], x, i * p.g.mpad + y, kMine);
 }
 
-__device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t, int live, uint32_t acc, int quarter) {
-  const int row = t.row0 + quarter * 32 + threadIdx.x % 32;
-  float* to = p.w.dh + ((int64_t)t.split * p.g.mpad + row) * p.g.dim + t.col0;
-  const int valid = min(kBN, p.g.dim - t.col0);
-  const bool vec = p.g.dim % 4 == 0;
-  float v[32];
-  for (int c = 0; c < valid; c += 32) {
-    tmem_load32(acc + c, v);
-    if (t.k_lo >= t.k_hi)  // a cut without columns: nothing was multiplied
+__device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t, int live, float (&v)[kMine],
+                                               int quarter, int part) {
+  const int row = t.row0 + quarter * 32 + threadIdx.x % 32, d0 = t.col0 + part * kMine;
+  if (row >= live) return;
+  float* to = p.w.dh + ((int64_t)t.split * p.g.mpad + row) * p.g.dim + d0;
+  const int valid = p.g.dim - d0;
+  const bool none = t.k_lo >= t.k_hi;  // a cut without columns: nothing was multiplied
+  if (p.g.dim % 4 == 0) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-    if (row >= live) continue;
-    if (vec) {
-#pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        if (c + j >= valid) break;
-        float4* at = reinterpret_cast<float4*>(to + c + j);
-        float4 o = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-        if (!p.first) {
-          const float4 b = *at;
-          o = make_float4(b.x + o.x, b.y + o.y, b.z + o.z, b.w + o.w);
-        }
-        *at = o;
+    for (int j = 0; j < kMine; j += 4) {
+      if (j >= valid) break;
+      float4* at = reinterpret_cast<float4*>(to + j);
+      float4 o = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      if (!p.first) {
+        const float4 b = *at;
+        o = make_float4(b.x + o.x, b.y + o.y, b.z + o.z, b.w + o.w);
       }
-    } else {
+      *at = o;
+    }
+  } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (c + j < valid) to[c + j] = p.first ? v[j] : to[c + j] + v[j];
+    for (int j = 0; j < kMine; ++j) {
+      const float o = none ? 0.0f : v[j];
+      if (j < valid) to[j] = p.first ? o : to[j] + o;
     }
   }
 }
 
 template <int PLANES>
-__device__ __forceinline__ void finish_dweight(const GemmArgs& p, const Item& t, uint32_t acc, int quarter, Stager& out) {
-  const int r0 = t.v0 + quarter * 32, row = r0 + threadIdx.x % 32;
-  const int rows = p.g.rows[t.shard], valid = min(kBN, p.g.dim - t.col0);
-  if (r0 >= rows) return;
-  float v[32];
-  for (int c = 0; c < valid; c += 64) {
-    uint32_t buf = 0;
-    if (PLANES == 1 && p.out_map) buf = out.open();
+__device__ __forceinline__ void finish_dweight(const GemmArgs& p, const Item& t, float (&v)[kMine], int quarter,
+                                               int part, Stager& out) {
+  const int r0 = t.v0 + quarter * 32, row = r0 + threadIdx.x % 32, d0 = t.col0 + part * kMine;
+  const int rows = p.g.rows[t.shard], valid = p.g.dim - d0;
+  if (r0 >= rows || valid <= 0) return;
+  if (t.k_hi == 0) {  // no live row: nothing was multiplied
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      tmem_load32(acc + c + 32 * h, v);
-      if (t.k_hi == 0)  // no live row: nothing was multiplied
+    for (int j = 0; j < kMine; ++j) v[j] = 0.0f;
+  }
+  if (PLANES == 1 && p.out_map) {
+    store_part(out, v, &p.c[t.shard], d0, r0, valid);
+    return;
+  }
+  if (row >= rows) return;
+  const int64_t at = (int64_t)row * p.sh.dw_ld + d0;
+  if (PLANES == 1) {
+    uint16_t* to = static_cast<uint16_t*>(p.sh.dw[t.shard]) + at;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-      if (PLANES == 1 && p.out_map) {
-        Stager::put(buf, h, v, 0);
-        continue;
-      }
-      if (row >= rows) continue;
-      const int64_t at = (int64_t)row * p.sh.dw_ld + t.col0 + c + 32 * h;
-      if (PLANES == 1) {
-        uint16_t* to = static_cast<uint16_t*>(p.sh.dw[t.shard]) + at;
+    for (int j = 0; j < kMine; ++j)
+      if (j < valid) to[j] = (uint16_t)(bf16x2_rn(v[j], 0.0f) & 0xffffu);
+  } else {
+    float* to = static_cast<float*>(p.sh.dw[t.shard]) + at;
+    const bool vec = p.out_map != 0;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (c + 32 * h + j < valid) to[j] = (uint16_t)(bf16x2_rn(v[j], 0.0f) & 0xffffu);
+    for (int j = 0; j < kMine; j += 4) {
+      if (vec && j + 4 <= valid) {
+        *reinterpret_cast<float4*>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
       } else {
-        float* to = static_cast<float*>(p.sh.dw[t.shard]) + at;
-        if (p.out_map && c + 32 * h + 32 <= valid) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c + 32 * h + j < valid) to[j] = v[j];
-        }
+        for (int i = 0; i < 4; ++i)
+          if (j + i < valid) to[j + i] = v[j + i];
       }
     }
-    if (PLANES == 1 && p.out_map) out.close(buf, &p.c[t.shard], t.col0 + c, r0);
   }
 }
 
@@ -488,7 +505,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(acc_full + 8 * i, 1);
-      bar_init(acc_empty + 8 * i, 4);
+      bar_init(acc_empty + 8 * i, kFinishWarps);
     }
     bar_init(drain, 1);
     s_gave_up = 0;
@@ -500,27 +517,59 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  if (warp == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeedRegs));
     if (threadIdx.x == 0) produce<P, PLANES>(p, live, ring, full, empty, &s_gave_up);
-  } else if (warp == 1) {
     if (threadIdx.x == 32)
       multiply<P, PLANES>(p, live, ring, full, empty, acc_full, acc_empty, drain, tmem, &s_gave_up);
   } else {
-    const int quarter = warp % 4;
-    Stager out{staging + quarter * 2 * kOutWarpBytes};
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFinishRegs));
+    // warps 4 to 7 finish a tile's first 128 columns, 8 to 11 its last; a warp reads the quarter of
+    // tensor memory's lanes that its number gives it
+    const int quarter = warp % 4, part = warp / 4 - 1;
+    Stager out{staging + (warp - 4) * kOutWarpBytes};
     int n = 0;
-    for (int i = blockIdx.x; i < items; i += gridDim.x, ++n) {
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
       const Item t = item_at<P>(p, live, i);
-      const int half = n & 1;
-      if (!__all_sync(~0u, bar_wait(acc_full + 8 * half, (n >> 1) & 1, &s_gave_up))) break;
-      tc_fence_after();
-      const uint32_t acc = tmem + half * kBN + ((uint32_t)(quarter * 32) << 16);
-      if (P == kDHidden) finish_dhidden(p, t, live, acc, quarter);
-      else if (P == kDWeight) finish_dweight<PLANES>(p, t, acc, quarter, out);
-      else finish_logits<P, PLANES>(p, t, live, acc, quarter, out);
-      tc_fence_before();
-      __syncwarp();
-      if (threadIdx.x % 32 == 0) bar_arrive(acc_empty + 8 * half);
+      Entries e;
+      if (P <= kGradient)  // under the products
+        e.seek(p.w, p.g, t.row0 + quarter * 32 + threadIdx.x % 32, live, t.tile * kHeadTile + part * kMine);
+      int chains = 1;
+      if (kChain<P, PLANES> != INT_MAX) {
+        int steps = 0;
+        for_steps<P>(p, t, [&](int, int, int) {
+          ++steps;
+          return true;
+        });
+        chains = max(1, (steps + kChain<P, PLANES> - 1) / kChain<P, PLANES>);
+      }
+      float v[kMine];
+      for (int c = 0; c < chains; ++c, ++n) {
+        const int half = n & 1;
+        if (!(ok = __all_sync(~0u, bar_wait(acc_full + 8 * half, (n >> 1) & 1, &s_gave_up)))) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + half * kBN + part * kMine + ((uint32_t)(quarter * 32) << 16);
+        if (kChain<P, PLANES> == INT_MAX || c == 0) {
+#pragma unroll
+          for (int j = 0; j < kMine; j += 16) tmem_load16(acc + j, v + j);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kMine; j += 16) {
+            float u[16];
+            tmem_load16(acc + j, u);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[j + k] = __fadd_rn(v[j + k], u[k]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) bar_arrive(acc_empty + 8 * half);
+      }
+      if (!ok) break;
+      if constexpr (P == kDHidden) finish_dhidden(p, t, live, v, quarter, part);
+      else if constexpr (P == kDWeight) finish_dweight<PLANES>(p, t, v, quarter, part, out);
+      else finish_logits<P, PLANES>(p, t, live, v, quarter, part, e, out);
     }
     if (threadIdx.x % 32 == 0) store_wait_all();
   }
@@ -607,6 +656,10 @@ cudaError_t launch(const GemmArgs& a, int64_t items, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (ready_device != dev) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, head_product_kernel<P, PLANES>);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;  // the split would wait forever
     e = cudaFuncSetAttribute(head_product_kernel<P, PLANES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     ready_device = dev;

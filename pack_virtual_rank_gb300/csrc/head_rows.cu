@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
     combine_kernel(const HeadGeom g, const HeadWork w, float* loss) {
   __shared__ float s_max[kCombineWarps][32], s_sum[kCombineWarps][32];
   const int live = *w.n_live, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int row = blockIdx.x * 32 + lane, tiles = g.tile0[RELAY_HEAD_MAX_SHARDS];
+  const int row = blockIdx.x * 32 + lane, tiles = g.tile0[RELAY_HEAD_MAX_SHARDS] * (kHeadTile / kHeadStatTile);
   if ((int)blockIdx.x * 32 >= live) return;
   float m = -INFINITY, s = 0.0f;
   if (row < live)
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
   }
 }
 
-// Kept exponentials to the gradient of the logits, in place: each is relative to its tile's
-// maximum, so a factor per row and tile makes it a probability times the row's weight. The
+// Kept exponentials to the gradient of the logits, in place: each is relative to the maximum of
+// its columns, so the difference to the row's log-sum-exp makes it a probability. The
 // entries' columns are computed from their fp32 logits instead: p - 1 of a confident row
 // would otherwise be the rounding error of p. A block takes 2048 columns of a row; rows after the
 // live ones, as far as products read them, become 0.
@@ -263,21 +263,30 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
   const bool on = row < live;
   const float lse = on ? w.lse[row] : 0.0f, weight = on ? w.wrow[row] : 0.0f;
   if (col < cols) {
-    const float f = on ? weight * exp2f(w.part[(int64_t)(col / kHeadTile) * g.mpad + row].x - lse) : 0.0f;
+    const float ref = on ? w.part[(int64_t)(col / kHeadStatTile) * g.mpad + row].x - lse : 0.0f;
     uint4 in[PLANES], out[PLANES];
     float v[8];
 #pragma unroll
     for (int i = 0; i < PLANES; ++i) in[i] = *reinterpret_cast<const uint4*>(line + i * plane + col);
-    TBF16::unpack(in[0], v);
-    if (PLANES > 1) {
+    if (PLANES == 1) {
+      const uint32_t word[4] = {in[0].x, in[0].y, in[0].z, in[0].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // the code as a float: 2^23 + code has it in its low bits
+        const uint32_t code = j & 1 ? word[j / 2] >> 16 : word[j / 2] & 0xffffu;
+        const float steps = __fsub_rn(__uint_as_float(0x4b000000u | code), 8388608.0f);
+        const float p = exp2f(fmaf(steps, -1.0f / kCodeSteps, ref));
+        v[j] = on && (steps < kCodeZero || ref != ref) ? weight * p : 0.0f;
+      }
+    } else {
+      const float f = on ? weight * exp2f(ref) : 0.0f;
       float x[8], y[8];
+      TBF16::unpack(in[0], v);
       TBF16::unpack(in[PLANES - 2], x);
       TBF16::unpack(in[PLANES - 1], y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(__fadd_rn(y[j], x[j]), v[j]);
+      for (int j = 0; j < 8; ++j) v[j] = on ? __fadd_rn(__fadd_rn(y[j], x[j]), v[j]) * f : 0.0f;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = on ? v[j] * f : 0.0f;
 #pragma unroll
     for (int i = 0; i < PLANES; ++i) {
       out[i] = TBF16::pack(v);
