@@ -458,11 +458,43 @@ def relay_copy(dst, src, max_ctas: int = 0, stream=None) -> None:
 
 # ------------------------------------------- training objective: losses and router --
 
+# What these calls ask torch for on every call, looked up once: small calls cost more host time
+# than kernel time.
+_torch = None
+_float32 = _int32 = _raw_stream = _device = None
+_code: dict = {}
+
+
+def _bind_torch() -> None:
+    global _torch, _float32, _int32, _raw_stream, _device
+    import torch
+    _torch, _float32, _int32 = torch, torch.float32, torch.int32
+    _code.update({torch.float32: F32, torch.bfloat16: BF16})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _handle(stream) -> int:
+    """The stream's handle; the current stream's for None."""
+    if stream is None and _raw_stream is not None and _device is not None:
+        return _raw_stream(_device())
+    return _stream(stream)
+
+
+def _dtype(x, name: str) -> int:
+    try:
+        return _code[x.dtype]
+    except KeyError:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {x.dtype}") from None
+
+
 def _array(x, name: str, dtype, shape) -> Optional[int]:
     """Address of a contiguous CUDA tensor of the given dtype and shape."""
-    if x.dtype != dtype or tuple(x.shape) != shape:
-        raise ValueError(f"{name} must be {dtype} of shape {shape}, got {x.dtype} of {tuple(x.shape)}")
-    return _ptr(x)
+    if x.dtype is not dtype or x.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {x.dtype} of {tuple(x.shape)}")
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor (device memory)")
+    return x.data_ptr()
 
 
 def _matrix(x, name: str) -> int:
@@ -552,33 +584,36 @@ def relay_linear_xent(head: RelayHead, targets, loss, row_weight=None, workspace
                       stream=None) -> None:
     """Cross entropy of the projection's logits against int32 targets (outside the vocabulary:
     the row is ignored), with the gradients the head asks for (see relay.h)."""
-    import torch
+    if _torch is None:
+        _bind_torch()
     t = (head.tokens,)
-    w = None if row_weight is None else _array(row_weight, "row_weight", torch.float32, t)
     if workspace is None:
         workspace = _own_workspace(lambda: alloc_head_workspace(head, loss.device), stream)
-    _check(lib().relay_linear_xent(ctypes.byref(head), _array(targets, "targets", torch.int32, t), w,
-                                   _array(loss, "loss", torch.float32, t), workspace.data_ptr(),
-                                   workspace.numel(), _stream(stream)))
+    _check(lib().relay_linear_xent(
+        ctypes.byref(head), _array(targets, "targets", _int32, t),
+        None if row_weight is None else _array(row_weight, "row_weight", _float32, t),
+        _array(loss, "loss", _float32, t), workspace.data_ptr(), workspace.numel(), _handle(stream)))
 
 
 def relay_linear_distill(head: RelayHead, teacher_logits, teacher_index, temperature: float, loss,
                          row_weight=None, workspace=None, stream=None) -> None:
     """Distillation from a teacher's top logits [tokens, top] (fp32 or bf16) at the int32 ids
     teacher_index (outside the vocabulary: no entry), with the gradients the head asks for."""
-    import torch
+    if _torch is None:
+        _bind_torch()
     t, top = (head.tokens,), teacher_index.shape[1]
-    w = None if row_weight is None else _array(row_weight, "row_weight", torch.float32, t)
     if workspace is None:
         workspace = _own_workspace(lambda: alloc_head_workspace(head, loss.device, top), stream)
+    code = _dtype(teacher_logits, "teacher_logits")
     _check(lib().relay_linear_distill(
         ctypes.byref(head), _array(teacher_logits, "teacher_logits", teacher_logits.dtype, t + (top,)),
-        dtype_code(teacher_logits.dtype), _array(teacher_index, "teacher_index", torch.int32, t + (top,)),
-        top, temperature, w, _array(loss, "loss", torch.float32, t), workspace.data_ptr(),
-        workspace.numel(), _stream(stream)))
+        code, _array(teacher_index, "teacher_index", _int32, t + (top,)), top, temperature,
+        None if row_weight is None else _array(row_weight, "row_weight", _float32, t),
+        _array(loss, "loss", _float32, t), workspace.data_ptr(), workspace.numel(), _handle(stream)))
 
 
 def alloc_router_workspace(tokens: int, experts: int, device):
+    """Workspace of relay_router_forward."""
     import torch
     n = int(lib().relay_router_workspace_size(tokens, experts))
     if n < 0:
@@ -590,42 +625,44 @@ def relay_router_forward(logits, index, gate, counts, prob_sum, mask=None, norma
                          workspace=None, stream=None) -> None:
     """Top-k experts of each row of logits [tokens, experts] (k = index.shape[1]), their gates, and
     the per-expert counts and probability sums (see relay.h). mask: bool or uint8 per row."""
-    import torch
+    if _torch is None:
+        _bind_torch()
     t, e = logits.shape
     k = index.shape[1]
     if mask is not None:
-        mask = _array(mask, "mask", torch.bool if mask.dtype == torch.bool else torch.uint8, (t,))
+        mask = _array(mask, "mask", _torch.bool if mask.dtype is _torch.bool else _torch.uint8, (t,))
     if workspace is None:
         workspace = _own_workspace(lambda: alloc_router_workspace(t, e, logits.device), stream)
     _check(lib().relay_router_forward(
-        _matrix(logits, "logits"), _row_stride(logits), dtype_code(logits.dtype), t, e, k, int(normalize),
-        mask, _array(index, "index", torch.int32, (t, k)), _array(gate, "gate", torch.float32, (t, k)),
-        _array(counts, "counts", torch.int32, (e,)), _array(prob_sum, "prob_sum", torch.float32, (e,)),
-        workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        _matrix(logits, "logits"), _row_stride(logits), _dtype(logits, "logits"), t, e, k, normalize,
+        mask, _array(index, "index", _int32, (t, k)), _array(gate, "gate", _float32, (t, k)),
+        _array(counts, "counts", _int32, (e,)), _array(prob_sum, "prob_sum", _float32, (e,)),
+        workspace.data_ptr(), workspace.numel(), _handle(stream)))
 
 
 def relay_balance_loss(counts, prob_sum, top: int, coef: float, loss, d_prob, stream=None) -> None:
     """Balance loss of (possibly all-reduced) counts and probability sums, and its derivative by
     one token's probability of each expert."""
-    import torch
-    e = counts.shape[0]
+    if _torch is None:
+        _bind_torch()
+    e = counts.shape
     _check(lib().relay_balance_loss(
-        _array(counts, "counts", torch.int32, (e,)), _array(prob_sum, "prob_sum", torch.float32, (e,)), e,
-        top, coef, _array(loss, "loss", torch.float32, (1,)), _array(d_prob, "d_prob", torch.float32, (e,)),
-        _stream(stream)))
+        _array(counts, "counts", _int32, e), _array(prob_sum, "prob_sum", _float32, e), counts.numel(),
+        top, coef, _array(loss, "loss", _float32, (1,)), _array(d_prob, "d_prob", _float32, e),
+        _handle(stream)))
 
 
 def relay_router_backward(logits, index, d_logits, d_gate=None, d_prob=None, normalize: bool = False,
                           stream=None) -> None:
     """Gradient of the router's logits from the gates' and the probabilities' (see relay.h)."""
-    import torch
+    if _torch is None:
+        _bind_torch()
     t, e = logits.shape
-    k = index.shape[1]
-    if d_logits.dtype != logits.dtype or d_logits.shape != logits.shape:
-        raise ValueError("d_logits must have the logits' dtype and shape")
-    dg = None if d_gate is None else _array(d_gate, "d_gate", torch.float32, (t, k))
-    dp = None if d_prob is None else _array(d_prob, "d_prob", torch.float32, (e,))
+    tk = index.shape
+    if d_logits.dtype is not logits.dtype or d_logits.shape != logits.shape or tk[0] != t:
+        raise ValueError("d_logits must have the logits' dtype and shape, index a row for each of theirs")
     _check(lib().relay_router_backward(
-        _matrix(logits, "logits"), _row_stride(logits), dtype_code(logits.dtype), t, e, k, int(normalize),
-        _array(index, "index", torch.int32, (t, k)), dg, dp, _matrix(d_logits, "d_logits"),
-        _row_stride(d_logits), _stream(stream)))
+        _matrix(logits, "logits"), _row_stride(logits), _dtype(logits, "logits"), t, e, tk[1], normalize,
+        _array(index, "index", _int32, tk), None if d_gate is None else _array(d_gate, "d_gate", _float32, tk),
+        None if d_prob is None else _array(d_prob, "d_prob", _float32, (e,)), _matrix(d_logits, "d_logits"),
+        _row_stride(d_logits), _handle(stream)))

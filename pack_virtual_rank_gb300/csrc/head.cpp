@@ -120,7 +120,10 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
     w.grad_ld = (int64_t)ar.tiles_per_piece * kHeadTile;
     w.grad = reinterpret_cast<uint16_t*>(l.take(per_tile * ar.tiles_per_piece));
     if (dh) {
-      w.splits = head_splits(g, ar.tiles_per_piece);
+      // room for the cuts of a batch that keeps few rows, up to 256 MiB of partial sums
+      const int64_t one = 4ll * g.mpad * g.dim;
+      w.tiles_per_piece = ar.tiles_per_piece;
+      w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(ar.tiles_per_piece, 64), (256ll << 20) / one));
       w.dh = reinterpret_cast<float*>(l.take(4ll * w.splits * g.mpad * g.dim));
     }
   }
@@ -202,9 +205,10 @@ relay_status_t check_buffers(const relay_head_t& h, const HeadGeom& g, int top, 
       return report_error(RELAY_ERR_CUDA, std::string("relay_head: ") + cudaGetErrorString(e_)); \
   } while (0)
 
-relay_status_t run_head(const relay_head_t& h, const HeadGeom& g, int top, const int32_t* entries,
+relay_status_t run_head(const relay_head_t& h, HeadGeom g, int top, const int32_t* entries,
                         const void* teacher, int teacher_dtype, const float* row_weight, float* loss,
                         void* workspace, cudaStream_t stream) {
+  g.sms = sm_count();
   const uintptr_t base = (uintptr_t)up((int64_t)reinterpret_cast<uintptr_t>(workspace), 256);
   const Arrangement ar = arrange(h, g, top, base);
   const HeadWork& w = ar.w;
@@ -217,6 +221,8 @@ relay_status_t run_head(const relay_head_t& h, const HeadGeom& g, int top, const
   }
   sh.w_ld = h.weight_stride;
   sh.dw_ld = h.d_weight_stride;
+  sh.dh = h.d_hidden;
+  sh.dh_ld = h.d_hidden_stride;
   if (g.tokens == 0) {
     if (dw)
       for (int a = 0; a < h.A; ++a)
@@ -238,10 +244,10 @@ relay_status_t run_head(const relay_head_t& h, const HeadGeom& g, int top, const
       RELAY_HEAD_TRY(head_scale(g, w, h.dtype, stream));
     else
       RELAY_HEAD_TRY(head_logits(g, w, sh, h.dtype, t, hi, kHeadGradient, stream));
-    if (dh) RELAY_HEAD_TRY(head_dhidden(g, w, sh, h.dtype, t, hi, t == 0, stream));
+    if (dh) RELAY_HEAD_TRY(head_dhidden(g, w, sh, h.dtype, t, hi, t == 0, ar.keep, stream));
     if (dw) RELAY_HEAD_TRY(head_dweight(g, w, sh, h.dtype, t, hi, stream));
   }
-  if (dh) RELAY_HEAD_TRY(head_write_dh(g, w, h.dtype, h.d_hidden, h.d_hidden_stride, stream));
+  if (dh) RELAY_HEAD_TRY(head_write_dh(g, w, h.dtype, ar.keep, h.d_hidden, h.d_hidden_stride, stream));
   return RELAY_OK;
 }
 

@@ -40,6 +40,7 @@ struct HeadGeom {
   int32_t base[RELAY_HEAD_MAX_SHARDS];      // first vocabulary id of each shard
   int32_t vocab;
   int32_t mpad;                             // tokens rounded up to kHeadRowTile
+  int32_t sms;
   float tau, inv_tau;
 };
 
@@ -60,6 +61,14 @@ int head_shard_of_tile(const HeadGeom& g, int tile) {
 constexpr int kHeadPlanesF32 = 3;
 inline int head_planes(int dtype) { return dtype == RELAY_F32 ? kHeadPlanesF32 : 1; }
 
+#ifdef __CUDACC__
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+#endif
+
 // Everything a call works with on the device.
 struct HeadWork {
   int32_t* n_live;    // [1]
@@ -77,13 +86,45 @@ struct HeadWork {
   uint16_t* grad;     // [planes][mpad][grad_ld] of one piece: codes or exponentials, then the gradient
   int64_t grad_ld;    // columns per row
   float* dh;          // [splits][mpad][dim] fp32 partial sums of d_hidden
-  int32_t splits;
+  int32_t splits;     // most cuts of the vocabulary d_hidden may take
+  int32_t tiles_per_piece;
 };
+
+// Cuts of the vocabulary for d_hidden, whose tiles alone are too few, or too few in the last
+// round, to fill the GPU. Costs are in inner steps of one tile (64 columns, about 0.27 us): the
+// rounds of the GPU's SMs times the steps of a cut, plus writing and reading a cut's fp32 partial
+// sums (8 bytes a value; a step's time moves about 1.8 MB). The live rows are known on
+// the device only, so kernels call this themselves and agree.
+#ifdef __CUDACC__
+__device__ __forceinline__ int head_cuts(const HeadGeom& g, int live, int tiles, int most) {
+  // whole warps call it: a lane prices two numbers of cuts (most is at most 64)
+  const int64_t items = (int64_t)((live + kHeadRowTile - 1) / kHeadRowTile) * ((g.dim + kHeadTile - 1) / kHeadTile);
+  if (most == 1 || items >= 4 * g.sms) return 1;
+  const int64_t move = 1 + (int64_t)live * g.dim / 225000;
+  uint32_t least = ~0u;
+  int best = 1;
+  for (int i = 0; i < 2; ++i) {
+    const int s = 1 + threadIdx.x % 32 + 32 * i;
+    if (s > most) continue;
+    const uint32_t rounds = ((uint32_t)items * s + g.sms - 1) / g.sms;
+    const int64_t cost = (int64_t)rounds * (((uint32_t)tiles * 4 + s - 1) / s + 8) + (s > 1 ? s * move : 0);
+    const uint32_t c = cost < 0xfffffffell ? (uint32_t)cost : 0xfffffffeu;
+    if (c < least) {
+      least = c;
+      best = s;
+    }
+  }
+  const uint32_t all = __reduce_min_sync(~0u, least);
+  return (int)__reduce_min_sync(~0u, least == all ? (uint32_t)best : ~0u);
+}
+#endif
 
 struct HeadShards {
   const void* w[RELAY_HEAD_MAX_SHARDS];
   void* dw[RELAY_HEAD_MAX_SHARDS];
   int64_t w_ld, dw_ld;
+  void* dh;  // d_hidden, for a product that writes it itself
+  int64_t dh_ld;
 };
 
 // head_rows.cu
@@ -98,7 +139,7 @@ cudaError_t head_pack_weight(const HeadGeom& g, const HeadWork& w, const HeadSha
 cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, float* loss,
                          cudaStream_t s);
 cudaError_t head_scale(const HeadGeom& g, const HeadWork& w, int dtype, cudaStream_t s);
-cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, void* d_hidden,
+cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, bool whole, void* d_hidden,
                           int64_t d_hidden_ld, cudaStream_t s);
 
 // head_gemm.cu
@@ -106,11 +147,9 @@ enum HeadLogits { kHeadStats, kHeadStatsKeep, kHeadGradient };
 cudaError_t head_logits(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
                         int tile_lo, int tile_hi, HeadLogits mode, cudaStream_t s);
 cudaError_t head_dhidden(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
-                         int tile_lo, int tile_hi, bool first, cudaStream_t s);
+                         int tile_lo, int tile_hi, bool first, bool whole, cudaStream_t s);
 cudaError_t head_dweight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
                          int tile_lo, int tile_hi, cudaStream_t s);
-// Ways to cut the vocabulary for d_hidden so that its tiles fill the GPU.
-int head_splits(const HeadGeom& g, int tiles);
 // Reads and clears the products' fault word.
 cudaError_t head_read_fault(unsigned* fault);
 

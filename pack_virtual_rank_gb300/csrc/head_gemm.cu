@@ -20,6 +20,7 @@
 
 #include "device.cuh"
 #include "head.h"
+#include "launch.cuh"
 #include "program.h"
 #include "tc.cuh"
 
@@ -65,6 +66,8 @@ struct GemmArgs {
   HeadShards sh;
   int32_t tile_lo, tile_hi;
   int32_t first;     // d_hidden: overwrite the partial sums
+  int32_t whole;     // d_hidden: the only piece; an uncut sum goes straight to its row
+  int32_t dh_vec;    // d_hidden's rows take 16-byte stores
   int32_t out_map;   // d_weight: its rows can be stored through tensor maps
   int32_t group;     // logits: row tiles walked together before the next column tile
 };
@@ -77,17 +80,18 @@ struct Item {
   int split;
 };
 
+// cuts: head_cuts (d_hidden).
 template <int P>
-__device__ __forceinline__ int item_count(const GemmArgs& p, int live) {
+__device__ __forceinline__ int item_count(const GemmArgs& p, int live, int cuts) {
   const int mt = (live + kBM - 1) / kBM, tiles = p.tile_hi - p.tile_lo;
   const int nd = (p.g.dim + kBN - 1) / kBN;
-  if (P == kDHidden) return mt * nd * p.w.splits;
+  if (P == kDHidden) return mt * nd * cuts;
   if (P == kDWeight) return tiles * 2 * nd;
   return mt * tiles;
 }
 
 template <int P>
-__device__ __forceinline__ Item item_at(const GemmArgs& p, int live, int i) {
+__device__ __forceinline__ Item item_at(const GemmArgs& p, int live, int cuts, int i) {
   const int mt = (live + kBM - 1) / kBM, tiles = p.tile_hi - p.tile_lo;
   const int nd = (p.g.dim + kBN - 1) / kBN;
   Item t{};
@@ -95,10 +99,10 @@ __device__ __forceinline__ Item item_at(const GemmArgs& p, int live, int i) {
     // every column tile of a row tile runs side by side: the gradient's rows are read once
     t.col0 = i % nd * kBN;
     i /= nd;
-    t.split = i % p.w.splits;
-    t.row0 = i / p.w.splits * kBM;
-    t.k_lo = p.tile_lo + (int)((int64_t)tiles * t.split / p.w.splits);
-    t.k_hi = p.tile_lo + (int)((int64_t)tiles * (t.split + 1) / p.w.splits);
+    t.split = i % cuts;
+    t.row0 = i / cuts * kBM;
+    t.k_lo = p.tile_lo + (int)((int64_t)tiles * t.split / cuts);
+    t.k_hi = p.tile_lo + (int)((int64_t)tiles * (t.split + 1) / cuts);
   } else if (P == kDWeight) {
     t.col0 = i % nd * kBN;
     i /= nd;
@@ -146,15 +150,15 @@ __device__ __forceinline__ int pair_a(int i) { return (0x200110 >> (4 * (5 - i))
 __device__ __forceinline__ int pair_b(int i) { return (0x021010 >> (4 * (5 - i))) & 15; }  // 0 2 1 0 1 0
 
 template <int P, int PLANES>
-__device__ void produce(const GemmArgs& p, int live, uint32_t ring, uint32_t full, uint32_t empty,
+__device__ void produce(const GemmArgs& p, int live, int cuts, uint32_t ring, uint32_t full, uint32_t empty,
                         volatile int* gave_up) {
   int stage = 0;
   uint32_t phase = 0;
   int64_t issued = 0;
-  const int items = item_count<P>(p, live);
+  const int items = item_count<P>(p, live, cuts);
   bool ok = true;
   for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-    const Item t = item_at<P>(p, live, i);
+    const Item t = item_at<P>(p, live, cuts, i);
     ok = for_steps<P>(p, t, [&](int k, int k_shard, int k_v) {
       for (int pair = 0; pair < kPairs<PLANES>; ++pair) {
         const int pa = PLANES == 1 ? 0 : pair_a(pair), pb = PLANES == 1 ? 0 : pair_b(pair);
@@ -203,17 +207,17 @@ __device__ void produce(const GemmArgs& p, int live, uint32_t ring, uint32_t ful
 }
 
 template <int P, int PLANES>
-__device__ void multiply(const GemmArgs& p, int live, uint32_t ring, uint32_t full, uint32_t empty,
+__device__ void multiply(const GemmArgs& p, int live, int cuts, uint32_t ring, uint32_t full, uint32_t empty,
                          uint32_t acc_full, uint32_t acc_empty, uint32_t drain, uint32_t tmem,
                          volatile int* gave_up) {
   constexpr bool kAOuter = P == kDWeight, kBOuter = P == kDWeight || P == kDHidden;
   constexpr uint32_t kDesc = product_desc(kBM, kBN, kAOuter, kBOuter);
   int stage = 0, n = 0;
   uint32_t phase = 0;
-  const int items = item_count<P>(p, live);
+  const int items = item_count<P>(p, live, cuts);
   bool ok = true;
   for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-    const Item t = item_at<P>(p, live, i);
+    const Item t = item_at<P>(p, live, cuts, i);
     int in_chain = 0;
     auto open = [&] {
       const bool free = bar_wait(acc_empty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, gave_up);
@@ -421,19 +425,46 @@ __device__ __forceinline__ void finish_logits(const GemmArgs& p, const Item& t, 
   for (int i = 0; i < PLANES; ++i) store_part(out, v, &p.c[0], x, i * p.g.mpad + y, kMine);
 }
 
-__device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t, int live, float (&v)[kMine],
-                                               int quarter, int part) {
+template <int PLANES>
+__device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t, int live, int cuts,
+                                               float (&v)[kMine], int quarter, int part) {
   const int row = t.row0 + quarter * 32 + threadIdx.x % 32, d0 = t.col0 + part * kMine;
   if (row >= live) return;
-  float* to = p.w.dh + ((int64_t)t.split * p.g.mpad + row) * p.g.dim + d0;
   const int valid = p.g.dim - d0;
-  const bool none = t.k_lo >= t.k_hi;  // a cut without columns: nothing was multiplied
-  if (p.g.dim % 4 == 0) {
+  if (t.k_lo >= t.k_hi) {  // a cut without columns: nothing was multiplied
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) v[j] = 0.0f;
+  }
+  if (p.whole && cuts == 1 && PLANES == 1) {
+    uint16_t* to = static_cast<uint16_t*>(p.sh.dh) + p.w.perm[row] * p.sh.dh_ld + d0;
+#pragma unroll
+    for (int j = 0; j < kMine; j += 8) {
+      if (j >= valid) break;
+      if (p.dh_vec && j + 8 <= valid) {
+        *reinterpret_cast<uint4*>(to + j) = TBF16::pack(v + j);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (j + i < valid) to[j + i] = (uint16_t)(bf16x2_rn(v[j + i], 0.0f) & 0xffffu);
+      }
+    }
+    return;
+  }
+  // an uncut fp32 sum of the only piece is d_hidden's row itself
+  const bool direct = p.whole && cuts == 1;
+  float* to = direct ? static_cast<float*>(p.sh.dh) + p.w.perm[row] * p.sh.dh_ld + d0
+                     : p.w.dh + ((int64_t)t.split * p.g.mpad + row) * p.g.dim + d0;
+  if (direct ? p.dh_vec != 0 : p.g.dim % 4 == 0) {
 #pragma unroll
     for (int j = 0; j < kMine; j += 4) {
-      if (j >= valid) break;
+      if (j + 4 > valid) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // only a row of its own has a ragged end here
+          if (j + i < valid) to[j + i] = v[j + i];
+        continue;
+      }
       float4* at = reinterpret_cast<float4*>(to + j);
-      float4 o = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      float4 o = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
       if (!p.first) {
         const float4 b = *at;
         o = make_float4(b.x + o.x, b.y + o.y, b.z + o.z, b.w + o.w);
@@ -442,10 +473,8 @@ __device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t,
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const float o = none ? 0.0f : v[j];
-      if (j < valid) to[j] = p.first ? o : to[j] + o;
-    }
+    for (int j = 0; j < kMine; ++j)
+      if (j < valid) to[j] = p.first ? v[j] : to[j] + v[j];
   }
 }
 
@@ -492,9 +521,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up;
-  const int live = *p.w.n_live, warp = threadIdx.x / 32;
-  const int items = item_count<P>(p, live);
-  if ((int)blockIdx.x >= items) return;
+  const int warp = threadIdx.x / 32;
+  dep_launch();
   const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u, staging = ring + kStages * kStageBytes;
   const uint32_t full = smem_addr(s_bar), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                  acc_empty = acc_full + 16, drain = acc_empty + 16;
@@ -517,11 +545,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  dep_wait();
+  const int live = *p.w.n_live;
+  const int cuts = P == kDHidden ? head_cuts(p.g, live, p.w.tiles_per_piece, p.w.splits) : 1;
+  const int items = item_count<P>(p, live, cuts);  // a CTA beyond them passes through
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeedRegs));
-    if (threadIdx.x == 0) produce<P, PLANES>(p, live, ring, full, empty, &s_gave_up);
+    if (threadIdx.x == 0) produce<P, PLANES>(p, live, cuts, ring, full, empty, &s_gave_up);
     if (threadIdx.x == 32)
-      multiply<P, PLANES>(p, live, ring, full, empty, acc_full, acc_empty, drain, tmem, &s_gave_up);
+      multiply<P, PLANES>(p, live, cuts, ring, full, empty, acc_full, acc_empty, drain, tmem, &s_gave_up);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFinishRegs));
     // warps 4 to 7 finish a tile's first 128 columns, 8 to 11 its last; a warp reads the quarter of
@@ -531,7 +563,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
     int n = 0;
     bool ok = true;
     for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-      const Item t = item_at<P>(p, live, i);
+      const Item t = item_at<P>(p, live, cuts, i);
       Entries e;
       if (P <= kGradient)  // under the products
         e.seek(p.w, p.g, t.row0 + quarter * 32 + threadIdx.x % 32, live, t.tile * kHeadTile + part * kMine);
@@ -567,7 +599,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
         if (threadIdx.x % 32 == 0) bar_arrive(acc_empty + 8 * half);
       }
       if (!ok) break;
-      if constexpr (P == kDHidden) finish_dhidden(p, t, live, v, quarter, part);
+      if constexpr (P == kDHidden) finish_dhidden<PLANES>(p, t, live, cuts, v, quarter, part);
       else if constexpr (P == kDWeight) finish_dweight<PLANES>(p, t, v, quarter, part, out);
       else finish_logits<P, PLANES>(p, t, live, v, quarter, part, e, out);
     }
@@ -665,13 +697,12 @@ cudaError_t launch(const GemmArgs& a, int64_t items, cudaStream_t s) {
     ready_device = dev;
   }
   const int blocks = (int)std::min<int64_t>(items, sm_count());
-  head_product_kernel<P, PLANES><<<blocks, kGemmThreads, kSmemBytes, s>>>(a);
-  return cudaGetLastError();
+  return launch_chained(head_product_kernel<P, PLANES>, blocks, kGemmThreads, kSmemBytes, s, a);
 }
 
 template <int P>
 cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int lo, int hi, bool first,
-                cudaStream_t s) {
+                bool whole, cudaStream_t s) {
   GemmArgs a{};
   a.g = g;
   a.w = w;
@@ -679,6 +710,8 @@ cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int 
   a.tile_lo = lo;
   a.tile_hi = hi;
   a.first = first;
+  a.whole = whole;
+  a.dh_vec = reinterpret_cast<uintptr_t>(sh.dh) % 16 == 0 && sh.dh_ld * esize_of(dtype) % 16 == 0;
   // row tiles whose packed hidden rows take 64 MiB, half of L2
   const int64_t mt = g.mpad / kBM, tiles = hi - lo, nd = (g.dim + kBN - 1) / kBN;
   a.group = (int)std::max<int64_t>(1, std::min<int64_t>(mt, (64ll << 20) / ((int64_t)kBM * w.dim_pad * 2 * head_planes(dtype))));
@@ -693,27 +726,20 @@ cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int 
 cudaError_t head_logits(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo,
                         int tile_hi, HeadLogits mode, cudaStream_t s) {
   switch (mode) {
-    case kHeadStats: return run<kStats>(g, w, sh, dtype, tile_lo, tile_hi, false, s);
-    case kHeadStatsKeep: return run<kStatsKeep>(g, w, sh, dtype, tile_lo, tile_hi, false, s);
-    default: return run<kGradient>(g, w, sh, dtype, tile_lo, tile_hi, false, s);
+    case kHeadStats: return run<kStats>(g, w, sh, dtype, tile_lo, tile_hi, false, false, s);
+    case kHeadStatsKeep: return run<kStatsKeep>(g, w, sh, dtype, tile_lo, tile_hi, false, false, s);
+    default: return run<kGradient>(g, w, sh, dtype, tile_lo, tile_hi, false, false, s);
   }
 }
 
 cudaError_t head_dhidden(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo,
-                         int tile_hi, bool first, cudaStream_t s) {
-  return run<kDHidden>(g, w, sh, dtype, tile_lo, tile_hi, first, s);
+                         int tile_hi, bool first, bool whole, cudaStream_t s) {
+  return run<kDHidden>(g, w, sh, dtype, tile_lo, tile_hi, first, whole, s);
 }
 
 cudaError_t head_dweight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo,
                          int tile_hi, cudaStream_t s) {
-  return run<kDWeight>(g, w, sh, dtype, tile_lo, tile_hi, false, s);
-}
-
-int head_splits(const HeadGeom& g, int tiles) {
-  const int64_t items = (int64_t)(g.mpad / kBM) * ((g.dim + kBN - 1) / kBN);
-  if (items == 0) return 1;
-  // as many cuts as one round of the GPU's SMs takes, at least one column tile each
-  return (int)std::max<int64_t>(1, std::min<int64_t>(tiles, 152 / items));
+  return run<kDWeight>(g, w, sh, dtype, tile_lo, tile_hi, false, false, s);
 }
 
 cudaError_t head_read_fault(unsigned* fault) {

@@ -7,6 +7,7 @@
 
 #include "device.cuh"
 #include "head.h"
+#include "launch.cuh"
 
 namespace relay {
 namespace {
@@ -39,6 +40,16 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// Streaming load of 16 bytes. Not the read-only path: a kernel here may start before the one that
+// writes what it reads has ended.
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
 // The three bf16 parts of an fp32 value. A value that rounds to infinity is cut instead, and an
 // infinity or NaN is its first part alone.
 __device__ __forceinline__ void parts_of(float v, uint16_t (&o)[3]) {
@@ -52,30 +63,59 @@ __device__ __forceinline__ void parts_of(float v, uint16_t (&o)[3]) {
   }
 }
 
-// Copies one row to its packed place: bf16 as it is, fp32 in three parts, `plane` elements apart.
-// Columns from dim to pad, and all of them when from is NULL, are 0.
+// A warp copies one row to its packed place: bf16 as it is, fp32 in three parts, `plane` elements
+// apart. Columns from dim to pad, and all of them when from is NULL, are 0. vec: 16-byte loads.
 __device__ __forceinline__ void pack_row(uint16_t* to, int64_t, const uint16_t* from, int dim, int pad, bool vec) {
-  const int whole_vecs = from != nullptr && vec ? dim / 8 : 0;
-  for (int v = threadIdx.x; v < whole_vecs; v += kThreadsRows)
-    reinterpret_cast<uint4*>(to)[v] = ld_stream_v4(from + v * 8);
-  for (int d = whole_vecs * 8 + threadIdx.x; d < pad; d += kThreadsRows)
-    to[d] = from != nullptr && d < dim ? from[d] : (uint16_t)0;
-}
-__device__ __forceinline__ void pack_row(uint16_t* to, int64_t plane, const float* from, int dim, int pad, bool) {
-  for (int d = threadIdx.x; d < pad; d += kThreadsRows) {
-    uint16_t o[3] = {0, 0, 0};
-    if (from != nullptr && d < dim) parts_of(from[d], o);
+  const int lane = threadIdx.x % 32;
+  const int vecs = from == nullptr ? pad / 8 : vec ? dim / 8 : 0;
+  for (int v0 = lane; v0 < vecs; v0 += 4 * 32) {
+    uint4 x[4];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) to[i * plane + d] = o[i];
+    for (int i = 0; i < 4; ++i)
+      x[i] = from != nullptr && v0 + 32 * i < vecs ? ld_once(from + (v0 + 32 * i) * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (v0 + 32 * i < vecs) reinterpret_cast<uint4*>(to)[v0 + 32 * i] = x[i];
+  }
+  for (int d = vecs * 8 + lane; d < pad; d += 32) to[d] = d < dim ? from[d] : (uint16_t)0;
+}
+__device__ __forceinline__ void pack_row(uint16_t* to, int64_t plane, const float* from, int dim, int pad, bool vec) {
+  const int lane = threadIdx.x % 32;
+  for (int d0 = lane * 8; d0 < pad; d0 += 8 * 32) {  // pad is a multiple of 8
+    float x[8];
+    if (from != nullptr && vec && d0 + 8 <= dim) {
+      TF32::unpack(ld_once(from + d0), x);
+      TF32::unpack(ld_once(from + d0 + 4), x + 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = from != nullptr && d0 + i < dim ? from[d0 + i] : 0.0f;
+    }
+    uint16_t o[8][3];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) parts_of(x[i], o[i]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      *reinterpret_cast<uint4*>(to + k * plane + d0) =
+          make_uint4(o[0][k] | (uint32_t)o[1][k] << 16, o[2][k] | (uint32_t)o[3][k] << 16,
+                     o[4][k] | (uint32_t)o[5][k] << 16, o[6][k] | (uint32_t)o[7][k] << 16);
   }
 }
-
-// The padded weight: one block per padded row.
 template <class T>
-__global__ void __launch_bounds__(kThreadsRows) pack_weight_kernel(const HeadGeom g, const HeadWork w, const HeadShards sh) {
-  const int row = blockIdx.x, a = head_shard_of_tile(g, row / kHeadTile), v = row - g.tile0[a] * kHeadTile;
+__device__ __forceinline__ void zero_row(T* to, int n) {
+  for (int d = threadIdx.x % 32; d < n; d += 32) store_from_f32(to + d, 0.0f);
+}
+
+// The padded weight: one warp per padded row.
+template <class T>
+__global__ void __launch_bounds__(kThreadsRows)
+    pack_weight_kernel(const HeadGeom g, const HeadWork w, const HeadShards sh, int vec) {
+  dep_launch();
+  dep_wait();
+  const int rows = g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
+  const int row = blockIdx.x * (kThreadsRows / 32) + threadIdx.x / 32;  // rows: a multiple of 256
+  const int a = head_shard_of_tile(g, row / kHeadTile), v = row - g.tile0[a] * kHeadTile;
   const T* from = v < g.rows[a] ? static_cast<const T*>(sh.w[a]) + v * sh.w_ld : nullptr;
-  pack_row(w.wpack + (int64_t)row * w.dim_pad, (int64_t)gridDim.x * w.dim_pad, from, g.dim, w.dim_pad, false);
+  pack_row(w.wpack + (int64_t)row * w.dim_pad, (int64_t)rows * w.dim_pad, from, g.dim, w.dim_pad, vec);
 }
 
 // One warp per row: the entries' columns in ascending order (by counting, each lane holds up to
@@ -84,6 +124,8 @@ template <class T>
 __global__ void __launch_bounds__(kThreadsRows) teacher_kernel(const HeadGeom g, const HeadWork w,
                                                                const T* logits, const int32_t* index) {
   constexpr int kPer = RELAY_HEAD_MAX_TOP / 32;
+  dep_launch();
+  dep_wait();
   const int row = blockIdx.x * (kThreadsRows / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
   if (row >= g.tokens) return;
   const int64_t at = (int64_t)row * g.top;
@@ -141,18 +183,22 @@ __device__ __forceinline__ bool row_live(const HeadGeom& g, const HeadWork& w, c
 }
 
 // A block owns `per` consecutive rows. It counts the live rows before them itself (a read of
-// every row's flag, from L2: no second launch, no order between blocks), then copies its live
-// rows to their packed places and zeroes the places its other rows leave free behind the last
-// live row, as far as products read them. Ignored rows get loss 0 and d_hidden 0 here.
+// every row's flag, from L2: no second launch, no order between blocks), then a warp per row
+// copies the live ones to their packed places and zeroes the places the others leave free
+// behind the last live row, as far as products read them. Ignored rows get loss 0 and d_hidden 0.
 template <class T, bool DISTILL>
 __global__ void __launch_bounds__(kThreadsRows)
     pack_kernel(const HeadGeom g, const HeadWork w, const T* hidden, int64_t ld, const int32_t* targets,
                 const float* row_weight, float* loss, T* dh, int64_t dh_ld, int per, int vec) {
-  __shared__ int s_before, s_total;
-  const int lo = blockIdx.x * per, hi = min(lo + per, g.tokens);
+  constexpr int kWarps = kThreadsRows / 32;
+  __shared__ int s_before, s_total, s_warp[kWarps], s_place[kThreadsRows];
+  dep_launch();
+  dep_wait();
+  const int lo = blockIdx.x * per, hi = min(lo + per, g.tokens), lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   if (threadIdx.x == 0) s_before = s_total = 0;
   __syncthreads();
   int before = 0, total = 0;
+#pragma unroll 4
   for (int r = threadIdx.x; r < g.tokens; r += kThreadsRows) {
     const int live = row_live<DISTILL>(g, w, targets, r);
     total += live;
@@ -160,90 +206,123 @@ __global__ void __launch_bounds__(kThreadsRows)
   }
   before = __reduce_add_sync(~0u, before);
   total = __reduce_add_sync(~0u, total);
-  if (threadIdx.x % 32 == 0) {
+  if (lane == 0) {
     atomicAdd(&s_before, before);  // integers: any order gives the same sum
     atomicAdd(&s_total, total);
   }
   __syncthreads();
   total = s_total;
-  int packed = s_before;          // live rows before row r
+  int packed = s_before;  // live rows before row `base`
   const int read_end = (total + kHeadRowTile - 1) / kHeadRowTile * kHeadRowTile;
   if (blockIdx.x == 0 && threadIdx.x == 0) *w.n_live = total;
   const int64_t plane = (int64_t)g.mpad * w.dim_pad;
-  for (int r = lo; r < hi; ++r) {
-    const bool live = row_live<DISTILL>(g, w, targets, r);
-    const int place = live ? packed : total + (r - packed);
-    packed += live;
-    if (threadIdx.x == 0) {
-      w.perm[place] = r;
-      w.wrow[place] = live ? (row_weight ? row_weight[r] : 1.0f) * g.tau : 0.0f;
-      if (!live) loss[r] = 0.0f;
+  for (int base = lo; base < hi; base += kThreadsRows) {
+    const int mine = base + threadIdx.x;
+    const bool live = mine < hi && row_live<DISTILL>(g, w, targets, mine);
+    const unsigned votes = __ballot_sync(~0u, live);
+    if (lane == 0) s_warp[warp] = __popc(votes);
+    __syncthreads();
+    int ahead = packed + __popc(votes & ((1u << lane) - 1));
+    for (int i = 0; i < warp; ++i) ahead += s_warp[i];
+    for (int i = 0; i < kWarps; ++i) packed += s_warp[i];
+    if (mine < hi) {
+      const int place = live ? ahead : total + (mine - ahead);
+      s_place[threadIdx.x] = live ? place : ~place;
+      w.perm[place] = mine;
+      w.wrow[place] = live ? (row_weight ? row_weight[mine] : 1.0f) * g.tau : 0.0f;
+      if (!live) loss[mine] = 0.0f;
       if (!DISTILL && live) {
-        w.ent_col[r] = column_of(g, targets[r]);
-        w.ent_q[r] = 1.0f;
+        w.ent_col[mine] = column_of(g, targets[mine]);
+        w.ent_q[mine] = 1.0f;
       }
     }
-    if (!live && dh != nullptr)
-      for (int d = threadIdx.x; d < g.dim; d += kThreadsRows) store_from_f32(dh + r * dh_ld + d, 0.0f);
-    if (!live && place >= read_end) continue;
-    pack_row(w.hid + (int64_t)place * w.dim_pad, plane, live ? hidden + r * ld : nullptr, g.dim, w.dim_pad, vec);
+    __syncthreads();
+    for (int i = warp; base + i < hi && i < kThreadsRows; i += kWarps) {
+      const int r = base + i, place = s_place[i];
+      if (place >= 0) {
+        pack_row(w.hid + (int64_t)place * w.dim_pad, plane, hidden + r * ld, g.dim, w.dim_pad, vec);
+      } else {
+        if (dh != nullptr) zero_row(dh + r * dh_ld, g.dim);
+        if (~place < read_end)
+          pack_row(w.hid + (int64_t)~place * w.dim_pad, plane, static_cast<const T*>(nullptr), g.dim, w.dim_pad, vec);
+      }
+    }
+    __syncthreads();
   }
-  // places past the last row of the batch
-  if (blockIdx.x == gridDim.x - 1)
-    for (int place = g.tokens; place < g.mpad; ++place) {
-      if (threadIdx.x == 0) {
-        w.perm[place] = 0;
-        w.wrow[place] = 0.0f;
-      }
-      if (place < read_end)
-        pack_row(w.hid + (int64_t)place * w.dim_pad, plane, static_cast<const T*>(nullptr), g.dim, w.dim_pad, false);
+  // places past the last row of the batch: fewer than kHeadRowTile, one per block where there are
+  // enough blocks
+  for (int place = g.tokens + blockIdx.x * kWarps + warp; place < g.mpad; place += gridDim.x * kWarps) {
+    if (lane == 0) {
+      w.perm[place] = 0;
+      w.wrow[place] = 0.0f;
     }
+    if (place < read_end)
+      pack_row(w.hid + (int64_t)place * w.dim_pad, plane, static_cast<const T*>(nullptr), g.dim, w.dim_pad, vec);
+  }
 }
 
-// Joins the tiles' (max, sum) of a row into its log-sum-exp and writes its loss. A block takes
-// 32 rows: lanes are rows (the statistics of a tile are contiguous over rows), warps stride over
-// the tiles and join in shared memory, in a fixed order.
-constexpr int kCombineWarps = 16;
+// Joins the (max, sum) of a row's columns into its log-sum-exp and writes its loss. A block takes
+// 32 rows: lanes are rows (the statistics of the same columns are contiguous over rows), warps
+// stride over the columns and join in shared memory, in a fixed order. Then a warp per row sums
+// its entries.
+constexpr int kCombineWarps = 32;
+__device__ __forceinline__ void join(float& m, float& s, float pm, float ps) {
+  const float top = fmaxf(m, pm);
+  // -inf - -inf: a side that holds nothing yet adds nothing
+  s = (m > -INFINITY || s != s ? s * exp2f(m - top) : 0.0f) + (pm > -INFINITY || ps != ps ? ps * exp2f(pm - top) : 0.0f);
+  m = top;
+}
 template <bool DISTILL>
-__global__ void __launch_bounds__(32 * kCombineWarps)
-    combine_kernel(const HeadGeom g, const HeadWork w, float* loss) {
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const HeadGeom g, const HeadWork w, float* loss) {
   __shared__ float s_max[kCombineWarps][32], s_sum[kCombineWarps][32];
+  dep_launch();
+  dep_wait();
   const int live = *w.n_live, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int row = blockIdx.x * 32 + lane, tiles = g.tile0[RELAY_HEAD_MAX_SHARDS] * (kHeadTile / kHeadStatTile);
+  const int row = blockIdx.x * 32 + lane, parts = g.tile0[RELAY_HEAD_MAX_SHARDS] * (kHeadTile / kHeadStatTile);
   if ((int)blockIdx.x * 32 >= live) return;
   float m = -INFINITY, s = 0.0f;
   if (row < live)
-    for (int t = warp; t < tiles; t += kCombineWarps) {
-      const float2 p = w.part[(int64_t)t * g.mpad + row];
-      const float top = fmaxf(m, p.x);
-      // -inf - -inf: a side that holds nothing yet adds nothing
-      s = (m > -INFINITY || s != s ? s * exp2f(m - top) : 0.0f) + (p.x > -INFINITY || p.y != p.y ? p.y * exp2f(p.x - top) : 0.0f);
-      m = top;
+    for (int t = warp; t < parts; t += 4 * kCombineWarps) {
+      float2 p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        p[i] = t + i * kCombineWarps < parts ? w.part[(int64_t)(t + i * kCombineWarps) * g.mpad + row]
+                                             : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) join(m, s, p[i].x, p[i].y);
     }
   s_max[warp][lane] = m;
   s_sum[warp][lane] = s;
   __syncthreads();
-  if (warp != 0 || row >= live) return;
-  for (int i = 1; i < kCombineWarps; ++i) {
-    const float pm = s_max[i][lane], ps = s_sum[i][lane], top = fmaxf(m, pm);
-    s = (m > -INFINITY || s != s ? s * exp2f(m - top) : 0.0f) + (pm > -INFINITY || ps != ps ? ps * exp2f(pm - top) : 0.0f);
-    m = top;
+  // warp i takes row i: lanes are the warps' shares
+  const int mine = blockIdx.x * 32 + warp;
+  if (mine >= live) return;
+  m = s_max[lane][warp];
+  s = s_sum[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float pm = __shfl_xor_sync(~0u, m, o), ps = __shfl_xor_sync(~0u, s, o);
+    // both sides of a pair join in the same order: the lower lane's share first
+    float am = lane & o ? pm : m, as = lane & o ? ps : s;
+    join(am, as, lane & o ? m : pm, lane & o ? s : ps);
+    m = am;
+    s = as;
   }
   const float lse2 = m + log2f(s), lse = lse2 * 0.6931471805599453f;
-  w.lse[row] = lse2;
-  const int r = w.perm[row];
+  const int r = w.perm[mine];
   const int64_t at = (int64_t)r * g.top;
+  if (lane == 0) w.lse[mine] = lse2;
   if (!DISTILL) {
-    loss[r] = lse - w.ent_z[at];
-  } else {
-    float sum = 0.0f;
-    for (int k = 0; k < g.top; ++k) {
-      const float q = w.ent_q[at + k];
-      if (w.ent_col[at + k] == INT_MAX) break;
-      if (q != 0.0f) sum += q * (logf(q) - (w.ent_z[at + k] - lse));  // 0 log 0 = 0
-    }
-    loss[r] = g.tau * g.tau * sum;
+    if (lane == 0) loss[r] = lse - w.ent_z[at];
+    return;
   }
+  float sum = 0.0f;
+  for (int k = lane; k < g.top; k += 32) {
+    const float q = w.ent_q[at + k];
+    if (w.ent_col[at + k] != INT_MAX && q != 0.0f) sum += q * (logf(q) - (w.ent_z[at + k] - lse));  // 0 log 0 = 0
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) loss[r] = g.tau * g.tau * sum;
 }
 
 // Kept exponentials to the gradient of the logits, in place: each is relative to the maximum of
@@ -251,50 +330,66 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
 // entries' columns are computed from their fp32 logits instead: p - 1 of a confident row
 // would otherwise be the rounding error of p. A block takes 2048 columns of a row; rows after the
 // live ones, as far as products read them, become 0.
-constexpr int kScaleCols = kThreadsRows * 8;
+constexpr int kScaleVecs = 4;  // 16-byte vectors in flight per thread and plane
+constexpr int kScaleCols = kThreadsRows * 8 * kScaleVecs;
 template <int PLANES>
 __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, const HeadWork w) {
+  dep_launch();
+  dep_wait();
   const int live = *w.n_live, row = blockIdx.x;
   if (row >= (live + kHeadRowTile - 1) / kHeadRowTile * kHeadRowTile) return;
-  const int col0 = blockIdx.y * kScaleCols, col = col0 + threadIdx.x * 8;
+  const int col0 = blockIdx.y * kScaleCols;
   const int cols = g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
   const int64_t plane = (int64_t)g.mpad * w.grad_ld;
   uint16_t* line = w.grad + (int64_t)row * w.grad_ld;
   const bool on = row < live;
   const float lse = on ? w.lse[row] : 0.0f, weight = on ? w.wrow[row] : 0.0f;
-  if (col < cols) {
-    const float ref = on ? w.part[(int64_t)(col / kHeadStatTile) * g.mpad + row].x - lse : 0.0f;
-    uint4 in[PLANES], out[PLANES];
-    float v[8];
+  uint4 in[kScaleVecs][PLANES];
+  float ref[kScaleVecs];
 #pragma unroll
-    for (int i = 0; i < PLANES; ++i) in[i] = *reinterpret_cast<const uint4*>(line + i * plane + col);
-    if (PLANES == 1) {
-      const uint32_t word[4] = {in[0].x, in[0].y, in[0].z, in[0].w};
+  for (int k = 0; k < kScaleVecs; ++k) {
+    const int col = col0 + (k * kThreadsRows + threadIdx.x) * 8;
+    if (col >= cols || !on) continue;
+#pragma unroll
+    for (int i = 0; i < PLANES; ++i) in[k][i] = ld_once(line + i * plane + col);
+    ref[k] = w.part[(int64_t)(col / kHeadStatTile) * g.mpad + row].x - lse;
+  }
+#pragma unroll
+  for (int k = 0; k < kScaleVecs; ++k) {
+    const int col = col0 + (k * kThreadsRows + threadIdx.x) * 8;
+    if (col >= cols) continue;
+    float v[8];
+    if (!on) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    } else if (PLANES == 1) {
+      const uint32_t word[4] = {in[k][0].x, in[k][0].y, in[k][0].z, in[k][0].w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // the code as a float: 2^23 + code has it in its low bits
         const uint32_t code = j & 1 ? word[j / 2] >> 16 : word[j / 2] & 0xffffu;
         const float steps = __fsub_rn(__uint_as_float(0x4b000000u | code), 8388608.0f);
-        const float p = exp2f(fmaf(steps, -1.0f / kCodeSteps, ref));
-        v[j] = on && (steps < kCodeZero || ref != ref) ? weight * p : 0.0f;
+        const float p = weight * exp2_approx(fmaf(steps, -1.0f / kCodeSteps, ref[k]));
+        v[j] = steps < kCodeZero || ref[k] != ref[k] ? p : 0.0f;
       }
     } else {
-      const float f = on ? weight * exp2f(ref) : 0.0f;
+      const float f = weight * exp2f(ref[k]);
       float x[8], y[8];
-      TBF16::unpack(in[0], v);
-      TBF16::unpack(in[PLANES - 2], x);
-      TBF16::unpack(in[PLANES - 1], y);
+      TBF16::unpack(in[k][0], v);
+      TBF16::unpack(in[k][PLANES > 1 ? 1 : 0], x);
+      TBF16::unpack(in[k][PLANES > 1 ? 2 : 0], y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = on ? __fadd_rn(__fadd_rn(y[j], x[j]), v[j]) * f : 0.0f;
+      for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(__fadd_rn(y[j], x[j]), v[j]) * f;
     }
 #pragma unroll
     for (int i = 0; i < PLANES; ++i) {
-      out[i] = TBF16::pack(v);
+      const uint4 out = TBF16::pack(v);
+      *reinterpret_cast<uint4*>(line + i * plane + col) = out;
+      if (i + 1 == PLANES) break;
       float r[8];
-      TBF16::unpack(out[i], r);
+      TBF16::unpack(out, r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = __fsub_rn(v[j], r[j]);
-      *reinterpret_cast<uint4*>(line + i * plane + col) = out[i];
     }
   }
   if (!on) return;
@@ -315,22 +410,46 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
   }
 }
 
+// Sums the cuts of d_hidden in order and puts each row where it belongs. Rows whose d_hidden the
+// product wrote itself (one cut, one piece) need nothing.
 template <class T>
 __global__ void __launch_bounds__(kThreadsRows)
-    write_dh_kernel(const HeadGeom g, const HeadWork w, T* dh, int64_t ld) {
-  const int live = *w.n_live;
-  for (int row = blockIdx.x; row < live; row += gridDim.x) {
-    T* to = dh + (int64_t)w.perm[row] * ld;
-    const float* from = w.dh + (int64_t)row * g.dim;
-    for (int d = threadIdx.x; d < g.dim; d += kThreadsRows) {
-      float sum = from[d];
-      for (int i = 1; i < w.splits; ++i) sum += from[(int64_t)i * g.mpad * g.dim + d];
-      store_from_f32(to + d, sum);
+    write_dh_kernel(const HeadGeom g, const HeadWork w, T* dh, int64_t ld, int whole, int vec) {
+  dep_launch();
+  dep_wait();
+  const int live = *w.n_live, cuts = head_cuts(g, live, w.tiles_per_piece, w.splits);
+  if (whole && cuts == 1) return;
+  const int64_t cut = (int64_t)g.mpad * g.dim;
+  constexpr int kLanes = 4;
+  const int64_t vecs = vec ? (int64_t)live * (g.dim / kLanes) : 0;
+  const int64_t first = (int64_t)blockIdx.x * kThreadsRows + threadIdx.x, stride = (int64_t)gridDim.x * kThreadsRows;
+  for (int64_t i = first; i < vecs; i += stride) {
+    const int row = (int)(i / (g.dim / kLanes)), d = (int)(i % (g.dim / kLanes)) * kLanes;
+    const float* from = w.dh + (int64_t)row * g.dim + d;
+    float4 sum = *reinterpret_cast<const float4*>(from);
+#pragma unroll 8
+    for (int c = 1; c < cuts; ++c) {
+      const float4 x = *reinterpret_cast<const float4*>(from + c * cut);
+      sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
     }
+    T* to = dh + (int64_t)w.perm[row] * ld + d;
+    if (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2_rn(sum.x, sum.y), bf16x2_rn(sum.z, sum.w));
+    else
+      *reinterpret_cast<float4*>(to) = sum;
+  }
+  if (vec) return;
+  for (int64_t i = first; i < (int64_t)live * g.dim; i += stride) {
+    const int row = (int)(i / g.dim), d = (int)(i % g.dim);
+    float sum = w.dh[i];
+#pragma unroll 4
+    for (int c = 1; c < cuts; ++c) sum += w.dh[c * cut + i];
+    store_from_f32(dh + (int64_t)w.perm[row] * ld + d, sum);
   }
 }
 
-int ceil_div(int a, int b) { return (a + b - 1) / b; }
+int ceil_div(int a, int b) { return (int)(((int64_t)a + b - 1) / b); }
+int64_t esize(int dtype) { return dtype == RELAY_BF16 ? 2 : 4; }
 
 }  // namespace
 
@@ -338,28 +457,24 @@ cudaError_t head_teacher(const HeadGeom& g, const HeadWork& w, const void* teach
                          const int32_t* index, cudaStream_t s) {
   const int blocks = ceil_div(g.tokens, kThreadsRows / 32);
   if (teacher_dtype == RELAY_BF16)
-    teacher_kernel<<<blocks, kThreadsRows, 0, s>>>(g, w, static_cast<const uint16_t*>(teacher), index);
-  else
-    teacher_kernel<<<blocks, kThreadsRows, 0, s>>>(g, w, static_cast<const float*>(teacher), index);
-  return cudaGetLastError();
+    return launch_chained(teacher_kernel<uint16_t>, blocks, kThreadsRows, 0, s, g, w,
+                          static_cast<const uint16_t*>(teacher), index);
+  return launch_chained(teacher_kernel<float>, blocks, kThreadsRows, 0, s, g, w, static_cast<const float*>(teacher),
+                        index);
 }
 
 template <class T>
 static cudaError_t pack_typed(const HeadGeom& g, const HeadWork& w, bool distill, const void* hidden,
                               int64_t ld, const int32_t* targets, const float* row_weight, float* loss,
                               void* dh, int64_t dh_ld, cudaStream_t s) {
-  // at most 1024 blocks read every row's flag; a few rows each while the batch is small
-  const int per = ceil_div(g.tokens, 1024) > 4 ? ceil_div(g.tokens, 1024) : 4;
+  // a warp per row; at most 2048 blocks read every row's flag
+  constexpr int kWarps = kThreadsRows / 32;
+  const int per = ceil_div(ceil_div(g.tokens, 2048), kWarps) * kWarps;
   const int blocks = ceil_div(g.tokens, per);
   const int vec = reinterpret_cast<uintptr_t>(hidden) % 16 == 0 && ld * sizeof(T) % 16 == 0;
-  const T* from = static_cast<const T*>(hidden);
-  if (distill)
-    pack_kernel<T, true><<<blocks, kThreadsRows, 0, s>>>(g, w, from, ld, targets, row_weight, loss,
-                                                         static_cast<T*>(dh), dh_ld, per, vec);
-  else
-    pack_kernel<T, false><<<blocks, kThreadsRows, 0, s>>>(g, w, from, ld, targets, row_weight, loss,
-                                                          static_cast<T*>(dh), dh_ld, per, vec);
-  return cudaGetLastError();
+  return launch_chained(distill ? pack_kernel<T, true> : pack_kernel<T, false>, blocks, kThreadsRows, 0, s, g, w,
+                        static_cast<const T*>(hidden), ld, targets, row_weight, loss, static_cast<T*>(dh), dh_ld, per,
+                        vec);
 }
 
 cudaError_t head_pack(const HeadGeom& g, const HeadWork& w, int dtype, bool distill, const void* hidden,
@@ -370,42 +485,38 @@ cudaError_t head_pack(const HeadGeom& g, const HeadWork& w, int dtype, bool dist
   return pack_typed<float>(g, w, distill, hidden, hidden_ld, targets, row_weight, loss, d_hidden, d_hidden_ld, s);
 }
 
-cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, float* loss, cudaStream_t s) {
-  const int blocks = ceil_div(g.tokens, 32);
-  if (distill)
-    combine_kernel<true><<<blocks, 32 * kCombineWarps, 0, s>>>(g, w, loss);
-  else
-    combine_kernel<false><<<blocks, 32 * kCombineWarps, 0, s>>>(g, w, loss);
-  return cudaGetLastError();
+cudaError_t head_pack_weight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, cudaStream_t s) {
+  const int blocks = g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile / (kThreadsRows / 32);
+  int vec = sh.w_ld * esize(dtype) % 16 == 0;
+  for (int a = 0; a < g.A; ++a)
+    if (g.rows[a] > 0) vec &= reinterpret_cast<uintptr_t>(sh.w[a]) % 16 == 0;
+  return launch_chained(dtype == RELAY_BF16 ? pack_weight_kernel<uint16_t> : pack_weight_kernel<float>, blocks,
+                        kThreadsRows, 0, s, g, w, sh, vec);
 }
 
-cudaError_t head_pack_weight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, cudaStream_t s) {
-  const int blocks = g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
-  if (dtype == RELAY_BF16)
-    pack_weight_kernel<uint16_t><<<blocks, kThreadsRows, 0, s>>>(g, w, sh);
-  else
-    pack_weight_kernel<float><<<blocks, kThreadsRows, 0, s>>>(g, w, sh);
-  return cudaGetLastError();
+cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, float* loss, cudaStream_t s) {
+  return launch_chained(distill ? combine_kernel<true> : combine_kernel<false>, ceil_div(g.tokens, 32),
+                        32 * kCombineWarps, 0, s, g, w, loss);
 }
 
 cudaError_t head_scale(const HeadGeom& g, const HeadWork& w, int dtype, cudaStream_t s) {
   const int cols = g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
   const dim3 grid(g.mpad, ceil_div(cols, kScaleCols));  // few column blocks: a piece is bounded
-  if (dtype == RELAY_BF16)
-    scale_kernel<1><<<grid, kThreadsRows, 0, s>>>(g, w);
-  else
-    scale_kernel<kHeadPlanesF32><<<grid, kThreadsRows, 0, s>>>(g, w);
-  return cudaGetLastError();
+  return launch_chained(dtype == RELAY_BF16 ? scale_kernel<1> : scale_kernel<kHeadPlanesF32>, grid, kThreadsRows, 0, s,
+                        g, w);
 }
 
-cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, void* d_hidden,
+cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, bool whole, void* d_hidden,
                           int64_t d_hidden_ld, cudaStream_t s) {
-  const int blocks = g.tokens < 4096 ? g.tokens : 4096;
+  const int64_t work = (int64_t)g.tokens * ceil_div(g.dim, 4);
+  const int blocks = (int)(work < 2432ll * kThreadsRows ? (work + kThreadsRows - 1) / kThreadsRows : 2432);  // 16 per SM
+  const int vec = g.dim % 4 == 0 && d_hidden_ld % 4 == 0 &&
+                  reinterpret_cast<uintptr_t>(d_hidden) % (4 * esize(dtype)) == 0;
   if (dtype == RELAY_BF16)
-    write_dh_kernel<<<blocks, kThreadsRows, 0, s>>>(g, w, static_cast<uint16_t*>(d_hidden), d_hidden_ld);
-  else
-    write_dh_kernel<<<blocks, kThreadsRows, 0, s>>>(g, w, static_cast<float*>(d_hidden), d_hidden_ld);
-  return cudaGetLastError();
+    return launch_chained(write_dh_kernel<uint16_t>, blocks, kThreadsRows, 0, s, g, w, static_cast<uint16_t*>(d_hidden),
+                          d_hidden_ld, (int)whole, vec);
+  return launch_chained(write_dh_kernel<float>, blocks, kThreadsRows, 0, s, g, w, static_cast<float*>(d_hidden),
+                        d_hidden_ld, (int)whole, vec);
 }
 
 }  // namespace relay

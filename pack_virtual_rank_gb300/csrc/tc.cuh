@@ -144,13 +144,5 @@ __device__ __forceinline__ void tc_product(uint32_t tmem, uint64_t a, uint64_t b
       : "memory");
 }
 
-// ---------------------------------------------------------------------- numbers --
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 }  // namespace
 }  // namespace relay
