@@ -121,10 +121,11 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
     w.grad = reinterpret_cast<uint16_t*>(l.take(per_tile * ar.tiles_per_piece));
     if (dh) {
       // room for the cuts of a batch that keeps few rows, up to 256 MiB of partial sums
-      const int64_t one = 4ll * g.mpad * g.dim;
+      w.dh_ld = (int32_t)up(g.dim, 4);
+      const int64_t one = 4ll * g.mpad * w.dh_ld;
       w.tiles_per_piece = ar.tiles_per_piece;
       w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(ar.tiles_per_piece, 64), (256ll << 20) / one));
-      w.dh = reinterpret_cast<float*>(l.take(4ll * w.splits * g.mpad * g.dim));
+      w.dh = reinterpret_cast<float*>(l.take(one * w.splits));
     }
   }
   ar.bytes = (int64_t)(l.at - base);

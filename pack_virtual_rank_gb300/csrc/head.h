@@ -85,7 +85,8 @@ struct HeadWork {
   float* lse;         // [mpad] log2 units
   uint16_t* grad;     // [planes][mpad][grad_ld] of one piece: codes or exponentials, then the gradient
   int64_t grad_ld;    // columns per row
-  float* dh;          // [splits][mpad][dim] fp32 partial sums of d_hidden
+  float* dh;          // [splits][mpad][dh_ld] fp32 partial sums of d_hidden
+  int32_t dh_ld;      // dim rounded up to 4
   int32_t splits;     // most cuts of the vocabulary d_hidden may take
   int32_t tiles_per_piece;
 };

@@ -284,11 +284,12 @@ struct Stager {
     const uint32_t at = buf + row * 128 + ((group ^ (row & 7)) << 4);
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
   }
-  __device__ __forceinline__ void close(const CUtensorMap* map, int x, int y) {
+  __device__ __forceinline__ void close(const CUtensorMap* map, int x, int y, bool add = false) {
     fence_async_smem();
     __syncwarp();
     if (threadIdx.x % 32 == 0) {
-      map_store(map, x, y, buf);
+      if (add) map_add(map, x, y, buf);
+      else map_store(map, x, y, buf);
       store_commit();
     }
   }
@@ -335,6 +336,16 @@ struct Entries {
   __device__ __forceinline__ void step() { next = ++at < n ? col[at] : INT_MAX; }
 };
 
+// The thread's value of a column known only at run time. Written as selects that the compiler does
+// not see through: it would put the 128 registers into memory to index them.
+__device__ __forceinline__ float value_at(const float (&v)[kMine], int at) {
+  float r = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kMine; ++j)
+    asm("{\n.reg .pred p;\nsetp.eq.s32 p, %1, %2;\nselp.f32 %0, %3, %0, p;\n}" : "+f"(r) : "r"(at), "r"(j), "f"(v[j]));
+  return r;
+}
+
 // Steps of 2^-10 below the maximum, in log2 units, as the low 16 bits of the result's bits:
 // kCodeZero (2^-64 of the maximum and less) stands for 0.
 __device__ __forceinline__ uint32_t code_bits(float log2_below) {
@@ -352,15 +363,9 @@ __device__ __forceinline__ void finish_logits(const GemmArgs& p, const Item& t, 
   const int x = t.col0 + part * kMine, y = t.row0 + quarter * 32;
   Entries e = seeked;
   if (P != kGradient) {
-#pragma unroll
-    for (int c = 0; c < kMine; c += 32) {
-      if (e.next >= first + c + 32) continue;
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        while (e.next == first + c + j) {
-          e.z[e.at] = v[c + j] * p.g.inv_tau;
-          e.step();
-        }
+    while (e.next < first + kMine) {
+      e.z[e.at] = value_at(v, e.next - first) * p.g.inv_tau;
+      e.step();
     }
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     if (valid < kMine) {
@@ -411,15 +416,12 @@ __device__ __forceinline__ void finish_logits(const GemmArgs& p, const Item& t, 
 #pragma unroll
   for (int j = 0; j < kMine; ++j)
     v[j] = j < valid && row < live ? weight * exp2_approx(fmaf(v[j], scale, -lse)) : 0.0f;
+  while (e.next < first + kMine) {
+    const float d = weight * e.q[e.at];
+    const int at = e.next - first;
 #pragma unroll
-  for (int c = 0; c < kMine; c += 32) {
-    if (e.next >= first + c + 32) continue;
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      while (e.next == first + c + j) {
-        v[c + j] = fmaf(-weight, e.q[e.at], v[c + j]);
-        e.step();
-      }
+    for (int j = 0; j < kMine; ++j) v[j] -= j == at ? d : 0.0f;
+    e.step();
   }
 #pragma unroll
   for (int i = 0; i < PLANES; ++i) store_part(out, v, &p.c[0], x, i * p.g.mpad + y, kMine);
@@ -427,15 +429,31 @@ __device__ __forceinline__ void finish_logits(const GemmArgs& p, const Item& t, 
 
 template <int PLANES>
 __device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t, int live, int cuts,
-                                               float (&v)[kMine], int quarter, int part) {
-  const int row = t.row0 + quarter * 32 + threadIdx.x % 32, d0 = t.col0 + part * kMine;
-  if (row >= live) return;
+                                               float (&v)[kMine], int quarter, int part, Stager& out) {
+  const int r0 = t.row0 + quarter * 32, row = r0 + threadIdx.x % 32, d0 = t.col0 + part * kMine;
   const int valid = p.g.dim - d0;
+  if (valid <= 0 || r0 >= live) return;
   if (t.k_lo >= t.k_hi) {  // a cut without columns: nothing was multiplied
 #pragma unroll
     for (int j = 0; j < kMine; ++j) v[j] = 0.0f;
   }
-  if (p.whole && cuts == 1 && PLANES == 1) {
+  if (!p.whole || cuts > 1) {
+    // partial sums: whole lines through the staging buffer, added to where a piece came before (one
+    // addition per element and launch: in a fixed order). Rows past the live ones go unread.
+#pragma unroll
+    for (int c = 0; c < kMine; c += 32) {
+      if (c >= valid) break;
+      out.open();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        out.put(j, __float_as_uint(v[c + 4 * j]), __float_as_uint(v[c + 4 * j + 1]), __float_as_uint(v[c + 4 * j + 2]),
+                __float_as_uint(v[c + 4 * j + 3]));
+      out.close(&p.c[0], d0 + c, t.split * p.g.mpad + r0, !p.first);
+    }
+    return;
+  }
+  if (row >= live) return;
+  if (PLANES == 1) {
     uint16_t* to = static_cast<uint16_t*>(p.sh.dh) + p.w.perm[row] * p.sh.dh_ld + d0;
 #pragma unroll
     for (int j = 0; j < kMine; j += 8) {
@@ -451,30 +469,16 @@ __device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t,
     return;
   }
   // an uncut fp32 sum of the only piece is d_hidden's row itself
-  const bool direct = p.whole && cuts == 1;
-  float* to = direct ? static_cast<float*>(p.sh.dh) + p.w.perm[row] * p.sh.dh_ld + d0
-                     : p.w.dh + ((int64_t)t.split * p.g.mpad + row) * p.g.dim + d0;
-  if (direct ? p.dh_vec != 0 : p.g.dim % 4 == 0) {
+  float* to = static_cast<float*>(p.sh.dh) + p.w.perm[row] * p.sh.dh_ld + d0;
 #pragma unroll
-    for (int j = 0; j < kMine; j += 4) {
-      if (j + 4 > valid) {
+  for (int j = 0; j < kMine; j += 4) {
+    if (p.dh_vec && j + 4 <= valid) {
+      *reinterpret_cast<float4*>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // only a row of its own has a ragged end here
-          if (j + i < valid) to[j + i] = v[j + i];
-        continue;
-      }
-      float4* at = reinterpret_cast<float4*>(to + j);
-      float4 o = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-      if (!p.first) {
-        const float4 b = *at;
-        o = make_float4(b.x + o.x, b.y + o.y, b.z + o.z, b.w + o.w);
-      }
-      *at = o;
+      for (int i = 0; i < 4; ++i)
+        if (j + i < valid) to[j + i] = v[j + i];
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < kMine; ++j)
-      if (j < valid) to[j] = p.first ? v[j] : to[j] + v[j];
   }
 }
 
@@ -599,7 +603,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
         if (threadIdx.x % 32 == 0) bar_arrive(acc_empty + 8 * half);
       }
       if (!ok) break;
-      if constexpr (P == kDHidden) finish_dhidden<PLANES>(p, t, live, cuts, v, quarter, part);
+      if constexpr (P == kDHidden) finish_dhidden<PLANES>(p, t, live, cuts, v, quarter, part, out);
       else if constexpr (P == kDWeight) finish_dweight<PLANES>(p, t, v, quarter, part, out);
       else finish_logits<P, PLANES>(p, t, live, v, quarter, part, e, out);
     }
@@ -632,13 +636,14 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// A bf16 matrix [rows][cols] (row stride ld elements) read or written in boxes of 64 columns.
-bool matrix_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+// A bf16 (fp32) matrix [rows][cols], row stride ld elements, read or written in boxes of 64 (32)
+// columns, 128 bytes.
+bool matrix_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f32 = false) {
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, unit[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, unit,
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * (f32 ? 4 : 2)};
+  const cuuint32_t box[2] = {f32 ? 32u : 64u, (cuuint32_t)box_rows}, unit[2] = {1, 1};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, unit,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -663,6 +668,7 @@ bool maps_for(GemmArgs* a, int dtype) {
   if (P == kDHidden) {
     ok &= matrix_map(&a->a, w.grad, grad_rows, w.grad_ld, w.grad_ld, kBM);
     weight(kBK);
+    ok &= matrix_map(&a->c[0], w.dh, (int64_t)w.splits * g.mpad, g.dim, w.dh_ld, 32, true);
   } else if (P == kDWeight) {
     ok &= matrix_map(&a->a, w.grad, grad_rows, w.grad_ld, w.grad_ld, kBK);
     ok &= matrix_map(&a->b[0], w.hid, grad_rows, g.dim, w.dim_pad, kBK);

@@ -419,13 +419,13 @@ __global__ void __launch_bounds__(kThreadsRows)
   dep_wait();
   const int live = *w.n_live, cuts = head_cuts(g, live, w.tiles_per_piece, w.splits);
   if (whole && cuts == 1) return;
-  const int64_t cut = (int64_t)g.mpad * g.dim;
+  const int64_t cut = (int64_t)g.mpad * w.dh_ld;
   constexpr int kLanes = 4;
   const int64_t vecs = vec ? (int64_t)live * (g.dim / kLanes) : 0;
   const int64_t first = (int64_t)blockIdx.x * kThreadsRows + threadIdx.x, stride = (int64_t)gridDim.x * kThreadsRows;
   for (int64_t i = first; i < vecs; i += stride) {
     const int row = (int)(i / (g.dim / kLanes)), d = (int)(i % (g.dim / kLanes)) * kLanes;
-    const float* from = w.dh + (int64_t)row * g.dim + d;
+    const float* from = w.dh + (int64_t)row * w.dh_ld + d;
     float4 sum = *reinterpret_cast<const float4*>(from);
 #pragma unroll 8
     for (int c = 1; c < cuts; ++c) {
@@ -441,9 +441,10 @@ __global__ void __launch_bounds__(kThreadsRows)
   if (vec) return;
   for (int64_t i = first; i < (int64_t)live * g.dim; i += stride) {
     const int row = (int)(i / g.dim), d = (int)(i % g.dim);
-    float sum = w.dh[i];
+    const float* from = w.dh + (int64_t)row * w.dh_ld + d;
+    float sum = from[0];
 #pragma unroll 4
-    for (int c = 1; c < cuts; ++c) sum += w.dh[c * cut + i];
+    for (int c = 1; c < cuts; ++c) sum += from[c * cut];
     store_from_f32(dh + (int64_t)w.perm[row] * ld + d, sum);
   }
 }

@@ -1,15 +1,21 @@
 // router.cu -- relay_router_forward, relay_balance_loss, relay_router_backward.
 //
-// One warp per row. Lane l holds the row's experts [l * N, (l + 1) * N) in registers, read with
-// 16-byte loads where the rows allow it; the lowest lane of a tie holds the lowest expert.
+// L lanes of a warp share a row (32 / L rows to a warp); a lane holds N neighbouring experts in
+// registers, so the lowest lane of a tie holds the lowest expert. Up to 256 experts N is 8, so
+// that a lane's values are one or two 16-byte loads where the rows allow it, and a warp's reductions
+// serve as many rows as fit. The next rows are loaded while the present ones are worked on.
 //
-// Forward. Choosing k of E takes k rounds of: the largest of the lanes' best (one warp-wide
-// integer maximum over keys in the order of the values), the lowest lane that holds it steps to
-// its next. A lane finds its two best up front; only a lane chosen from twice, about one row in
-// two at 8 of 256, scans its values again, for the largest after the last one taken. Clearing
-// and rescanning in every round took three times the instructions. The softmax per expert adds up in registers over the rows
-// that a warp walks (a fixed assignment); warps join in shared memory in order and a second
-// launch joins the blocks in order: no sum of floats depends on timing.
+// Forward. The time goes into choosing, not into memory. Choosing takes k rounds of: the
+// largest of the lanes' best, over unsigned keys in the order of the values; the lane that holds
+// it steps to its next. A key is the value's upper 22 bits in order and the expert counted down,
+// so keys are unique, a tie goes to the lower expert, and a round needs neither the holder's lane
+// nor its index. That is exact for bf16. For fp32 it is exact unless two of the k + 1 largest
+// agree in their upper 22 bits; such a row, and one with a NaN, chooses again by whole values
+// (choose_exact). A lane finds its two best up front; only a lane chosen from twice, about one
+// row in two at 8 of 256, scans its values again. The softmax
+// per expert adds up in registers over the rows that a lane walks (a fixed assignment); lanes of a block join
+// in shared memory in order and a second launch joins the blocks in order: no sum of floats
+// depends on timing.
 //
 // Backward. p (a - sum p a) with a = d_prob plus d_gate at the chosen. The chosen are k of E, so the
 // row is written from d_prob alone and lane j then completes the j-th chosen expert: comparing
@@ -35,22 +41,44 @@ __device__ __forceinline__ float ld1(const uint16_t* p) { return __uint_as_float
 __device__ __forceinline__ void st1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st1(uint16_t* p, float v) { *p = (uint16_t)(bf16x2_rn(v, 0.0f) & 0xffffu); }
 
-// An unsigned key in the order of the value: +0 and -0 equal, NaN below -inf (1), 0 left for
-// "no expert here, or already chosen".
+// Unsigned and in the order of the value; +0 and -0 equal; 0 is left for "none". A NaN's key is
+// out of order.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));
-  const uint32_t k = (u >> 31) ? ~u : u | 0x80000000u;
-  return v != v ? 1u : k;
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
 }
+// The upper 22 bits of the key, then the expert counted down.
+constexpr uint32_t kExpertMask = RELAY_ROUTER_MAX_EXPERTS - 1;
+static_assert(kExpertMask == 1023, "ten bits of a key name the expert");
+__device__ __forceinline__ uint32_t unique_key(float v, int e) {
+  return (order_key(v) & ~kExpertMask) | (kExpertMask - (uint32_t)e);
+}
+__device__ __forceinline__ int key_expert(uint32_t k) { return (int)(kExpertMask - (k & kExpertMask)); }
 __device__ __forceinline__ float sum_warp(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
-
+// Over the L lanes of a row.
+template <int L>
+__device__ __forceinline__ float sum_row(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t max_row(uint32_t v) {
+  if constexpr (L == 32) {
+    return __reduce_max_sync(~0u, v);
+  } else {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(~0u, v, o));
+    return v;
+  }
+}
 // exp(x - m). The difference first: x and m may be the type's lowest value, which has no log2.
 __device__ __forceinline__ float exp_below(float x, float m) {
   float y;
@@ -58,101 +86,72 @@ __device__ __forceinline__ float exp_below(float x, float m) {
   return y;
 }
 
-// The lane's N values of a row; -inf past the last expert. vec: the rows are aligned to a lane's
-// values (at most 16 bytes) and a lane holds N experts or none.
-__device__ __forceinline__ uint4 ld16(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-  return r;
-}
-template <int N>
-__device__ __forceinline__ void load_row(float (&v)[N], const float* x, int lane, int experts, bool vec) {
-  const int e0 = lane * N;
-  if (vec) {
-    if constexpr (N >= 4) {
+// A lane's N values of a row as they lie in memory, -inf past the last expert. bytes: what one
+// load may take (16, 8, or one value), by the alignment of the rows.
+template <class T, int N>
+struct Lane {
+  static constexpr int kWords = N * (int)sizeof(T) / 4, kPerWord = 4 / (int)sizeof(T);
+  static constexpr uint32_t kNegInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+  uint32_t word[kWords];
+  __device__ __forceinline__ void load(const T* x, int e0, int experts, int bytes) {
 #pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        const uint4 u = e0 < experts ? ld16(x + e0 + i) : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-        TF32::unpack(u, v + i);
-      }
-      return;
-    } else if constexpr (N == 2) {
-      const float2 u = e0 < experts ? *reinterpret_cast<const float2*>(x + e0) : make_float2(-INFINITY, -INFINITY);
-      v[0] = u.x;
-      v[1] = u.y;
-      return;
+    for (int i = 0; i < kWords; ++i) word[i] = kNegInf;
+    if (bytes == 16) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4)
+        if (e0 + i * kPerWord < experts) {
+          const uint4 u = *reinterpret_cast<const uint4*>(x + e0 + i * kPerWord);
+          word[i] = u.x; word[i + 1] = u.y; word[i + 2] = u.z; word[i + 3] = u.w;
+        }
+    } else if (bytes == 8) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 2)
+        if (e0 + i * kPerWord < experts) {
+          const uint2 u = *reinterpret_cast<const uint2*>(x + e0 + i * kPerWord);
+          word[i] = u.x; word[i + 1] = u.y;
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (e0 + i < experts) {
+          if constexpr (sizeof(T) == 4) word[i] = __float_as_uint(x[e0 + i]);
+          else word[i / 2] = i % 2 ? (word[i / 2] & 0xffffu) | (uint32_t)x[e0 + i] << 16 : (word[i / 2] & 0xffff0000u) | x[e0 + i];
+        }
     }
   }
+  __device__ __forceinline__ void values(float (&v)[N]) const {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = e0 + i < experts ? x[e0 + i] : -INFINITY;
-}
-template <int N>
-__device__ __forceinline__ void load_row(float (&v)[N], const uint16_t* x, int lane, int experts, bool vec) {
-  const int e0 = lane * N;
-  if (vec) {
-    if constexpr (N >= 8) {
+    for (int i = 0; i < N; ++i)
+      v[i] = sizeof(T) == 4 ? __uint_as_float(word[i])
+                            : __uint_as_float(i % 2 ? word[i / kPerWord] & 0xffff0000u : word[i / kPerWord] << 16);
+  }
+  static __device__ __forceinline__ void store(T* x, const float (&v)[N], int e0, int experts, int bytes) {
+    uint32_t w[kWords];
 #pragma unroll
-      for (int i = 0; i < N; i += 8) {
-        const uint4 u = e0 < experts ? ld16(x + e0 + i) : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-        TBF16::unpack(u, v + i);
-      }
-      return;
-    } else if constexpr (N >= 2) {
+    for (int i = 0; i < kWords; ++i)
+      w[i] = sizeof(T) == 4 ? __float_as_uint(v[i]) : bf16x2_rn(v[i * kPerWord], v[i * kPerWord + kPerWord - 1]);
+    if (bytes == 16) {
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const uint32_t u = e0 < experts ? *reinterpret_cast<const uint32_t*>(x + e0 + i) : 0xff80ff80u;
-        v[i] = __uint_as_float(u << 16);
-        v[i + 1] = __uint_as_float(u & 0xffff0000u);
-      }
-      return;
+      for (int i = 0; i < kWords; i += 4)
+        if (e0 + i * kPerWord < experts)
+          *reinterpret_cast<uint4*>(x + e0 + i * kPerWord) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else if (bytes == 8) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 2)
+        if (e0 + i * kPerWord < experts)
+          *reinterpret_cast<uint2*>(x + e0 + i * kPerWord) = make_uint2(w[i], w[i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (e0 + i < experts) st1(x + e0 + i, v[i]);
     }
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = e0 + i < experts ? ld1(x + e0 + i) : -INFINITY;
-}
-template <int N>
-__device__ __forceinline__ void store_row(float* x, const float (&v)[N], int lane, int experts, bool vec) {
-  const int e0 = lane * N;
-  if (e0 >= experts) return;
-  if (vec) {
-    if constexpr (N >= 4) {
-#pragma unroll
-      for (int i = 0; i < N; i += 4)
-        *reinterpret_cast<float4*>(x + e0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-      return;
-    } else if constexpr (N == 2) {
-      *reinterpret_cast<float2*>(x + e0) = make_float2(v[0], v[1]);
-      return;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (e0 + i < experts) x[e0 + i] = v[i];
-}
-template <int N>
-__device__ __forceinline__ void store_row(uint16_t* x, const float (&v)[N], int lane, int experts, bool vec) {
-  const int e0 = lane * N;
-  if (e0 >= experts) return;
-  if (vec) {
-    if constexpr (N >= 8) {
-#pragma unroll
-      for (int i = 0; i < N; i += 8) *reinterpret_cast<uint4*>(x + e0 + i) = TBF16::pack(v + i);
-      return;
-    } else if constexpr (N >= 2) {
-#pragma unroll
-      for (int i = 0; i < N; i += 2) *reinterpret_cast<uint32_t*>(x + e0 + i) = bf16x2_rn(v[i], v[i + 1]);
-      return;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (e0 + i < experts) st1(x + e0 + i, v[i]);
-}
+};
 
 struct ForwardArgs {
   const void* logits;
   int64_t ld, tokens;
-  int experts, top, normalize, vec;
+  int experts, top, normalize, bytes;
   const uint8_t* mask;
   int32_t* index;
   float* gate;
@@ -160,11 +159,43 @@ struct ForwardArgs {
   float* part_prob;
 };
 
-template <class T, int N>
-__global__ void __launch_bounds__(kRouterThreads) router_forward_kernel(const ForwardArgs a) {
-  extern __shared__ float s_prob[];  // [warps][experts], then the counts [experts]
-  int32_t* s_count = reinterpret_cast<int32_t*>(s_prob + kRouterWarps * a.experts);
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+// Chooses by whole values, NaN below -inf, for the L lanes of a row: lane j gets the j-th expert.
+// Returns whether the row has a logit above -inf. Rare, and kept out of the kernel's registers.
+template <class T, int N, int L>
+__device__ __noinline__ bool choose_exact(const T* x, int experts, int top, bool counted, int* chosen) {
+  const int lane = threadIdx.x % 32, sub = lane % L;
+  uint32_t last = ~0u;
+  int last_e = -1;
+  bool live = false;
+  for (int j = 0; j < top; ++j) {
+    uint32_t best = 0;
+    int best_e = 0;
+    for (int i = 0; i < N && counted; ++i) {
+      const int e = sub * N + i;
+      if (e >= experts) break;
+      const float v = ld1(x + e);
+      const uint32_t k = v != v ? 1u : order_key(v);
+      if ((k < last || (k == last && e > last_e)) && k > best) {
+        best = k;
+        best_e = e;
+      }
+    }
+    const uint32_t win = max_row<L>(best);
+    const unsigned holders = __ballot_sync(~0u, best == win) >> (lane - sub) & (L == 32 ? ~0u : (1u << (L % 32)) - 1);
+    last_e = __shfl_sync(~0u, best_e, lane - sub + __ffs(holders) - 1);
+    last = win;
+    if (j == 0) live = win > kKeyNegInf;
+    if (sub == j) *chosen = last_e;
+  }
+  return live;
+}
+
+template <class T, int N, int L>
+__global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) router_forward_kernel(const ForwardArgs a) {
+  constexpr int kRows = 32 / L;
+  extern __shared__ float s_prob[];  // [warps * kRows][experts], then the counts [experts]
+  int32_t* s_count = reinterpret_cast<int32_t*>(s_prob + kRouterWarps * kRows * a.experts);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane % L, e0 = sub * N;
   dep_launch();
   for (int e = threadIdx.x; e < a.experts; e += kRouterThreads) s_count[e] = 0;
   dep_wait();
@@ -172,93 +203,93 @@ __global__ void __launch_bounds__(kRouterThreads) router_forward_kernel(const Fo
   float psum[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) psum[i] = 0.0f;
-  const unsigned below = (1u << lane) - 1;
-  const int64_t stride = (int64_t)gridDim.x * kRouterWarps;
-  for (int64_t row = (int64_t)blockIdx.x * kRouterWarps + warp; row < a.tokens; row += stride) {
-    int32_t* index = a.index + row * a.top;
-    float* gate = a.gate + row * a.top;
-    uint32_t key[N], best = 0, second = 0;
-    int best_i = 0, second_i = 0;
+  const int64_t stride = (int64_t)gridDim.x * kRouterWarps * kRows;
+  int64_t row = ((int64_t)blockIdx.x * kRouterWarps + warp) * kRows + lane / L;
+  const T* x = static_cast<const T*>(a.logits);
+  Lane<T, N> next;
+  bool next_counted = false;
+  auto fetch = [&](int64_t r) {
+    next_counted = r < a.tokens && (a.mask == nullptr || a.mask[r] != 0);
+    if (r < a.tokens) next.load(x + r * a.ld, e0, a.experts, a.bytes);
+  };
+  fetch(row);
+  for (; row - lane / L < a.tokens; row += stride) {
     float v[N];
-    bool counted = a.mask == nullptr || a.mask[row] != 0;
-    if (counted) {
-      load_row<N>(v, static_cast<const T*>(a.logits) + row * a.ld, lane, a.experts, a.vec);
+    next.values(v);
+    const bool counted = next_counted;
+    fetch(row + stride);
+    uint32_t key[N], best = 0, second = 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        key[i] = lane * N + i < a.experts ? order_key(v[i]) : 0u;
-        // equal keys: the lower expert stays ahead
-        if (key[i] > best) {
-          second = best;
-          second_i = best_i;
-          best = key[i];
-          best_i = i;
-        } else if (key[i] > second) {
-          second = key[i];
-          second_i = i;
-        }
-      }
+    for (int i = 0; i < N; ++i) {
+      key[i] = counted && e0 + i < a.experts ? unique_key(v[i], e0 + i) : 0u;
+      second = max(second, min(best, key[i]));
+      best = max(best, key[i]);
     }
-    uint32_t win = counted ? __reduce_max_sync(~0u, best) : 0u;
-    if (win <= kKeyNegInf) {  // masked out, or no logit above -inf
-      if (lane < a.top) {
-        index[lane] = -1;
-        gate[lane] = 0.0f;
-      }
-      continue;
+    uint32_t win = max_row<L>(best);
+    bool live = win > (kKeyNegInf | kExpertMask);  // else masked out, or no logit above -inf
+    // the largest value: a bf16 key holds all of it
+    float m;
+    if (sizeof(T) == 2) {
+      m = __uint_as_float(__float_as_uint(key_value(win)) & 0xffff0000u);
+    } else {
+      m = v[0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+      m = key_value(max_row<L>(order_key(m)));
     }
-    const float m = key_value(win);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       v[i] = exp_below(v[i], m);
       sum += v[i];
     }
-    sum = sum_warp(sum);
+    sum = sum_row<L>(sum);
     const float inv = 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < N; ++i) psum[i] = fmaf(v[i], inv, psum[i]);
-    bool again = false;  // the lane's second best is its best now
-    float mine = 0.0f, chosen_sum = 0.0f;
+    bool again = false;   // the lane's second best is its best now
+    bool close = false;   // two of the largest agree in their upper bits
+    uint32_t mine = 0;    // lane j: the key chosen j-th
     for (int j = 0; j < a.top; ++j) {
-      const float val = win <= 1u ? NAN : exp_below(key_value(win), m);
-      chosen_sum += val;
-      if (lane == j) mine = val;
-      const unsigned holders = __ballot_sync(~0u, best == win);
-      if (best == win && (holders & below) == 0) {
-        const int e = lane * N + best_i;
-        index[j] = e;
-        atomicAdd(&s_count[e], 1);  // integers: any order gives the same sum
-        if (!again) {
-          again = true;
-          best = second;
-          best_i = second_i;
-        } else {
-          // the largest after the one just taken
-          uint32_t k = 0;
-          int at = 0;
+      const bool holder = best == win;
+      if (sub == j) mine = win;
+      uint32_t after = second;
+      if (holder && again) {  // the largest after the one just taken
+        after = 0;
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            if ((key[i] < win || (key[i] == win && i > best_i)) && key[i] > k) {
-              k = key[i];
-              at = i;
-            }
-          best = k;
-          best_i = at;
-        }
+        for (int i = 0; i < N; ++i)
+          if (key[i] < win) after = max(after, key[i]);
       }
-      win = __reduce_max_sync(~0u, best);
+      if (holder) best = after;
+      again |= holder;
+      const uint32_t then = max_row<L>(best);
+      if (sizeof(T) == 4) close |= (win ^ then) <= kExpertMask;
+      win = then;
     }
-    float scale = a.normalize ? 1.0f / chosen_sum : inv;
+    int chosen = key_expert(mine);
+    if (__any_sync(~0u, counted && (close || sum != sum)))
+      live = choose_exact<T, N, L>(x + (row < a.tokens ? row : 0) * a.ld, a.experts, a.top, counted, &chosen);
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) psum[i] = fmaf(v[i], inv, psum[i]);
+    }
+    const bool chose = live && sub < a.top;
+    // the key lost the value's lower bits (fp32): read it again
+    const float val = chose ? exp_below(ld1(x + row * a.ld + chosen), m) : 0.0f;
+    float scale = inv;
+    if (a.normalize) scale = 1.0f / sum_row<L>(val);
     if (sum != sum) scale = sum;
-    if (lane < a.top) gate[lane] = mine * scale;
+    if (sub < a.top && row < a.tokens) {
+      a.index[row * a.top + sub] = live ? chosen : -1;
+      a.gate[row * a.top + sub] = live ? val * scale : 0.0f;
+      if (live) atomicAdd(&s_count[chosen], 1);  // integers: any order gives the same sum
+    }
   }
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    if (lane * N + i < a.experts) s_prob[warp * a.experts + lane * N + i] = psum[i];
+    if (e0 + i < a.experts) s_prob[(warp * kRows + lane / L) * a.experts + e0 + i] = psum[i];
   __syncthreads();
   for (int e = threadIdx.x; e < a.experts; e += kRouterThreads) {
     float p = 0.0f;
-    for (int i = 0; i < kRouterWarps; ++i) p += s_prob[i * a.experts + e];
+    for (int i = 0; i < kRouterWarps * kRows; ++i) p += s_prob[i * a.experts + e];
     a.part_prob[(int64_t)blockIdx.x * a.experts + e] = p;
     a.part_count[(int64_t)blockIdx.x * a.experts + e] = s_count[e];
   }
@@ -337,42 +368,52 @@ struct BackwardArgs {
   const void* logits;
   void* d_logits;
   int64_t ld, d_ld, tokens;
-  int experts, top, normalize, vec, d_vec;
+  int experts, top, normalize, bytes, d_bytes;
   const int32_t* index;
   const float* d_gate;
   const float* d_prob;
 };
 
-template <class T, int N>
+template <class T, int N, int L>
 __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const BackwardArgs a) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  constexpr int kRows = 32 / L;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane % L, e0 = sub * N;
   dep_launch();
   dep_wait();
   float g[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    g[i] = lane * N + i < a.experts && a.d_prob != nullptr ? a.d_prob[lane * N + i] : 0.0f;
-  const int64_t stride = (int64_t)gridDim.x * kRouterWarps;
-  for (int64_t row = (int64_t)blockIdx.x * kRouterWarps + warp; row < a.tokens; row += stride) {
-    const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-    T* dx = static_cast<T*>(a.d_logits) + row * a.d_ld;
-    const int mine = lane < a.top ? a.index[row * a.top + lane] : -1;
-    const float dg = lane < a.top && a.d_gate != nullptr ? a.d_gate[row * a.top + lane] : 0.0f;
-    float p[N];
-    if (__shfl_sync(~0u, mine, 0) < 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) p[i] = 0.0f;
-      store_row<N>(dx, p, lane, a.experts, a.d_vec);
-      continue;
+  for (int i = 0; i < N; ++i) g[i] = e0 + i < a.experts && a.d_prob != nullptr ? a.d_prob[e0 + i] : 0.0f;
+  const int64_t stride = (int64_t)gridDim.x * kRouterWarps * kRows;
+  int64_t row = ((int64_t)blockIdx.x * kRouterWarps + warp) * kRows + lane / L;
+  const T* x = static_cast<const T*>(a.logits);
+  Lane<T, N> next;
+  int next_index = -1;
+  float next_dg = 0.0f;
+  auto fetch = [&](int64_t r) {
+    next_index = -1;
+    next_dg = 0.0f;
+    if (r >= a.tokens) return;
+    next.load(x + r * a.ld, e0, a.experts, a.bytes);
+    if (sub < a.top) {
+      next_index = a.index[r * a.top + sub];
+      if (a.d_gate != nullptr) next_dg = a.d_gate[r * a.top + sub];
     }
-    load_row<N>(p, x, lane, a.experts, a.vec);
-    const bool holds = mine >= 0 && mine < a.experts;
-    const float own = holds ? ld1(x + mine) : -INFINITY;
-    // the first chosen logit is the row's largest, but the index is the caller's
+  };
+  fetch(row);
+  for (; row - lane / L < a.tokens; row += stride) {
+    float p[N];
+    next.values(p);
+    const int mine = next_index;
+    const float dg = next_dg;
+    fetch(row + stride);
+    const bool in = row < a.tokens, live = __shfl_sync(~0u, mine, lane - sub) >= 0;
+    const bool holds = live && mine >= 0 && mine < a.experts;
+    const float own = holds ? ld1(x + row * a.ld + mine) : -INFINITY;
+    const float own_g = holds && a.d_prob != nullptr ? a.d_prob[mine] : 0.0f;
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i) m = fmaxf(m, p[i]);
-    m = key_value(__reduce_max_sync(~0u, order_key(m)));
+    m = key_value(max_row<L>(order_key(m)));
     float sum = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -380,36 +421,35 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const B
       sum += p[i];
       dot = fmaf(p[i], g[i], dot);
     }
-    const float e = exp_below(own, m);  // 0 for a lane without a choice
-    const float own_prob = holds && a.d_prob != nullptr ? a.d_prob[mine] : 0.0f;
-    const float inv = 1.0f / sum_warp(sum);
-    const float own_p = e * inv;
+    const float e = holds ? exp_below(own, m) : 0.0f;
+    const float inv = 1.0f / sum_row<L>(sum);
     if (!a.normalize) dot = fmaf(e, dg, dot);
-    dot = sum_warp(dot) * inv;
-    float extra;
+    dot = sum_row<L>(dot) * inv;
+    float extra = e * inv * dg;
     if (a.normalize) {
-      const float c = e / sum_warp(e), inner = sum_warp(c * dg);
+      const float c = e / sum_row<L>(e), inner = sum_row<L>(c * dg);
       extra = c * (dg - inner);
-    } else {
-      extra = own_p * dg;
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = p[i] * inv * (g[i] - dot);
-    store_row<N>(dx, p, lane, a.experts, a.d_vec);
+    for (int i = 0; i < N; ++i) p[i] = live ? p[i] * inv * (g[i] - dot) : 0.0f;
+    T* dx = static_cast<T*>(a.d_logits) + row * a.d_ld;
+    if (in) Lane<T, N>::store(dx, p, e0, a.experts, a.d_bytes);
     __syncwarp();  // orders the row's stores before the chosen experts'
-    if (holds) st1(dx + mine, own_p * (own_prob - dot) + extra);
+    if (in && holds) st1(dx + mine, e * inv * (own_g - dot) + extra);
   }
 }
 
-// Registers per lane for a number of experts.
+// Values per lane and lanes per row: 8 and as few lanes as hold the experts and the choice.
 template <class F>
-cudaError_t by_width(int experts, F f) {
-  if (experts <= 32) return f(std::integral_constant<int, 1>());
-  if (experts <= 64) return f(std::integral_constant<int, 2>());
-  if (experts <= 128) return f(std::integral_constant<int, 4>());
-  if (experts <= 256) return f(std::integral_constant<int, 8>());
-  if (experts <= 512) return f(std::integral_constant<int, 16>());
-  return f(std::integral_constant<int, 32>());
+cudaError_t by_width(int experts, int top, F f) {
+  using std::integral_constant;
+  const int lanes = std::max((experts + 7) / 8, top);
+  if (lanes <= 4) return f(integral_constant<int, 8>(), integral_constant<int, 4>());
+  if (lanes <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 8>());
+  if (lanes <= 16) return f(integral_constant<int, 8>(), integral_constant<int, 16>());
+  if (lanes <= 32) return f(integral_constant<int, 8>(), integral_constant<int, 32>());
+  if (lanes <= 64) return f(integral_constant<int, 16>(), integral_constant<int, 32>());
+  return f(integral_constant<int, 32>(), integral_constant<int, 32>());
 }
 
 // Blocks of the forward pass, whose statistics are joined afterwards: at most four an SM of the
@@ -418,12 +458,12 @@ int64_t forward_blocks(int64_t tokens) {
   return std::max<int64_t>(1, std::min<int64_t>((tokens + kRouterWarps - 1) / kRouterWarps, 4 * 152));
 }
 
-// Rows a lane's values can be read from (or written to) whole: see load_row.
-int whole_lanes(const void* p, int64_t ld, int64_t esize, int experts) {
-  int n = 1;
-  while (n * 32 < experts) n *= 2;
-  const int64_t bytes = std::min<int64_t>(16, n * esize);
-  return experts % n == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * esize % bytes == 0;
+// Bytes one load of a lane's values may take: rows aligned to them, and made of whole ones.
+int load_bytes(const void* p, int64_t ld, int64_t esize, int experts) {
+  for (int bytes = 16; bytes > 4; bytes /= 2)
+    if (reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * esize % bytes == 0 && experts * esize % bytes == 0)
+      return bytes;
+  return (int)esize;
 }
 
 relay_status_t bad(const std::string& msg) {
@@ -505,13 +545,13 @@ relay_status_t relay_router_forward(const void* logits, int64_t row_stride, rela
   const int blocks = (int)forward_blocks(tokens);
   int32_t* part_count = reinterpret_cast<int32_t*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~(uintptr_t)15);
   float* part_prob = reinterpret_cast<float*>(part_count + (int64_t)blocks * experts);
-  const ForwardArgs a{logits, row_stride, tokens, experts, top, normalize, whole_lanes(logits, row_stride, E, experts),
+  const ForwardArgs a{logits, row_stride, tokens, experts, top, normalize, load_bytes(logits, row_stride, E, experts),
                       mask, index, gate,
                       blocks == 1 ? counts : part_count, blocks == 1 ? prob_sum : part_prob};
-  const size_t smem = (size_t)(kRouterWarps + 1) * experts * 4;
-  cudaError_t e = by_width(experts, [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    return launch_chained(dtype == RELAY_BF16 ? router_forward_kernel<uint16_t, N> : router_forward_kernel<float, N>,
+  cudaError_t e = by_width(experts, top, [&](auto n, auto l) {
+    constexpr int N = decltype(n)::value, L = decltype(l)::value;
+    const size_t smem = (size_t)(kRouterWarps * (32 / L) + 1) * experts * 4;
+    return launch_chained(dtype == RELAY_BF16 ? router_forward_kernel<uint16_t, N, L> : router_forward_kernel<float, N, L>,
                           blocks, kRouterThreads, smem, stream, a);
   });
   if (e == cudaSuccess && blocks > 1) {
@@ -559,12 +599,12 @@ relay_status_t relay_router_backward(const void* logits, int64_t row_stride, rel
   st = check_spans(s, 5);
   if (st != RELAY_OK) return st;
   const BackwardArgs a{logits, d_logits, row_stride, d_row_stride, tokens, experts, top, normalize,
-                       whole_lanes(logits, row_stride, E, experts), whole_lanes(d_logits, d_row_stride, E, experts),
+                       load_bytes(logits, row_stride, E, experts), load_bytes(d_logits, d_row_stride, E, experts),
                        index, d_gate, d_prob};
   const int blocks = (int)std::min<int64_t>((tokens + kRouterWarps - 1) / kRouterWarps, 8 * 152);
-  return done(by_width(experts, [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    return launch_chained(dtype == RELAY_BF16 ? router_backward_kernel<uint16_t, N> : router_backward_kernel<float, N>,
+  return done(by_width(experts, top, [&](auto n, auto l) {
+    constexpr int N = decltype(n)::value, L = decltype(l)::value;
+    return launch_chained(dtype == RELAY_BF16 ? router_backward_kernel<uint16_t, N, L> : router_backward_kernel<float, N, L>,
                           blocks, kRouterThreads, 0, stream, a);
   }));
 }

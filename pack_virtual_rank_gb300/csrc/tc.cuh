@@ -73,6 +73,12 @@ __device__ __forceinline__ void map_store(const CUtensorMap* map, int x, int y, 
                "r"(y), "r"(src)
                : "memory");
 }
+// Adds the box to what memory holds (fp32).
+__device__ __forceinline__ void map_add(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 template <int PENDING>
 __device__ __forceinline__ void store_wait_read() {

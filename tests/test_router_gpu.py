@@ -168,3 +168,25 @@ def test_equal_calls_equal_bits(dtype):
     a, b = run(x, 6), run(x, 6)
     for name in a:
         assert torch.equal(a[name], b[name]), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("experts,top", [(8, 3), (60, 4), (128, 8), (256, 8), (600, 5)])
+def test_large_offsets_and_near_equal_logits(experts, top, dtype):
+    """Rows far from 0 (an additive mask over all experts), rows whose values differ in their last bits
+    only, and NaN beside them: the choice is by whole values."""
+    g = torch.Generator().manual_seed(17)
+    x = torch.randn(300, experts, generator=g)
+    x[0:50] = x[0:50] * 100 - 1e9
+    x[50:100] = x[50:100] * 1e30
+    x[100:200] = 1.0 + torch.randint(0, 40, (100, experts), generator=g) * 2.0 ** -23
+    x[200:250] = -3.0 - torch.randint(0, 5, (50, experts), generator=g) * 2.0 ** -22
+    x = x.to(DT[dtype])
+    for normalize in (False, True):
+        want = ref.router(x, top, normalize, None, 1.0, None)
+        out = run(x, top, normalize, coef=1.0)
+        assert torch.equal(out["index"], want["index"])
+        assert torch.equal(out["counts"], want["counts"])
+        # exp of a difference d is off by |d| f: 2^-9 covers d up to 88 in bf16's and fp32's arithmetic
+        small = want["gate"] > 1e-30
+        assert bool(((out["gate"].double() - want["gate"]).abs() <= 2.0 ** -15 * want["gate"] + 1e-30).all()), small.sum()
