@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) router_forward
     if (r < a.tokens) next.load(x + r * a.ld, e0, a.experts, a.bytes);
   };
   fetch(row);
+  const bool full = a.experts == N * L;
   for (; row - lane / L < a.tokens; row += stride) {
     float v[N];
     next.values(v);
@@ -221,10 +222,12 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) router_forward
     uint32_t key[N], best = 0, second = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      key[i] = counted && e0 + i < a.experts ? unique_key(v[i], e0 + i) : 0u;
+      key[i] = unique_key(v[i], e0 + i);
+      if (!full && e0 + i >= a.experts) key[i] = 0u;
       second = max(second, min(best, key[i]));
       best = max(best, key[i]);
     }
+    if (!counted) best = second = 0;
     uint32_t win = max_row<L>(best);
     bool live = win > (kKeyNegInf | kExpertMask);  // else masked out, or no logit above -inf
     // the largest value: a bf16 key holds all of it
@@ -248,21 +251,26 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) router_forward
     bool again = false;   // the lane's second best is its best now
     bool close = false;   // two of the largest agree in their upper bits
     uint32_t mine = 0;    // lane j: the key chosen j-th
+#pragma unroll 4
     for (int j = 0; j < a.top; ++j) {
       const bool holder = best == win;
       if (sub == j) mine = win;
       uint32_t after = second;
-      if (holder && again) {  // the largest after the one just taken
-        after = 0;
+      // the largest after the one just taken; a vote, so that it is a branch and not predicated
+      // into every round
+      if (__any_sync(~0u, holder && again)) {
+        uint32_t left = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (key[i] < win) after = max(after, key[i]);
+        for (int i = 0; i < N; ++i) left = max(left, key[i] < win ? key[i] : 0u);
+        if (again) after = left;
       }
       if (holder) best = after;
       again |= holder;
-      const uint32_t then = max_row<L>(best);
-      if (sizeof(T) == 4) close |= (win ^ then) <= kExpertMask;
-      win = then;
+      win = max_row<L>(best);
+    }
+    if (sizeof(T) == 4) {
+      const uint32_t after = __shfl_down_sync(~0u, mine, 1, L);
+      close = sub < a.top && (mine ^ (sub + 1 == a.top ? win : after)) <= kExpertMask;
     }
     int chosen = key_expert(mine);
     if (__any_sync(~0u, counted && (close || sum != sum)))
