@@ -21,7 +21,7 @@
 namespace relay {
 
 constexpr int kHeadTile = 256;     // columns a shard is padded to
-constexpr int kHeadRowTile = 128;  // rows the live rows are padded to
+constexpr int kHeadRowTile = 256;  // rows the live rows are padded to
 constexpr int kHeadStatTile = 128; // columns one (max, sum) of a row stands for
 
 // The form in which the exponentials of a bf16 head are kept: how far a logit lies below the
@@ -93,21 +93,22 @@ struct HeadWork {
 
 // Cuts of the vocabulary for d_hidden, whose tiles alone are too few, or too few in the last
 // round, to fill the GPU. Costs are in inner steps of one tile (64 columns, about 0.27 us): the
-// rounds of the GPU's SMs times the steps of a cut, plus writing and reading a cut's fp32 partial
+// rounds of the GPU's pairs of SMs times the steps of a cut, plus writing and reading a cut's fp32 partial
 // sums (8 bytes a value; a step's time moves about 1.8 MB). The live rows are known on
 // the device only, so kernels call this themselves and agree.
 #ifdef __CUDACC__
 __device__ __forceinline__ int head_cuts(const HeadGeom& g, int live, int tiles, int most) {
   // whole warps call it: a lane prices two numbers of cuts (most is at most 64)
   const int64_t items = (int64_t)((live + kHeadRowTile - 1) / kHeadRowTile) * ((g.dim + kHeadTile - 1) / kHeadTile);
-  if (most == 1 || items >= 4 * g.sms) return 1;
+  const int pairs = g.sms / 2;
+  if (most == 1 || items >= 4 * pairs) return 1;
   const int64_t move = 1 + (int64_t)live * g.dim / 225000;
   uint32_t least = ~0u;
   int best = 1;
   for (int i = 0; i < 2; ++i) {
     const int s = 1 + threadIdx.x % 32 + 32 * i;
     if (s > most) continue;
-    const uint32_t rounds = ((uint32_t)items * s + g.sms - 1) / g.sms;
+    const uint32_t rounds = ((uint32_t)items * s + pairs - 1) / pairs;
     const int64_t cost = (int64_t)rounds * (((uint32_t)tiles * 4 + s - 1) / s + 8) + (s > 1 ? s * move : 0);
     const uint32_t c = cost < 0xfffffffell ? (uint32_t)cost : 0xfffffffeu;
     if (c < least) {

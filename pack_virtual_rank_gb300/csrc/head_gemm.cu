@@ -4,12 +4,17 @@
 //   d_hidden   g . weight                 rows x dim, inner dimension the piece's columns
 //   d_weight   g^T . hidden               columns x dim, inner dimension the live rows
 //
-// One CTA per SM walks 128 x 256 tiles of the result. A producer thread brings 64 elements of the
-// inner dimension at a time into a ring of shared memory stages (tensor map loads, 128-byte
-// swizzle); one thread issues the products, whose accumulators alternate between two halves of
-// tensor memory; eight warps turn one half into its result while the other fills. Operands are
+// A pair of CTAs, one per SM, walks 256 x 256 tiles of the result; each holds 128 rows of it. A
+// producer thread in each brings its half of both operands, 64 elements of the inner dimension at a
+// time, into a ring of shared memory stages (tensor map loads, 128-byte swizzle); one thread of the
+// pair issues the products (M = 256), whose accumulators alternate between two halves of tensor
+// memory; eight warps turn one half into its result while the other fills. Operands are
 // read as they lie: where the outer dimension is the contiguous one (weight in d_hidden, both in
 // d_weight) the descriptors say so, and nothing is transposed in memory.
+//
+// Why pairs: a single CTA's 128 x 256 tile reads 48 KiB for 512 cycles of products, and the path from
+// L2 into an SM carries 64 bytes a cycle: the tensor pipe was 69-71% busy at 18 TB/s of such
+// reads. A pair shares the second operand, 32 KiB for the same products.
 //
 // The accumulator puts a row of the tile into one lane, so the softmax statistics of a row are
 // one thread's registers: no shuffles.
@@ -30,9 +35,12 @@ namespace {
 // Bit 1: a wait ran out, the call's outputs are unspecified.
 __device__ unsigned g_head_fault;
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;
-constexpr int kStages = 4;
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kBM = 128, kBN = 256, kBK = 64;  // rows of one CTA, columns of the pair, inner step
+constexpr int kPairM = 2 * kBM;
+constexpr int kHalf = kBN / 2;                 // columns (B's rows) one CTA brings
+constexpr int kStages = 6;
+constexpr int kABytes = kBM * kBK * 2, kBBytes = kHalf * kBK * 2, kStageBytes = kABytes + kBBytes;
+static_assert(kPairM == kHeadRowTile && kBN == kHeadTile, "tiles are what rows and columns are padded to");
 constexpr int kFinishWarps = 8;                        // warps that turn accumulators into results
 constexpr int kOutWarpBytes = 32 * 64 * 2;             // 32 rows x 64 columns of 16 bits, one per warp
 constexpr int kOutBytes = kFinishWarps * kOutWarpBytes;
@@ -72,10 +80,10 @@ struct GemmArgs {
   int32_t group;     // logits: row tiles walked together before the next column tile
 };
 
-// One tile of the result and the inner range behind it.
+// This CTA's rows of one tile of the result, and the inner range behind it.
 struct Item {
-  int row0, col0;          // first row and column of the tile
-  int tile, shard, v0;     // padded column tile, its shard, first row of the shard's weight
+  int row0, col0;          // first row of this CTA's half and first column of the tile
+  int tile, shard, v0;     // padded column tile, its shard, the shard's weight row it starts at
   int k_lo, k_hi;          // inner steps of 64 (d_hidden: column tiles)
   int split;
 };
@@ -83,16 +91,16 @@ struct Item {
 // cuts: head_cuts (d_hidden).
 template <int P>
 __device__ __forceinline__ int item_count(const GemmArgs& p, int live, int cuts) {
-  const int mt = (live + kBM - 1) / kBM, tiles = p.tile_hi - p.tile_lo;
+  const int mt = (live + kPairM - 1) / kPairM, tiles = p.tile_hi - p.tile_lo;
   const int nd = (p.g.dim + kBN - 1) / kBN;
   if (P == kDHidden) return mt * nd * cuts;
-  if (P == kDWeight) return tiles * 2 * nd;
+  if (P == kDWeight) return tiles * nd;
   return mt * tiles;
 }
 
 template <int P>
-__device__ __forceinline__ Item item_at(const GemmArgs& p, int live, int cuts, int i) {
-  const int mt = (live + kBM - 1) / kBM, tiles = p.tile_hi - p.tile_lo;
+__device__ __forceinline__ Item item_at(const GemmArgs& p, int live, int cuts, int rank, int i) {
+  const int mt = (live + kPairM - 1) / kPairM, tiles = p.tile_hi - p.tile_lo;
   const int nd = (p.g.dim + kBN - 1) / kBN;
   Item t{};
   if (P == kDHidden) {
@@ -100,21 +108,20 @@ __device__ __forceinline__ Item item_at(const GemmArgs& p, int live, int cuts, i
     t.col0 = i % nd * kBN;
     i /= nd;
     t.split = i % cuts;
-    t.row0 = i / cuts * kBM;
+    t.row0 = i / cuts * kPairM + rank * kBM;
     t.k_lo = p.tile_lo + (int)((int64_t)tiles * t.split / cuts);
     t.k_hi = p.tile_lo + (int)((int64_t)tiles * (t.split + 1) / cuts);
   } else if (P == kDWeight) {
     t.col0 = i % nd * kBN;
-    i /= nd;
-    t.tile = p.tile_lo + i / 2;
+    t.tile = p.tile_lo + i / nd;
     t.shard = head_shard_of_tile(p.g, t.tile);
-    t.v0 = (t.tile - p.g.tile0[t.shard]) * kHeadTile + i % 2 * kBM;
-    t.row0 = (t.tile - p.tile_lo) * kHeadTile + i % 2 * kBM;
-    t.k_hi = t.v0 < p.g.rows[t.shard] ? (live + kBK - 1) / kBK : 0;
+    t.v0 = (t.tile - p.g.tile0[t.shard]) * kHeadTile + rank * kBM;
+    t.row0 = (t.tile - p.tile_lo) * kHeadTile + rank * kBM;
+    t.k_hi = (live + kBK - 1) / kBK;
   } else {
     const int per = p.group * tiles, band = i / per, in_band = i % per;
     const int width = min(p.group, mt - band * p.group);
-    t.row0 = (band * p.group + in_band % width) * kBM;
+    t.row0 = (band * p.group + in_band % width) * kPairM + rank * kBM;
     t.tile = p.tile_lo + in_band / width;
     t.shard = head_shard_of_tile(p.g, t.tile);
     t.v0 = (t.tile - p.g.tile0[t.shard]) * kHeadTile;
@@ -149,22 +156,25 @@ constexpr int kPairs = PLANES == 1 ? 1 : 6;
 __device__ __forceinline__ int pair_a(int i) { return (0x200110 >> (4 * (5 - i))) & 15; }  // 2 0 0 1 1 0
 __device__ __forceinline__ int pair_b(int i) { return (0x021010 >> (4 * (5 - i))) & 15; }  // 0 2 1 0 1 0
 
+// full: the stage barriers of the pair's first CTA; empty: this CTA's own.
 template <int P, int PLANES>
-__device__ void produce(const GemmArgs& p, int live, int cuts, uint32_t ring, uint32_t full, uint32_t empty,
+__device__ void produce(const GemmArgs& p, int live, int cuts, int rank, uint32_t ring, uint32_t full, uint32_t empty,
                         volatile int* gave_up) {
+  const uint32_t pair_full = pair_addr(full, 0);
+  const int half = rank * kHalf;
   int stage = 0;
   uint32_t phase = 0;
   int64_t issued = 0;
   const int items = item_count<P>(p, live, cuts);
   bool ok = true;
-  for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-    const Item t = item_at<P>(p, live, cuts, i);
+  for (int i = blockIdx.x / 2; ok && i < items; i += gridDim.x / 2) {
+    const Item t = item_at<P>(p, live, cuts, rank, i);
     ok = for_steps<P>(p, t, [&](int k, int k_shard, int k_v) {
       for (int pair = 0; pair < kPairs<PLANES>; ++pair) {
         const int pa = PLANES == 1 ? 0 : pair_a(pair), pb = PLANES == 1 ? 0 : pair_b(pair);
         if (!bar_wait(empty + 8 * stage, phase ^ 1, gave_up)) return false;
-        const uint32_t bar = full + 8 * stage, sa = ring + stage * kStageBytes, sb = sa + kABytes;
-        bar_expect(bar, kStageBytes);
+        const uint32_t bar = pair_full + 8 * stage, sa = ring + stage * kStageBytes, sb = sa + kABytes;
+        if (rank == 0) bar_expect(full + 8 * stage, 2 * kStageBytes);
         ++issued;
         const int wrow = pb * p.g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;  // plane of a packed weight
         if (P == kDHidden) {
@@ -172,18 +182,18 @@ __device__ void produce(const GemmArgs& p, int live, int cuts, uint32_t ring, ui
           const bool packed = p.w.wpack != nullptr;
           const CUtensorMap* m = &p.b[packed ? 0 : k_shard];
           const int y = packed ? wrow + p.g.tile0[k_shard] * kHeadTile + k_v : k_v;
-          for (int j = 0; j < kBN / 64; ++j) map_load(sb + j * 8192, m, t.col0 + 64 * j, y, bar);
+          for (int j = 0; j < kHalf / 64; ++j) map_load(sb + j * 8192, m, t.col0 + half + 64 * j, y, bar);
         } else if (P == kDWeight) {
           for (int j = 0; j < kBM / 64; ++j)
             map_load(sa + j * 8192, &p.a, t.row0 + 64 * j, pa * p.g.mpad + k * kBK, bar);
-          for (int j = 0; j < kBN / 64; ++j)
-            map_load(sb + j * 8192, &p.b[0], t.col0 + 64 * j, pb * p.g.mpad + k * kBK, bar);
+          for (int j = 0; j < kHalf / 64; ++j)
+            map_load(sb + j * 8192, &p.b[0], t.col0 + half + 64 * j, pb * p.g.mpad + k * kBK, bar);
         } else {
           map_load(sa, &p.a, k * kBK, pa * p.g.mpad + t.row0, bar);
           if (p.w.wpack != nullptr)
-            map_load(sb, &p.b[0], k * kBK, wrow + t.tile * kHeadTile, bar);
+            map_load(sb, &p.b[0], k * kBK, wrow + t.tile * kHeadTile + half, bar);
           else
-            map_load(sb, &p.b[t.shard], k * kBK, t.v0, bar);
+            map_load(sb, &p.b[t.shard], k * kBK, t.v0 + half, bar);
         }
         if (++stage == kStages) {
           stage = 0;
@@ -194,15 +204,20 @@ __device__ void produce(const GemmArgs& p, int live, int cuts, uint32_t ring, ui
     });
   }
   if (ok) return;
-  // giving up: no load may still be on its way into shared memory when the CTA leaves
+  // giving up: no load may still be on its way into shared memory when the CTA leaves. The first CTA's
+  // barriers count both CTAs' loads, and the pair leaves together; what they do not count (a stage
+  // only one of the two asked for) lands in microseconds.
   const uint64_t start = global_ns();
-  for (int back = 0; back < kStages && back < issued; ++back) {
+  for (int back = 0; rank == 0 && back < kStages && back < issued; ++back) {
     if (--stage < 0) {
       stage = kStages - 1;
       phase ^= 1;
     }
     while (!bar_try(full + 8 * stage, phase) && global_ns() - start < kWaitNs) {
     }
+  }
+  const uint64_t drained = global_ns();
+  while (global_ns() - drained < 10000000ull) {
   }
 }
 
@@ -211,13 +226,13 @@ __device__ void multiply(const GemmArgs& p, int live, int cuts, uint32_t ring, u
                          uint32_t acc_full, uint32_t acc_empty, uint32_t drain, uint32_t tmem,
                          volatile int* gave_up) {
   constexpr bool kAOuter = P == kDWeight, kBOuter = P == kDWeight || P == kDHidden;
-  constexpr uint32_t kDesc = product_desc(kBM, kBN, kAOuter, kBOuter);
+  constexpr uint32_t kDesc = product_desc(kPairM, kBN, kAOuter, kBOuter);
   int stage = 0, n = 0;
   uint32_t phase = 0;
   const int items = item_count<P>(p, live, cuts);
   bool ok = true;
-  for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-    const Item t = item_at<P>(p, live, cuts, i);
+  for (int i = blockIdx.x / 2; ok && i < items; i += gridDim.x / 2) {
+    const Item t = item_at<P>(p, live, cuts, 0, i);
     int in_chain = 0;
     auto open = [&] {
       const bool free = bar_wait(acc_empty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, gave_up);
@@ -520,12 +535,12 @@ __device__ __forceinline__ void finish_dweight(const GemmArgs& p, const Item& t,
 }
 
 template <int P, int PLANES>
-__global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __grid_constant__ GemmArgs p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __grid_constant__ GemmArgs p) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up;
-  const int warp = threadIdx.x / 32;
+  const int warp = threadIdx.x / 32, rank = (int)pair_rank();
   dep_launch();
   const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u, staging = ring + kStages * kStageBytes;
   const uint32_t full = smem_addr(s_bar), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
@@ -537,7 +552,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(acc_full + 8 * i, 1);
-      bar_init(acc_empty + 8 * i, kFinishWarps);
+      bar_init(acc_empty + 8 * i, 2 * kFinishWarps);  // of both CTAs, at the first's
     }
     bar_init(drain, 1);
     s_gave_up = 0;
@@ -547,6 +562,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
   if (warp == 1) tmem_alloc(smem_addr(&s_tmem), 512);
   tc_fence_before();
   __syncthreads();
+  pair_sync();  // the other CTA's barriers are ready
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   dep_wait();
@@ -555,8 +571,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
   const int items = item_count<P>(p, live, cuts);  // a CTA beyond them passes through
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeedRegs));
-    if (threadIdx.x == 0) produce<P, PLANES>(p, live, cuts, ring, full, empty, &s_gave_up);
-    if (threadIdx.x == 32)
+    if (threadIdx.x == 0) produce<P, PLANES>(p, live, cuts, rank, ring, full, empty, &s_gave_up);
+    if (threadIdx.x == 32 && rank == 0)
       multiply<P, PLANES>(p, live, cuts, ring, full, empty, acc_full, acc_empty, drain, tmem, &s_gave_up);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFinishRegs));
@@ -566,8 +582,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
     Stager out{staging + (warp - 4) * kOutWarpBytes};
     int n = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-      const Item t = item_at<P>(p, live, cuts, i);
+    const uint32_t first_empty = pair_addr(acc_empty, 0);
+    for (int i = blockIdx.x / 2; ok && i < items; i += gridDim.x / 2) {
+      const Item t = item_at<P>(p, live, cuts, rank, i);
       Entries e;
       if (P <= kGradient)  // under the products
         e.seek(p.w, p.g, t.row0 + quarter * 32 + threadIdx.x % 32, live, t.tile * kHeadTile + part * kMine);
@@ -600,7 +617,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
         }
         tc_fence_before();
         __syncwarp();
-        if (threadIdx.x % 32 == 0) bar_arrive(acc_empty + 8 * half);
+        if (threadIdx.x % 32 == 0) bar_arrive_pair(first_empty + 8 * half);
       }
       if (!ok) break;
       if constexpr (P == kDHidden) finish_dhidden<PLANES>(p, t, live, cuts, v, quarter, part, out);
@@ -612,6 +629,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  pair_sync();  // neither CTA's memory is used by the other any more
   if (threadIdx.x == 0 && s_gave_up) atomicOr(&g_head_fault, 2u);
   if (warp == 1) {
     tc_fence_after();
@@ -655,7 +673,7 @@ bool maps_for(GemmArgs* a, int dtype) {
   const int planes = head_planes(dtype);
   const int64_t padded = (int64_t)g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
   bool ok = true;
-  // the weight: boxes of 256 rows by 64 of dim (logits), or of 64 rows by 64 (d_hidden)
+  // the weight: boxes of 128 rows by 64 of dim (logits), or of 64 rows by 64 (d_hidden)
   auto weight = [&](int box_rows) {
     if (w.wpack != nullptr) {
       ok &= matrix_map(&a->b[0], w.wpack, planes * padded, g.dim, w.dim_pad, box_rows);
@@ -681,7 +699,7 @@ bool maps_for(GemmArgs* a, int dtype) {
         if (g.rows[s] > 0) ok &= matrix_map(&a->c[s], a->sh.dw[s], g.rows[s], g.dim, a->sh.dw_ld, 32);
   } else {
     ok &= matrix_map(&a->a, w.hid, grad_rows, g.dim, w.dim_pad, kBM);
-    weight(kBN);
+    weight(kHalf);
     if (P != kStats) ok &= matrix_map(&a->c[0], w.grad, grad_rows, w.grad_ld, w.grad_ld, 32);
   }
   return ok;
@@ -702,7 +720,7 @@ cudaError_t launch(const GemmArgs& a, int64_t items, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     ready_device = dev;
   }
-  const int blocks = (int)std::min<int64_t>(items, sm_count());
+  const int blocks = (int)std::min<int64_t>(2 * items, sm_count() / 2 * 2);
   return launch_chained(head_product_kernel<P, PLANES>, blocks, kGemmThreads, kSmemBytes, s, a);
 }
 
@@ -719,10 +737,10 @@ cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int 
   a.whole = whole;
   a.dh_vec = reinterpret_cast<uintptr_t>(sh.dh) % 16 == 0 && sh.dh_ld * esize_of(dtype) % 16 == 0;
   // row tiles whose packed hidden rows take 64 MiB, half of L2
-  const int64_t mt = g.mpad / kBM, tiles = hi - lo, nd = (g.dim + kBN - 1) / kBN;
-  a.group = (int)std::max<int64_t>(1, std::min<int64_t>(mt, (64ll << 20) / ((int64_t)kBM * w.dim_pad * 2 * head_planes(dtype))));
+  const int64_t mt = g.mpad / kPairM, tiles = hi - lo, nd = (g.dim + kBN - 1) / kBN;
+  a.group = (int)std::max<int64_t>(1, std::min<int64_t>(mt, (64ll << 20) / ((int64_t)kPairM * w.dim_pad * 2 * head_planes(dtype))));
   if (!maps_for<P>(&a, dtype)) return cudaErrorInvalidValue;
-  const int64_t items = P == kDHidden ? mt * nd * w.splits : P == kDWeight ? tiles * 2 * nd : mt * tiles;
+  const int64_t items = P == kDHidden ? mt * nd * w.splits : P == kDWeight ? tiles * nd : mt * tiles;
   if (items > INT_MAX) return cudaErrorInvalidValue;
   return dtype == RELAY_BF16 ? launch<P, 1>(a, items, s) : launch<P, kHeadPlanesF32>(a, items, s);
 }
