@@ -5,8 +5,8 @@
 //             packed too where its rows cannot be read through tensor maps, or are fp32
 //   logits    tile maxima and sums, and the logits at the entries
 //   combine   log-sum-exp and loss of each row
-//   gradient  every piece: gradient of the logits, d_hidden += its product with the weight,
-//             d_weight of the piece's rows = its transposed product with hidden
+//   gradient  every piece: gradient of the logits; then, in one launch, d_hidden += its product with
+//             the weight and d_weight of the piece's rows = its transposed product with hidden
 //
 // When all the logits of the batch make one piece, the first pass keeps their exponentials and
 // the gradient is a scaling of them; otherwise each piece multiplies its logits again.
@@ -124,6 +124,7 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
       w.dh_ld = (int32_t)up(g.dim, 4);
       const int64_t one = 4ll * g.mpad * w.dh_ld;
       w.tiles_per_piece = ar.tiles_per_piece;
+      w.with_dw = dw;
       w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(ar.tiles_per_piece, 64), (256ll << 20) / one));
       w.dh = reinterpret_cast<float*>(l.take(one * w.splits));
     }
@@ -237,16 +238,15 @@ relay_status_t run_head(const relay_head_t& h, HeadGeom g, int top, const int32_
                            h.d_hidden, h.d_hidden_stride, stream));
   if (w.wpack != nullptr) RELAY_HEAD_TRY(head_pack_weight(g, w, sh, h.dtype, stream));
   RELAY_HEAD_TRY(head_logits(g, w, sh, h.dtype, 0, tiles, ar.keep ? kHeadStatsKeep : kHeadStats, stream));
-  RELAY_HEAD_TRY(head_combine(g, w, distill, loss, stream));
+  if (!ar.keep || !head_scale_joins(g)) RELAY_HEAD_TRY(head_combine(g, w, distill, loss, stream));
   if (!dh && !dw) return RELAY_OK;
   for (int t = 0; t < tiles; t += ar.tiles_per_piece) {
     const int hi = std::min(tiles, t + ar.tiles_per_piece);
     if (ar.keep)
-      RELAY_HEAD_TRY(head_scale(g, w, h.dtype, stream));
+      RELAY_HEAD_TRY(head_scale(g, w, h.dtype, distill, loss, stream));
     else
       RELAY_HEAD_TRY(head_logits(g, w, sh, h.dtype, t, hi, kHeadGradient, stream));
-    if (dh) RELAY_HEAD_TRY(head_dhidden(g, w, sh, h.dtype, t, hi, t == 0, ar.keep, stream));
-    if (dw) RELAY_HEAD_TRY(head_dweight(g, w, sh, h.dtype, t, hi, stream));
+    RELAY_HEAD_TRY(head_back(g, w, sh, h.dtype, t, hi, t == 0, ar.keep, dh, dw, stream));
   }
   if (dh) RELAY_HEAD_TRY(head_write_dh(g, w, h.dtype, ar.keep, h.d_hidden, h.d_hidden_stride, stream));
   return RELAY_OK;

@@ -89,27 +89,41 @@ struct HeadWork {
   int32_t dh_ld;      // dim rounded up to 4
   int32_t splits;     // most cuts of the vocabulary d_hidden may take
   int32_t tiles_per_piece;
+  int32_t with_dw;    // d_weight's tiles run beside d_hidden's
 };
 
-// Cuts of the vocabulary for d_hidden, whose tiles alone are too few, or too few in the last
-// round, to fill the GPU. Costs are in inner steps of one tile (64 columns, about 0.27 us): the
-// rounds of the GPU's pairs of SMs times the steps of a cut, plus writing and reading a cut's fp32 partial
-// sums (8 bytes a value; a step's time moves about 1.8 MB). The live rows are known on
-// the device only, so kernels call this themselves and agree.
+// Cuts of the vocabulary for d_hidden, whose tiles alone are too few, or too long beside what else
+// runs, to fill the GPU evenly. Costs are in inner steps of one tile (64 columns, about 0.27 us):
+// the rounds of the GPU's pairs of SMs over d_hidden's tiles, or all the work spread evenly plus the
+// longest tile at its end, whichever is more; plus writing and reading a cut's fp32 partial sums (8 bytes
+// a value; a step's time moves about 1.8 MB). The live rows are known on the device only, so
+// kernels call this themselves and agree.
 #ifdef __CUDACC__
-__device__ __forceinline__ int head_cuts(const HeadGeom& g, int live, int tiles, int most) {
-  // whole warps call it: a lane prices two numbers of cuts (most is at most 64)
-  const int64_t items = (int64_t)((live + kHeadRowTile - 1) / kHeadRowTile) * ((g.dim + kHeadTile - 1) / kHeadTile);
-  const int pairs = g.sms / 2;
-  if (most == 1 || items >= 4 * pairs) return 1;
+constexpr int kHeadOpenSteps = 8;  // steps a tile costs besides its own
+__device__ __forceinline__ int head_long_steps(int tiles, int cuts) {  // a tile of d_hidden
+  return (int)(((uint32_t)tiles * 4 + cuts - 1) / cuts) + kHeadOpenSteps;
+}
+__device__ __forceinline__ int head_short_steps(int live) { return (live + 63) / 64 + kHeadOpenSteps; }  // of d_weight
+__device__ __forceinline__ int head_cuts(const HeadGeom& g, const HeadWork& w, int live) {
+  // whole warps call it: a lane prices two numbers of cuts (there are at most 64)
+  const int pairs = g.sms / 2, nd = (g.dim + kHeadTile - 1) / kHeadTile;
+  const int64_t items = (int64_t)((live + kHeadRowTile - 1) / kHeadRowTile) * nd;
+  if (w.splits == 1 || items >= 4 * pairs) return 1;
   const int64_t move = 1 + (int64_t)live * g.dim / 225000;
+  const int dw_steps = w.with_dw ? head_short_steps(live) : 0;
+  const int64_t dw_work = (int64_t)w.tiles_per_piece * nd * dw_steps;
   uint32_t least = ~0u;
   int best = 1;
   for (int i = 0; i < 2; ++i) {
     const int s = 1 + threadIdx.x % 32 + 32 * i;
-    if (s > most) continue;
-    const uint32_t rounds = ((uint32_t)items * s + pairs - 1) / pairs;
-    const int64_t cost = (int64_t)rounds * (((uint32_t)tiles * 4 + s - 1) / s + 8) + (s > 1 ? s * move : 0);
+    if (s > w.splits) continue;
+    const int steps = head_long_steps(w.tiles_per_piece, s);
+    const int64_t rounds = (int64_t)(((uint32_t)items * s + pairs - 1) / pairs) * steps;
+    // (in float: a few parts in 10^7 decide nothing, and every lane of every kernel gets the same)
+    const int64_t spread = (int64_t)((float)((int64_t)((uint32_t)items * s) * steps + dw_work) / (float)pairs) +
+                           (w.with_dw ? dw_steps : steps);
+    int64_t cost = rounds > spread ? rounds : spread;
+    if (s > 1) cost += s * move;
     const uint32_t c = cost < 0xfffffffell ? (uint32_t)cost : 0xfffffffeu;
     if (c < least) {
       least = c;
@@ -140,7 +154,10 @@ cudaError_t head_pack_weight(const HeadGeom& g, const HeadWork& w, const HeadSha
                              cudaStream_t s);
 cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, float* loss,
                          cudaStream_t s);
-cudaError_t head_scale(const HeadGeom& g, const HeadWork& w, int dtype, cudaStream_t s);
+// Kept exponentials to the gradient. Where a row is short (head_scale_joins) it does head_combine's work
+// as well: one launch less.
+bool head_scale_joins(const HeadGeom& g);
+cudaError_t head_scale(const HeadGeom& g, const HeadWork& w, int dtype, bool distill, float* loss, cudaStream_t s);
 cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, bool whole, void* d_hidden,
                           int64_t d_hidden_ld, cudaStream_t s);
 
@@ -148,10 +165,9 @@ cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, bool 
 enum HeadLogits { kHeadStats, kHeadStatsKeep, kHeadGradient };
 cudaError_t head_logits(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
                         int tile_lo, int tile_hi, HeadLogits mode, cudaStream_t s);
-cudaError_t head_dhidden(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
-                         int tile_lo, int tile_hi, bool first, bool whole, cudaStream_t s);
-cudaError_t head_dweight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
-                         int tile_lo, int tile_hi, cudaStream_t s);
+// d_hidden and d_weight of one piece, either or both. first: the first piece; whole: the only one.
+cudaError_t head_back(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo, int tile_hi,
+                      bool first, bool whole, bool dh, bool dw, cudaStream_t s);
 // Reads and clears the products' fault word.
 cudaError_t head_read_fault(unsigned* fault);
 

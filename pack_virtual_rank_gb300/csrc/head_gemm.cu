@@ -4,6 +4,9 @@
 //   d_hidden   g . weight                 rows x dim, inner dimension the piece's columns
 //   d_weight   g^T . hidden               columns x dim, inner dimension the live rows
 //
+// The last two are one launch: they read the same gradient, neither needs the other, and the tiles of
+// one fill the SMs that the last tiles of the other leave idle.
+//
 // A pair of CTAs, one per SM, walks 256 x 256 tiles of the result; each holds 128 rows of it. A
 // producer thread in each brings its half of both operands, 64 elements of the inner dimension at a
 // time, into a ring of shared memory stages (tensor map loads, 128-byte swizzle); one thread of the
@@ -55,7 +58,7 @@ static_assert(kFeedRegs + 2 * kFinishRegs == 3 * kLaunchRegs, "the groups' regis
 constexpr int kMine = kBN / 2;                         // columns of a tile's row one thread finishes
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum Product { kStats, kStatsKeep, kGradient, kDHidden, kDWeight };
+enum Product { kStats, kStatsKeep, kGradient, kBack };
 
 // Inner steps (of 64) summed in tensor memory before the sum moves on into registers. The tensor
 // cores cut what does not fit 24 bits at every product instead of rounding it, which drifts with
@@ -63,16 +66,19 @@ enum Product { kStats, kStatsKeep, kGradient, kDHidden, kDWeight };
 // 64-bit value as an fp32 sum. Chains of 32 products (48 for the six products of fp32 parts)
 // are as close as that sum. A result that is rounded to bf16 does not show the drift.
 template <int P, int PLANES>
-constexpr int kChain = PLANES > 1 ? 2 : P == kDHidden || P == kDWeight ? INT_MAX : 8;
+constexpr int kChain = PLANES > 1 ? 2 : P == kBack ? INT_MAX : 8;
 
 struct GemmArgs {
-  CUtensorMap a;
-  CUtensorMap b[RELAY_HEAD_MAX_SHARDS];
-  CUtensorMap c[RELAY_HEAD_MAX_SHARDS];
+  CUtensorMap a;                         // first operand: hidden (logits), gradient
+  CUtensorMap b[RELAY_HEAD_MAX_SHARDS];  // weight shards, or the packed weight
+  CUtensorMap hid;                       // hidden as d_weight's second operand
+  CUtensorMap c[RELAY_HEAD_MAX_SHARDS];  // results: gradient or codes (logits), d_weight
+  CUtensorMap dh;                        // d_hidden's partial sums
   HeadGeom g;
   HeadWork w;
   HeadShards sh;
   int32_t tile_lo, tile_hi;
+  int32_t want_dh, want_dw;
   int32_t first;     // d_hidden: overwrite the partial sums
   int32_t whole;     // d_hidden: the only piece; an uncut sum goes straight to its row
   int32_t dh_vec;    // d_hidden's rows take 16-byte stores
@@ -86,38 +92,82 @@ struct Item {
   int tile, shard, v0;     // padded column tile, its shard, the shard's weight row it starts at
   int k_lo, k_hi;          // inner steps of 64 (d_hidden: column tiles)
   int split;
+  bool weight;             // kBack: a tile of d_weight
 };
 
-// cuts: head_cuts (d_hidden).
+// Which tiles a pair of CTAs takes, in order. Tiles of one cost go round the pairs. kBack has two
+// kinds: d_hidden's long tiles go round first, and the pairs left out in the last round take as
+// many of d_weight's as that round lasts before the rest goes round all.
+struct Schedule {
+  int cuts;                // head_cuts
+  int pairs, mine;         // pairs of CTAs, and which this is
+  int long_items, items;   // d_hidden's, all
+  int late, lead, led;     // first pair without a last long tile; tiles each such pair takes ahead; their sum
+  __device__ __forceinline__ int at(int slot) const {
+    int i = mine + slot * pairs;
+    if (i < long_items) return i;
+    slot -= (long_items - mine + pairs - 1) / pairs * (mine < long_items);
+    if (mine >= late) {
+      if (slot < lead) {
+        i = long_items + slot * (pairs - late) + mine - late;
+        return i < long_items + led ? i : -1;
+      }
+      slot -= lead;
+    }
+    i = long_items + led + slot * pairs + mine;
+    return i < items ? i : -1;
+  }
+};
+
 template <int P>
-__device__ __forceinline__ int item_count(const GemmArgs& p, int live, int cuts) {
+__device__ __forceinline__ Schedule schedule(const GemmArgs& p, int live) {
   const int mt = (live + kPairM - 1) / kPairM, tiles = p.tile_hi - p.tile_lo;
   const int nd = (p.g.dim + kBN - 1) / kBN;
-  if (P == kDHidden) return mt * nd * cuts;
-  if (P == kDWeight) return tiles * nd;
-  return mt * tiles;
+  Schedule s{};
+  s.cuts = 1;
+  s.pairs = gridDim.x / 2;
+  s.mine = blockIdx.x / 2;
+  if (P != kBack) {
+    s.items = mt * tiles;
+    return s;
+  }
+  const int short_items = p.want_dw ? tiles * nd : 0;
+  if (p.want_dh) {
+    s.cuts = head_cuts(p.g, p.w, live);
+    s.long_items = mt * nd * s.cuts;
+  }
+  s.items = s.long_items + short_items;
+  s.late = s.long_items % s.pairs;
+  if (s.late > 0) {
+    s.lead = min(head_long_steps(tiles, s.cuts) / head_short_steps(live), short_items / (s.pairs - s.late));
+    s.led = s.lead * (s.pairs - s.late);
+  }
+  return s;
 }
 
 template <int P>
-__device__ __forceinline__ Item item_at(const GemmArgs& p, int live, int cuts, int rank, int i) {
+__device__ __forceinline__ Item item_at(const GemmArgs& p, const Schedule& sched, int live, int rank, int i) {
   const int mt = (live + kPairM - 1) / kPairM, tiles = p.tile_hi - p.tile_lo;
   const int nd = (p.g.dim + kBN - 1) / kBN;
   Item t{};
-  if (P == kDHidden) {
-    // every column tile of a row tile runs side by side: the gradient's rows are read once
+  if (P == kBack) {
+    t.weight = i >= sched.long_items;
+    if (t.weight) i -= sched.long_items;
+    // the tiles of dim side by side: a piece of the gradient is read once
     t.col0 = i % nd * kBN;
     i /= nd;
-    t.split = i % cuts;
-    t.row0 = i / cuts * kPairM + rank * kBM;
-    t.k_lo = p.tile_lo + (int)((int64_t)tiles * t.split / cuts);
-    t.k_hi = p.tile_lo + (int)((int64_t)tiles * (t.split + 1) / cuts);
-  } else if (P == kDWeight) {
-    t.col0 = i % nd * kBN;
-    t.tile = p.tile_lo + i / nd;
-    t.shard = head_shard_of_tile(p.g, t.tile);
-    t.v0 = (t.tile - p.g.tile0[t.shard]) * kHeadTile + rank * kBM;
-    t.row0 = (t.tile - p.tile_lo) * kHeadTile + rank * kBM;
-    t.k_hi = (live + kBK - 1) / kBK;
+    if (t.weight) {
+      t.tile = p.tile_lo + i;
+      t.shard = head_shard_of_tile(p.g, t.tile);
+      t.v0 = (t.tile - p.g.tile0[t.shard]) * kHeadTile + rank * kBM;
+      t.row0 = (t.tile - p.tile_lo) * kHeadTile + rank * kBM;
+      t.k_hi = (live + kBK - 1) / kBK;
+    } else {
+      t.split = i % sched.cuts;
+      t.row0 = i / sched.cuts * kPairM + rank * kBM;
+      t.k_lo = p.tile_lo + (int)((int64_t)tiles * t.split / sched.cuts);
+      t.k_hi = p.tile_lo + (int)((int64_t)tiles * (t.split + 1) / sched.cuts);
+    }
   } else {
     const int per = p.group * tiles, band = i / per, in_band = i % per;
     const int width = min(p.group, mt - band * p.group);
@@ -134,11 +184,11 @@ __device__ __forceinline__ Item item_at(const GemmArgs& p, int live, int cuts, i
 // Inner steps of a tile, one call of f(step) each.
 template <int P, class F>
 __device__ __forceinline__ bool for_steps(const GemmArgs& p, const Item& t, F f) {
-  if constexpr (P != kDHidden) {
+  if (P != kBack || t.weight) {
     for (int k = t.k_lo; k < t.k_hi; ++k)
       if (!f(k, 0, 0)) return false;
     return true;
-  } else {
+  }
   for (int tile = t.k_lo; tile < t.k_hi; ++tile) {
     const int shard = head_shard_of_tile(p.g, tile), v0 = (tile - p.g.tile0[shard]) * kHeadTile;
     for (int k = 0; k < kHeadTile / kBK; ++k) {
@@ -147,7 +197,6 @@ __device__ __forceinline__ bool for_steps(const GemmArgs& p, const Item& t, F f)
     }
   }
   return true;
-  }
 }
 
 // Pairs of parts whose products make up an fp32 product.
@@ -158,17 +207,16 @@ __device__ __forceinline__ int pair_b(int i) { return (0x021010 >> (4 * (5 - i))
 
 // full: the stage barriers of the pair's first CTA; empty: this CTA's own.
 template <int P, int PLANES>
-__device__ void produce(const GemmArgs& p, int live, int cuts, int rank, uint32_t ring, uint32_t full, uint32_t empty,
+__device__ void produce(const GemmArgs& p, const Schedule& sched, int live, int rank, uint32_t ring, uint32_t full, uint32_t empty,
                         volatile int* gave_up) {
   const uint32_t pair_full = pair_addr(full, 0);
   const int half = rank * kHalf;
   int stage = 0;
   uint32_t phase = 0;
   int64_t issued = 0;
-  const int items = item_count<P>(p, live, cuts);
   bool ok = true;
-  for (int i = blockIdx.x / 2; ok && i < items; i += gridDim.x / 2) {
-    const Item t = item_at<P>(p, live, cuts, rank, i);
+  for (int slot = 0, i; ok && (i = sched.at(slot)) >= 0; ++slot) {
+    const Item t = item_at<P>(p, sched, live, rank, i);
     ok = for_steps<P>(p, t, [&](int k, int k_shard, int k_v) {
       for (int pair = 0; pair < kPairs<PLANES>; ++pair) {
         const int pa = PLANES == 1 ? 0 : pair_a(pair), pb = PLANES == 1 ? 0 : pair_b(pair);
@@ -177,17 +225,18 @@ __device__ void produce(const GemmArgs& p, int live, int cuts, int rank, uint32_
         if (rank == 0) bar_expect(full + 8 * stage, 2 * kStageBytes);
         ++issued;
         const int wrow = pb * p.g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;  // plane of a packed weight
-        if (P == kDHidden) {
-          map_load(sa, &p.a, k * kBK, pa * p.g.mpad + t.row0, bar);
+        if (P == kBack && t.weight) {
+          for (int j = 0; j < kBM / 64; ++j)
+            map_load(sa + j * 8192, &p.a, t.row0 + 64 * j, pa * p.g.mpad + k * kBK, bar);
+          for (int j = 0; j < kHalf / 64; ++j)
+            map_load(sb + j * 8192, &p.hid, t.col0 + half + 64 * j, pb * p.g.mpad + k * kBK, bar);
+        } else if (P == kBack) {
+          for (int j = 0; j < kBM / 64; ++j)
+            map_load(sa + j * 8192, &p.a, k * kBK, pa * p.g.mpad + t.row0 + 64 * j, bar);
           const bool packed = p.w.wpack != nullptr;
           const CUtensorMap* m = &p.b[packed ? 0 : k_shard];
           const int y = packed ? wrow + p.g.tile0[k_shard] * kHeadTile + k_v : k_v;
           for (int j = 0; j < kHalf / 64; ++j) map_load(sb + j * 8192, m, t.col0 + half + 64 * j, y, bar);
-        } else if (P == kDWeight) {
-          for (int j = 0; j < kBM / 64; ++j)
-            map_load(sa + j * 8192, &p.a, t.row0 + 64 * j, pa * p.g.mpad + k * kBK, bar);
-          for (int j = 0; j < kHalf / 64; ++j)
-            map_load(sb + j * 8192, &p.b[0], t.col0 + half + 64 * j, pb * p.g.mpad + k * kBK, bar);
         } else {
           map_load(sa, &p.a, k * kBK, pa * p.g.mpad + t.row0, bar);
           if (p.w.wpack != nullptr)
@@ -222,17 +271,17 @@ __device__ void produce(const GemmArgs& p, int live, int cuts, int rank, uint32_
 }
 
 template <int P, int PLANES>
-__device__ void multiply(const GemmArgs& p, int live, int cuts, uint32_t ring, uint32_t full, uint32_t empty,
+__device__ void multiply(const GemmArgs& p, const Schedule& sched, int live, uint32_t ring, uint32_t full, uint32_t empty,
                          uint32_t acc_full, uint32_t acc_empty, uint32_t drain, uint32_t tmem,
                          volatile int* gave_up) {
-  constexpr bool kAOuter = P == kDWeight, kBOuter = P == kDWeight || P == kDHidden;
-  constexpr uint32_t kDesc = product_desc(kPairM, kBN, kAOuter, kBOuter);
+  constexpr bool kBOuter = P == kBack;
   int stage = 0, n = 0;
   uint32_t phase = 0;
-  const int items = item_count<P>(p, live, cuts);
   bool ok = true;
-  for (int i = blockIdx.x / 2; ok && i < items; i += gridDim.x / 2) {
-    const Item t = item_at<P>(p, live, cuts, 0, i);
+  for (int slot = 0, i; ok && (i = sched.at(slot)) >= 0; ++slot) {
+    const Item t = item_at<P>(p, sched, live, 0, i);
+    const bool a_outer = P == kBack && t.weight;
+    const uint32_t desc = a_outer ? product_desc(kPairM, kBN, true, kBOuter) : product_desc(kPairM, kBN, false, kBOuter);
     int in_chain = 0;
     auto open = [&] {
       const bool free = bar_wait(acc_empty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, gave_up);
@@ -252,10 +301,10 @@ __device__ void multiply(const GemmArgs& p, int live, int cuts, uint32_t ring, u
         if (!bar_wait(full + 8 * stage, phase, gave_up)) return false;
         tc_fence_after();
         const uint32_t sa = ring + stage * kStageBytes;
-        const uint64_t da = operand_desc(sa, kAOuter), db = operand_desc(sa + kABytes, kBOuter);
+        const uint64_t da = operand_desc(sa, a_outer), db = operand_desc(sa + kABytes, kBOuter);
 #pragma unroll
         for (int k = 0; k < kBK / 16; ++k)
-          tc_product(acc, da + k * operand_step(kAOuter), db + k * operand_step(kBOuter), kDesc,
+          tc_product(acc, da + k * operand_step(a_outer), db + k * operand_step(kBOuter), desc,
                      in_chain > 0 || pair > 0 || k > 0);
         tc_commit(empty + 8 * stage);
         if (++stage == kStages) {
@@ -463,7 +512,7 @@ __device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t,
       for (int j = 0; j < 8; ++j)
         out.put(j, __float_as_uint(v[c + 4 * j]), __float_as_uint(v[c + 4 * j + 1]), __float_as_uint(v[c + 4 * j + 2]),
                 __float_as_uint(v[c + 4 * j + 3]));
-      out.close(&p.c[0], d0 + c, t.split * p.g.mpad + r0, !p.first);
+      out.close(&p.dh, d0 + c, t.split * p.g.mpad + r0, !p.first);
     }
     return;
   }
@@ -567,13 +616,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) hea
   const uint32_t tmem = s_tmem;
   dep_wait();
   const int live = *p.w.n_live;
-  const int cuts = P == kDHidden ? head_cuts(p.g, live, p.w.tiles_per_piece, p.w.splits) : 1;
-  const int items = item_count<P>(p, live, cuts);  // a CTA beyond them passes through
+  const Schedule sched = schedule<P>(p, live);  // a pair without a tile passes through
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeedRegs));
-    if (threadIdx.x == 0) produce<P, PLANES>(p, live, cuts, rank, ring, full, empty, &s_gave_up);
+    if (threadIdx.x == 0) produce<P, PLANES>(p, sched, live, rank, ring, full, empty, &s_gave_up);
     if (threadIdx.x == 32 && rank == 0)
-      multiply<P, PLANES>(p, live, cuts, ring, full, empty, acc_full, acc_empty, drain, tmem, &s_gave_up);
+      multiply<P, PLANES>(p, sched, live, ring, full, empty, acc_full, acc_empty, drain, tmem, &s_gave_up);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFinishRegs));
     // warps 4 to 7 finish a tile's first 128 columns, 8 to 11 its last; a warp reads the quarter of
@@ -583,8 +631,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) hea
     int n = 0;
     bool ok = true;
     const uint32_t first_empty = pair_addr(acc_empty, 0);
-    for (int i = blockIdx.x / 2; ok && i < items; i += gridDim.x / 2) {
-      const Item t = item_at<P>(p, live, cuts, rank, i);
+    for (int slot = 0, i; ok && (i = sched.at(slot)) >= 0; ++slot) {
+      const Item t = item_at<P>(p, sched, live, rank, i);
       Entries e;
       if (P <= kGradient)  // under the products
         e.seek(p.w, p.g, t.row0 + quarter * 32 + threadIdx.x % 32, live, t.tile * kHeadTile + part * kMine);
@@ -620,9 +668,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) hea
         if (threadIdx.x % 32 == 0) bar_arrive_pair(first_empty + 8 * half);
       }
       if (!ok) break;
-      if constexpr (P == kDHidden) finish_dhidden<PLANES>(p, t, live, cuts, v, quarter, part, out);
-      else if constexpr (P == kDWeight) finish_dweight<PLANES>(p, t, v, quarter, part, out);
-      else finish_logits<P, PLANES>(p, t, live, v, quarter, part, e, out);
+      if constexpr (P == kBack) {
+        if (t.weight) finish_dweight<PLANES>(p, t, v, quarter, part, out);
+        else finish_dhidden<PLANES>(p, t, live, sched.cuts, v, quarter, part, out);
+      } else finish_logits<P, PLANES>(p, t, live, v, quarter, part, e, out);
     }
     if (threadIdx.x % 32 == 0) store_wait_all();
   }
@@ -683,20 +732,22 @@ bool maps_for(GemmArgs* a, int dtype) {
     }
   };
   const int64_t grad_rows = (int64_t)planes * g.mpad;
-  if (P == kDHidden) {
-    ok &= matrix_map(&a->a, w.grad, grad_rows, w.grad_ld, w.grad_ld, kBM);
-    weight(kBK);
-    ok &= matrix_map(&a->c[0], w.dh, (int64_t)w.splits * g.mpad, g.dim, w.dh_ld, 32, true);
-  } else if (P == kDWeight) {
+  if (P == kBack) {
     ok &= matrix_map(&a->a, w.grad, grad_rows, w.grad_ld, w.grad_ld, kBK);
-    ok &= matrix_map(&a->b[0], w.hid, grad_rows, g.dim, w.dim_pad, kBK);
-    a->out_map = 1;
-    for (int s = 0; s < g.A; ++s)
-      if (g.rows[s] > 0)
-        a->out_map &= reinterpret_cast<uintptr_t>(a->sh.dw[s]) % 16 == 0 && a->sh.dw_ld * esize_of(dtype) % 16 == 0;
-    if (planes == 1 && a->out_map)
+    if (a->want_dh) {
+      weight(kBK);
+      ok &= matrix_map(&a->dh, w.dh, (int64_t)w.splits * g.mpad, g.dim, w.dh_ld, 32, true);
+    }
+    if (a->want_dw) {
+      ok &= matrix_map(&a->hid, w.hid, grad_rows, g.dim, w.dim_pad, kBK);
+      a->out_map = 1;
       for (int s = 0; s < g.A; ++s)
-        if (g.rows[s] > 0) ok &= matrix_map(&a->c[s], a->sh.dw[s], g.rows[s], g.dim, a->sh.dw_ld, 32);
+        if (g.rows[s] > 0)
+          a->out_map &= reinterpret_cast<uintptr_t>(a->sh.dw[s]) % 16 == 0 && a->sh.dw_ld * esize_of(dtype) % 16 == 0;
+      if (planes == 1 && a->out_map)
+        for (int s = 0; s < g.A; ++s)
+          if (g.rows[s] > 0) ok &= matrix_map(&a->c[s], a->sh.dw[s], g.rows[s], g.dim, a->sh.dw_ld, 32);
+    }
   } else {
     ok &= matrix_map(&a->a, w.hid, grad_rows, g.dim, w.dim_pad, kBM);
     weight(kHalf);
@@ -726,7 +777,7 @@ cudaError_t launch(const GemmArgs& a, int64_t items, cudaStream_t s) {
 
 template <int P>
 cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int lo, int hi, bool first,
-                bool whole, cudaStream_t s) {
+                bool whole, bool dh, bool dw, cudaStream_t s) {
   GemmArgs a{};
   a.g = g;
   a.w = w;
@@ -735,12 +786,14 @@ cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int 
   a.tile_hi = hi;
   a.first = first;
   a.whole = whole;
+  a.want_dh = dh;
+  a.want_dw = dw;
   a.dh_vec = reinterpret_cast<uintptr_t>(sh.dh) % 16 == 0 && sh.dh_ld * esize_of(dtype) % 16 == 0;
   // row tiles whose packed hidden rows take 64 MiB, half of L2
   const int64_t mt = g.mpad / kPairM, tiles = hi - lo, nd = (g.dim + kBN - 1) / kBN;
   a.group = (int)std::max<int64_t>(1, std::min<int64_t>(mt, (64ll << 20) / ((int64_t)kPairM * w.dim_pad * 2 * head_planes(dtype))));
   if (!maps_for<P>(&a, dtype)) return cudaErrorInvalidValue;
-  const int64_t items = P == kDHidden ? mt * nd * w.splits : P == kDWeight ? tiles * nd : mt * tiles;
+  const int64_t items = P == kBack ? (dh ? mt * nd * w.splits : 0) + (dw ? tiles * nd : 0) : mt * tiles;
   if (items > INT_MAX) return cudaErrorInvalidValue;
   return dtype == RELAY_BF16 ? launch<P, 1>(a, items, s) : launch<P, kHeadPlanesF32>(a, items, s);
 }
@@ -750,20 +803,15 @@ cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int 
 cudaError_t head_logits(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo,
                         int tile_hi, HeadLogits mode, cudaStream_t s) {
   switch (mode) {
-    case kHeadStats: return run<kStats>(g, w, sh, dtype, tile_lo, tile_hi, false, false, s);
-    case kHeadStatsKeep: return run<kStatsKeep>(g, w, sh, dtype, tile_lo, tile_hi, false, false, s);
-    default: return run<kGradient>(g, w, sh, dtype, tile_lo, tile_hi, false, false, s);
+    case kHeadStats: return run<kStats>(g, w, sh, dtype, tile_lo, tile_hi, false, false, false, false, s);
+    case kHeadStatsKeep: return run<kStatsKeep>(g, w, sh, dtype, tile_lo, tile_hi, false, false, false, false, s);
+    default: return run<kGradient>(g, w, sh, dtype, tile_lo, tile_hi, false, false, false, false, s);
   }
 }
 
-cudaError_t head_dhidden(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo,
-                         int tile_hi, bool first, bool whole, cudaStream_t s) {
-  return run<kDHidden>(g, w, sh, dtype, tile_lo, tile_hi, first, whole, s);
-}
-
-cudaError_t head_dweight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo,
-                         int tile_hi, cudaStream_t s) {
-  return run<kDWeight>(g, w, sh, dtype, tile_lo, tile_hi, false, false, s);
+cudaError_t head_back(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo, int tile_hi,
+                      bool first, bool whole, bool dh, bool dw, cudaStream_t s) {
+  return run<kBack>(g, w, sh, dtype, tile_lo, tile_hi, first, whole, dh, dw, s);
 }
 
 cudaError_t head_read_fault(unsigned* fault) {

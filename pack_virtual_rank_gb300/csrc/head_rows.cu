@@ -272,9 +272,41 @@ __device__ __forceinline__ void join(float& m, float& s, float pm, float ps) {
   s = (m > -INFINITY || s != s ? s * exp2f(m - top) : 0.0f) + (pm > -INFINITY || ps != ps ? ps * exp2f(pm - top) : 0.0f);
   m = top;
 }
+// Joins the lanes' shares; every lane gets the row's log-sum-exp in log2 units.
+__device__ __forceinline__ float join_warp(float m, float s) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float pm = __shfl_xor_sync(~0u, m, o), ps = __shfl_xor_sync(~0u, s, o);
+    // both sides of a pair join in the same order: the lower lane's share first
+    float am = lane & o ? pm : m, as = lane & o ? ps : s;
+    join(am, as, lane & o ? m : pm, lane & o ? s : ps);
+    m = am;
+    s = as;
+  }
+  return m + log2f(s);
+}
+// The loss of a packed row, by one warp.
+template <bool DISTILL>
+__device__ __forceinline__ void row_loss(const HeadGeom& g, const HeadWork& w, int row, float lse2, float* loss) {
+  const int lane = threadIdx.x % 32, r = w.perm[row];
+  const float lse = lse2 * 0.6931471805599453f;
+  const int64_t at = (int64_t)r * g.top;
+  if (!DISTILL) {
+    if (lane == 0) loss[r] = lse - w.ent_z[at];
+    return;
+  }
+  float sum = 0.0f;
+  for (int k = lane; k < g.top; k += 32) {
+    const float q = w.ent_q[at + k];
+    if (w.ent_col[at + k] != INT_MAX && q != 0.0f) sum += q * (logf(q) - (w.ent_z[at + k] - lse));  // 0 log 0 = 0
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) loss[r] = g.tau * g.tau * sum;
+}
 template <bool DISTILL>
 __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const HeadGeom g, const HeadWork w, float* loss) {
-  __shared__ float s_max[kCombineWarps][32], s_sum[kCombineWarps][32];
+  __shared__ float s_max[kCombineWarps][33], s_sum[kCombineWarps][33];
   dep_launch();
   dep_wait();
   const int live = *w.n_live, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -297,32 +329,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const HeadG
   // warp i takes row i: lanes are the warps' shares
   const int mine = blockIdx.x * 32 + warp;
   if (mine >= live) return;
-  m = s_max[lane][warp];
-  s = s_sum[lane][warp];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float pm = __shfl_xor_sync(~0u, m, o), ps = __shfl_xor_sync(~0u, s, o);
-    // both sides of a pair join in the same order: the lower lane's share first
-    float am = lane & o ? pm : m, as = lane & o ? ps : s;
-    join(am, as, lane & o ? m : pm, lane & o ? s : ps);
-    m = am;
-    s = as;
-  }
-  const float lse2 = m + log2f(s), lse = lse2 * 0.6931471805599453f;
-  const int r = w.perm[mine];
-  const int64_t at = (int64_t)r * g.top;
+  const float lse2 = join_warp(s_max[lane][warp], s_sum[lane][warp]);
   if (lane == 0) w.lse[mine] = lse2;
-  if (!DISTILL) {
-    if (lane == 0) loss[r] = lse - w.ent_z[at];
-    return;
-  }
-  float sum = 0.0f;
-  for (int k = lane; k < g.top; k += 32) {
-    const float q = w.ent_q[at + k];
-    if (w.ent_col[at + k] != INT_MAX && q != 0.0f) sum += q * (logf(q) - (w.ent_z[at + k] - lse));  // 0 log 0 = 0
-  }
-  sum = warp_sum(sum);
-  if (lane == 0) loss[r] = g.tau * g.tau * sum;
+  row_loss<DISTILL>(g, w, mine, lse2, loss);
 }
 
 // Kept exponentials to the gradient of the logits, in place: each is relative to the maximum of
@@ -332,8 +341,11 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const HeadG
 // live ones, as far as products read them, become 0.
 constexpr int kScaleVecs = 4;  // 16-byte vectors in flight per thread and plane
 constexpr int kScaleCols = kThreadsRows * 8 * kScaleVecs;
-template <int PLANES>
-__global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, const HeadWork w) {
+// JOIN 1 (cross entropy), 2 (distillation): the block has the whole row, and does combine_kernel's
+// work for it first.
+template <int PLANES, int JOIN>
+__global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, const HeadWork w, float* loss) {
+  __shared__ float s_lse;
   dep_launch();
   dep_wait();
   const int live = *w.n_live, row = blockIdx.x;
@@ -343,7 +355,8 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
   const int64_t plane = (int64_t)g.mpad * w.grad_ld;
   uint16_t* line = w.grad + (int64_t)row * w.grad_ld;
   const bool on = row < live;
-  const float lse = on ? w.lse[row] : 0.0f, weight = on ? w.wrow[row] : 0.0f;
+  const float weight = on ? w.wrow[row] : 0.0f;
+  float lse = on && JOIN == 0 ? w.lse[row] : 0.0f;
   uint4 in[kScaleVecs][PLANES];
   float ref[kScaleVecs];
 #pragma unroll
@@ -352,8 +365,24 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
     if (col >= cols || !on) continue;
 #pragma unroll
     for (int i = 0; i < PLANES; ++i) in[k][i] = ld_once(line + i * plane + col);
-    ref[k] = w.part[(int64_t)(col / kHeadStatTile) * g.mpad + row].x - lse;
+    ref[k] = w.part[(int64_t)(col / kHeadStatTile) * g.mpad + row].x;
   }
+  if (JOIN != 0 && on) {
+    if (threadIdx.x < 32) {
+      float m = -INFINITY, s = 0.0f;
+      for (int t = threadIdx.x; t < cols / kHeadStatTile; t += 32) {
+        const float2 p = w.part[(int64_t)t * g.mpad + row];
+        join(m, s, p.x, p.y);
+      }
+      const float lse2 = join_warp(m, s);
+      row_loss<JOIN == 2>(g, w, row, lse2, loss);
+      if (threadIdx.x == 0) s_lse = lse2;
+    }
+    __syncthreads();
+    lse = s_lse;
+  }
+#pragma unroll
+  for (int k = 0; k < kScaleVecs; ++k) ref[k] -= lse;
 #pragma unroll
   for (int k = 0; k < kScaleVecs; ++k) {
     const int col = col0 + (k * kThreadsRows + threadIdx.x) * 8;
@@ -417,7 +446,7 @@ __global__ void __launch_bounds__(kThreadsRows)
     write_dh_kernel(const HeadGeom g, const HeadWork w, T* dh, int64_t ld, int whole, int vec) {
   dep_launch();
   dep_wait();
-  const int live = *w.n_live, cuts = head_cuts(g, live, w.tiles_per_piece, w.splits);
+  const int live = *w.n_live, cuts = head_cuts(g, w, live);
   if (whole && cuts == 1) return;
   const int64_t cut = (int64_t)g.mpad * w.dh_ld;
   constexpr int kLanes = 4;
@@ -500,11 +529,16 @@ cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, flo
                         32 * kCombineWarps, 0, s, g, w, loss);
 }
 
-cudaError_t head_scale(const HeadGeom& g, const HeadWork& w, int dtype, cudaStream_t s) {
-  const int cols = g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
-  const dim3 grid(g.mpad, ceil_div(cols, kScaleCols));  // few column blocks: a piece is bounded
-  return launch_chained(dtype == RELAY_BF16 ? scale_kernel<1> : scale_kernel<kHeadPlanesF32>, grid, kThreadsRows, 0, s,
-                        g, w);
+bool head_scale_joins(const HeadGeom& g) { return g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile <= kScaleCols; }
+
+template <int PLANES>
+static cudaError_t scale_typed(const HeadGeom& g, const HeadWork& w, bool distill, float* loss, cudaStream_t s) {
+  const dim3 grid(g.mpad, ceil_div(g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile, kScaleCols));  // a piece is bounded
+  auto* kernel = !head_scale_joins(g) ? scale_kernel<PLANES, 0> : distill ? scale_kernel<PLANES, 2> : scale_kernel<PLANES, 1>;
+  return launch_chained(kernel, grid, kThreadsRows, 0, s, g, w, loss);
+}
+cudaError_t head_scale(const HeadGeom& g, const HeadWork& w, int dtype, bool distill, float* loss, cudaStream_t s) {
+  return dtype == RELAY_BF16 ? scale_typed<1>(g, w, distill, loss, s) : scale_typed<kHeadPlanesF32>(g, w, distill, loss, s);
 }
 
 cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, bool whole, void* d_hidden,
