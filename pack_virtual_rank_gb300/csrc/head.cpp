@@ -211,6 +211,7 @@ relay_status_t run_head(const relay_head_t& h, HeadGeom g, int top, const int32_
                         const void* teacher, int teacher_dtype, const float* row_weight, float* loss,
                         void* workspace, cudaStream_t stream) {
   g.sms = sm_count();
+  g.ctas = g.tokens <= kHeadRowTile / 2 ? 1 : 2;  // one CTA's rows: the other would multiply padding
   const uintptr_t base = (uintptr_t)up((int64_t)reinterpret_cast<uintptr_t>(workspace), 256);
   const Arrangement ar = arrange(h, g, top, base);
   const HeadWork& w = ar.w;

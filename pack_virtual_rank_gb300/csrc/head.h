@@ -41,8 +41,16 @@ struct HeadGeom {
   int32_t vocab;
   int32_t mpad;                             // tokens rounded up to kHeadRowTile
   int32_t sms;
+  int32_t ctas;                             // that make one product: 2, or 1 for few rows
   float tau, inv_tau;
 };
+
+#ifdef __CUDACC__
+__host__ __device__ __forceinline__
+#else
+inline
+#endif
+int head_row_tile(const HeadGeom& g) { return kHeadRowTile / 2 * g.ctas; }  // rows of one product
 
 #ifdef __CUDACC__
 __host__ __device__ __forceinline__
@@ -106,12 +114,12 @@ __device__ __forceinline__ int head_long_steps(int tiles, int cuts) {  // a tile
 __device__ __forceinline__ int head_short_steps(int live) { return (live + 63) / 64 + kHeadOpenSteps; }  // of d_weight
 __device__ __forceinline__ int head_cuts(const HeadGeom& g, const HeadWork& w, int live) {
   // whole warps call it: a lane prices two numbers of cuts (there are at most 64)
-  const int pairs = g.sms / 2, nd = (g.dim + kHeadTile - 1) / kHeadTile;
-  const int64_t items = (int64_t)((live + kHeadRowTile - 1) / kHeadRowTile) * nd;
+  const int pairs = g.sms / g.ctas, nd = (g.dim + kHeadTile - 1) / kHeadTile, rows = head_row_tile(g);
+  const int64_t items = (int64_t)((live + rows - 1) / rows) * nd;
   if (w.splits == 1 || items >= 4 * pairs) return 1;
   const int64_t move = 1 + (int64_t)live * g.dim / 225000;
   const int dw_steps = w.with_dw ? head_short_steps(live) : 0;
-  const int64_t dw_work = (int64_t)w.tiles_per_piece * nd * dw_steps;
+  const int64_t dw_work = (int64_t)w.tiles_per_piece * (2 / g.ctas) * nd * dw_steps;
   uint32_t least = ~0u;
   int best = 1;
   for (int i = 0; i < 2; ++i) {

@@ -17,7 +17,9 @@
 //
 // Why pairs: a single CTA's 128 x 256 tile reads 48 KiB for 512 cycles of products, and the path from
 // L2 into an SM carries 64 bytes a cycle: the tensor pipe was 69-71% busy at 18 TB/s of such
-// reads. A pair shares the second operand, 32 KiB for the same products.
+// reads. A pair shares the second operand, 32 KiB for the same products, and keeps it 76-79% busy. Up
+// to 128 rows one CTA works alone (CTAS = 1): half of a pair's product would be padding rows (8 rows,
+// 1024 x 32768: 20 us a call alone, 30 us in pairs).
 //
 // The accumulator puts a row of the tile into one lane, so the softmax statistics of a row are
 // one thread's registers: no shuffles.
@@ -39,15 +41,21 @@ namespace {
 __device__ unsigned g_head_fault;
 
 constexpr int kBM = 128, kBN = 256, kBK = 64;  // rows of one CTA, columns of the pair, inner step
-constexpr int kPairM = 2 * kBM;
-constexpr int kHalf = kBN / 2;                 // columns (B's rows) one CTA brings
-constexpr int kStages = 6;
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kHalf * kBK * 2, kStageBytes = kABytes + kBBytes;
-static_assert(kPairM == kHeadRowTile && kBN == kHeadTile, "tiles are what rows and columns are padded to");
+// What depends on the number of CTAs that make one product.
+template <int CTAS>
+struct Shape {
+  static constexpr int kM = CTAS * kBM;       // rows of the product
+  static constexpr int kShare = kBN / CTAS;   // columns (B's rows) one CTA brings
+  static constexpr int kStages = CTAS == 2 ? 6 : 4;
+  static constexpr int kABytes = kBM * kBK * 2, kBBytes = kShare * kBK * 2, kStageBytes = kABytes + kBBytes;
+};
+static_assert(Shape<2>::kM == kHeadRowTile && kBN == kHeadTile, "tiles are what rows and columns are padded to");
+constexpr int kRingBytes = Shape<2>::kStages * Shape<2>::kStageBytes;
+static_assert(kRingBytes == Shape<1>::kStages * Shape<1>::kStageBytes, "one ring size");
 constexpr int kFinishWarps = 8;                        // warps that turn accumulators into results
 constexpr int kOutWarpBytes = 32 * 64 * 2;             // 32 rows x 64 columns of 16 bits, one per warp
 constexpr int kOutBytes = kFinishWarps * kOutWarpBytes;
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kOutBytes;
+constexpr int kSmemBytes = 1024 + kRingBytes + kOutBytes;
 // Three groups of four warps: one that loads and multiplies (two threads of it), two that
 // finish. The finishing threads hold 128 accumulators each, so registers move to them: at launch
 // every thread has kLaunchRegs, and 56 + 2 * 224 = 3 * 168. The launch checks that the kernel was
@@ -119,19 +127,20 @@ struct Schedule {
   }
 };
 
-template <int P>
+template <int P, int CTAS>
 __device__ __forceinline__ Schedule schedule(const GemmArgs& p, int live) {
-  const int mt = (live + kPairM - 1) / kPairM, tiles = p.tile_hi - p.tile_lo;
+  constexpr int kM = Shape<CTAS>::kM;
+  const int mt = (live + kM - 1) / kM, tiles = p.tile_hi - p.tile_lo;
   const int nd = (p.g.dim + kBN - 1) / kBN;
   Schedule s{};
   s.cuts = 1;
-  s.pairs = gridDim.x / 2;
-  s.mine = blockIdx.x / 2;
+  s.pairs = gridDim.x / CTAS;
+  s.mine = blockIdx.x / CTAS;
   if (P != kBack) {
     s.items = mt * tiles;
     return s;
   }
-  const int short_items = p.want_dw ? tiles * nd : 0;
+  const int short_items = p.want_dw ? tiles * (kHeadTile / kM) * nd : 0;
   if (p.want_dh) {
     s.cuts = head_cuts(p.g, p.w, live);
     s.long_items = mt * nd * s.cuts;
@@ -145,9 +154,10 @@ __device__ __forceinline__ Schedule schedule(const GemmArgs& p, int live) {
   return s;
 }
 
-template <int P>
+template <int P, int CTAS>
 __device__ __forceinline__ Item item_at(const GemmArgs& p, const Schedule& sched, int live, int rank, int i) {
-  const int mt = (live + kPairM - 1) / kPairM, tiles = p.tile_hi - p.tile_lo;
+  constexpr int kM = Shape<CTAS>::kM, kPerTile = kHeadTile / kM;
+  const int mt = (live + kM - 1) / kM, tiles = p.tile_hi - p.tile_lo;
   const int nd = (p.g.dim + kBN - 1) / kBN;
   Item t{};
   if (P == kBack) {
@@ -157,21 +167,22 @@ __device__ __forceinline__ Item item_at(const GemmArgs& p, const Schedule& sched
     t.col0 = i % nd * kBN;
     i /= nd;
     if (t.weight) {
-      t.tile = p.tile_lo + i;
+      const int within = i % kPerTile * kM + rank * kBM;
+      t.tile = p.tile_lo + i / kPerTile;
       t.shard = head_shard_of_tile(p.g, t.tile);
-      t.v0 = (t.tile - p.g.tile0[t.shard]) * kHeadTile + rank * kBM;
-      t.row0 = (t.tile - p.tile_lo) * kHeadTile + rank * kBM;
+      t.v0 = (t.tile - p.g.tile0[t.shard]) * kHeadTile + within;
+      t.row0 = (t.tile - p.tile_lo) * kHeadTile + within;
       t.k_hi = (live + kBK - 1) / kBK;
     } else {
       t.split = i % sched.cuts;
-      t.row0 = i / sched.cuts * kPairM + rank * kBM;
+      t.row0 = i / sched.cuts * kM + rank * kBM;
       t.k_lo = p.tile_lo + (int)((int64_t)tiles * t.split / sched.cuts);
       t.k_hi = p.tile_lo + (int)((int64_t)tiles * (t.split + 1) / sched.cuts);
     }
   } else {
     const int per = p.group * tiles, band = i / per, in_band = i % per;
     const int width = min(p.group, mt - band * p.group);
-    t.row0 = (band * p.group + in_band % width) * kPairM + rank * kBM;
+    t.row0 = (band * p.group + in_band % width) * kM + rank * kBM;
     t.tile = p.tile_lo + in_band / width;
     t.shard = head_shard_of_tile(p.g, t.tile);
     t.v0 = (t.tile - p.g.tile0[t.shard]) * kHeadTile;
@@ -206,45 +217,46 @@ __device__ __forceinline__ int pair_a(int i) { return (0x200110 >> (4 * (5 - i))
 __device__ __forceinline__ int pair_b(int i) { return (0x021010 >> (4 * (5 - i))) & 15; }  // 0 2 1 0 1 0
 
 // full: the stage barriers of the pair's first CTA; empty: this CTA's own.
-template <int P, int PLANES>
+template <int P, int PLANES, int CTAS>
 __device__ void produce(const GemmArgs& p, const Schedule& sched, int live, int rank, uint32_t ring, uint32_t full, uint32_t empty,
                         volatile int* gave_up) {
   const uint32_t pair_full = pair_addr(full, 0);
-  const int half = rank * kHalf;
+  using S = Shape<CTAS>;
+  const int share = rank * S::kShare;
   int stage = 0;
   uint32_t phase = 0;
   int64_t issued = 0;
   bool ok = true;
   for (int slot = 0, i; ok && (i = sched.at(slot)) >= 0; ++slot) {
-    const Item t = item_at<P>(p, sched, live, rank, i);
+    const Item t = item_at<P, CTAS>(p, sched, live, rank, i);
     ok = for_steps<P>(p, t, [&](int k, int k_shard, int k_v) {
       for (int pair = 0; pair < kPairs<PLANES>; ++pair) {
         const int pa = PLANES == 1 ? 0 : pair_a(pair), pb = PLANES == 1 ? 0 : pair_b(pair);
         if (!bar_wait(empty + 8 * stage, phase ^ 1, gave_up)) return false;
-        const uint32_t bar = pair_full + 8 * stage, sa = ring + stage * kStageBytes, sb = sa + kABytes;
-        if (rank == 0) bar_expect(full + 8 * stage, 2 * kStageBytes);
+        const uint32_t bar = pair_full + 8 * stage, sa = ring + stage * S::kStageBytes, sb = sa + S::kABytes;
+        if (rank == 0) bar_expect(full + 8 * stage, CTAS * S::kStageBytes);
         ++issued;
         const int wrow = pb * p.g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;  // plane of a packed weight
         if (P == kBack && t.weight) {
           for (int j = 0; j < kBM / 64; ++j)
-            map_load(sa + j * 8192, &p.a, t.row0 + 64 * j, pa * p.g.mpad + k * kBK, bar);
-          for (int j = 0; j < kHalf / 64; ++j)
-            map_load(sb + j * 8192, &p.hid, t.col0 + half + 64 * j, pb * p.g.mpad + k * kBK, bar);
+            map_load<CTAS>(sa + j * 8192, &p.a, t.row0 + 64 * j, pa * p.g.mpad + k * kBK, bar);
+          for (int j = 0; j < S::kShare / 64; ++j)
+            map_load<CTAS>(sb + j * 8192, &p.hid, t.col0 + share + 64 * j, pb * p.g.mpad + k * kBK, bar);
         } else if (P == kBack) {
           for (int j = 0; j < kBM / 64; ++j)
-            map_load(sa + j * 8192, &p.a, k * kBK, pa * p.g.mpad + t.row0 + 64 * j, bar);
+            map_load<CTAS>(sa + j * 8192, &p.a, k * kBK, pa * p.g.mpad + t.row0 + 64 * j, bar);
           const bool packed = p.w.wpack != nullptr;
           const CUtensorMap* m = &p.b[packed ? 0 : k_shard];
           const int y = packed ? wrow + p.g.tile0[k_shard] * kHeadTile + k_v : k_v;
-          for (int j = 0; j < kHalf / 64; ++j) map_load(sb + j * 8192, m, t.col0 + half + 64 * j, y, bar);
+          for (int j = 0; j < S::kShare / 64; ++j) map_load<CTAS>(sb + j * 8192, m, t.col0 + share + 64 * j, y, bar);
         } else {
-          map_load(sa, &p.a, k * kBK, pa * p.g.mpad + t.row0, bar);
+          map_load<CTAS>(sa, &p.a, k * kBK, pa * p.g.mpad + t.row0, bar);
           if (p.w.wpack != nullptr)
-            map_load(sb, &p.b[0], k * kBK, wrow + t.tile * kHeadTile + half, bar);
+            map_load<CTAS>(sb, &p.b[0], k * kBK, wrow + t.tile * kHeadTile + share, bar);
           else
-            map_load(sb, &p.b[t.shard], k * kBK, t.v0 + half, bar);
+            map_load<CTAS>(sb, &p.b[t.shard], k * kBK, t.v0 + share, bar);
         }
-        if (++stage == kStages) {
+        if (++stage == Shape<CTAS>::kStages) {
           stage = 0;
           phase ^= 1;
         }
@@ -257,9 +269,9 @@ __device__ void produce(const GemmArgs& p, const Schedule& sched, int live, int 
   // barriers count both CTAs' loads, and the pair leaves together; what they do not count (a stage
   // only one of the two asked for) lands in microseconds.
   const uint64_t start = global_ns();
-  for (int back = 0; rank == 0 && back < kStages && back < issued; ++back) {
+  for (int back = 0; rank == 0 && back < Shape<CTAS>::kStages && back < issued; ++back) {
     if (--stage < 0) {
-      stage = kStages - 1;
+      stage = Shape<CTAS>::kStages - 1;
       phase ^= 1;
     }
     while (!bar_try(full + 8 * stage, phase) && global_ns() - start < kWaitNs) {
@@ -270,18 +282,19 @@ __device__ void produce(const GemmArgs& p, const Schedule& sched, int live, int 
   }
 }
 
-template <int P, int PLANES>
+template <int P, int PLANES, int CTAS>
 __device__ void multiply(const GemmArgs& p, const Schedule& sched, int live, uint32_t ring, uint32_t full, uint32_t empty,
                          uint32_t acc_full, uint32_t acc_empty, uint32_t drain, uint32_t tmem,
                          volatile int* gave_up) {
+  using S = Shape<CTAS>;
   constexpr bool kBOuter = P == kBack;
   int stage = 0, n = 0;
   uint32_t phase = 0;
   bool ok = true;
   for (int slot = 0, i; ok && (i = sched.at(slot)) >= 0; ++slot) {
-    const Item t = item_at<P>(p, sched, live, 0, i);
+    const Item t = item_at<P, CTAS>(p, sched, live, 0, i);
     const bool a_outer = P == kBack && t.weight;
-    const uint32_t desc = a_outer ? product_desc(kPairM, kBN, true, kBOuter) : product_desc(kPairM, kBN, false, kBOuter);
+    const uint32_t desc = a_outer ? product_desc(S::kM, kBN, true, kBOuter) : product_desc(S::kM, kBN, false, kBOuter);
     int in_chain = 0;
     auto open = [&] {
       const bool free = bar_wait(acc_empty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, gave_up);
@@ -291,7 +304,7 @@ __device__ void multiply(const GemmArgs& p, const Schedule& sched, int live, uin
     if (!(ok = open())) break;
     ok = for_steps<P>(p, t, [&](int, int, int) {
       if (in_chain == kChain<P, PLANES>) {
-        tc_commit(acc_full + 8 * (n & 1));
+        tc_commit<CTAS>(acc_full + 8 * (n & 1));
         ++n;
         in_chain = 0;
         if (!open()) return false;
@@ -300,14 +313,14 @@ __device__ void multiply(const GemmArgs& p, const Schedule& sched, int live, uin
       for (int pair = 0; pair < kPairs<PLANES>; ++pair) {
         if (!bar_wait(full + 8 * stage, phase, gave_up)) return false;
         tc_fence_after();
-        const uint32_t sa = ring + stage * kStageBytes;
-        const uint64_t da = operand_desc(sa, a_outer), db = operand_desc(sa + kABytes, kBOuter);
+        const uint32_t sa = ring + stage * S::kStageBytes;
+        const uint64_t da = operand_desc(sa, a_outer), db = operand_desc(sa + S::kABytes, kBOuter);
 #pragma unroll
         for (int k = 0; k < kBK / 16; ++k)
-          tc_product(acc, da + k * operand_step(a_outer), db + k * operand_step(kBOuter), desc,
+          tc_product<CTAS>(acc, da + k * operand_step(a_outer), db + k * operand_step(kBOuter), desc,
                      in_chain > 0 || pair > 0 || k > 0);
-        tc_commit(empty + 8 * stage);
-        if (++stage == kStages) {
+        tc_commit<CTAS>(empty + 8 * stage);
+        if (++stage == Shape<CTAS>::kStages) {
           stage = 0;
           phase ^= 1;
         }
@@ -315,11 +328,11 @@ __device__ void multiply(const GemmArgs& p, const Schedule& sched, int live, uin
       ++in_chain;
       return true;
     });
-    if (ok) tc_commit(acc_full + 8 * (n++ & 1));
+    if (ok) tc_commit<CTAS>(acc_full + 8 * (n++ & 1));
   }
   // giving up: products still running write the tensor memory that is about to be freed
   if (!ok) {
-    tc_commit(drain);
+    tc_commit<CTAS>(drain);
     const uint64_t start = global_ns();
     while (!bar_try(drain, 0) && global_ns() - start < kWaitNs) {
     }
@@ -583,15 +596,16 @@ __device__ __forceinline__ void finish_dweight(const GemmArgs& p, const Item& t,
   }
 }
 
-template <int P, int PLANES>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __grid_constant__ GemmArgs p) {
+template <int P, int PLANES, int CTAS>
+__global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __grid_constant__ GemmArgs p) {
+  constexpr int kStages = Shape<CTAS>::kStages;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up;
   const int warp = threadIdx.x / 32, rank = (int)pair_rank();
   dep_launch();
-  const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u, staging = ring + kStages * kStageBytes;
+  const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u, staging = ring + kRingBytes;
   const uint32_t full = smem_addr(s_bar), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                  acc_empty = acc_full + 16, drain = acc_empty + 16;
   if (threadIdx.x == 0) {
@@ -601,27 +615,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) hea
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(acc_full + 8 * i, 1);
-      bar_init(acc_empty + 8 * i, 2 * kFinishWarps);  // of both CTAs, at the first's
+      bar_init(acc_empty + 8 * i, CTAS * kFinishWarps);  // of all CTAs, at the first's
     }
     bar_init(drain, 1);
     s_gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc(smem_addr(&s_tmem), 512);
+  if (warp == 1) tmem_alloc<CTAS>(smem_addr(&s_tmem), 512);
   tc_fence_before();
   __syncthreads();
-  pair_sync();  // the other CTA's barriers are ready
+  if (CTAS == 2) pair_sync();  // the other CTA's barriers are ready
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   dep_wait();
   const int live = *p.w.n_live;
-  const Schedule sched = schedule<P>(p, live);  // a pair without a tile passes through
+  const Schedule sched = schedule<P, CTAS>(p, live);  // a pair without a tile passes through
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeedRegs));
-    if (threadIdx.x == 0) produce<P, PLANES>(p, sched, live, rank, ring, full, empty, &s_gave_up);
+    if (threadIdx.x == 0) produce<P, PLANES, CTAS>(p, sched, live, rank, ring, full, empty, &s_gave_up);
     if (threadIdx.x == 32 && rank == 0)
-      multiply<P, PLANES>(p, sched, live, ring, full, empty, acc_full, acc_empty, drain, tmem, &s_gave_up);
+      multiply<P, PLANES, CTAS>(p, sched, live, ring, full, empty, acc_full, acc_empty, drain, tmem, &s_gave_up);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFinishRegs));
     // warps 4 to 7 finish a tile's first 128 columns, 8 to 11 its last; a warp reads the quarter of
@@ -632,7 +646,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) hea
     bool ok = true;
     const uint32_t first_empty = pair_addr(acc_empty, 0);
     for (int slot = 0, i; ok && (i = sched.at(slot)) >= 0; ++slot) {
-      const Item t = item_at<P>(p, sched, live, rank, i);
+      const Item t = item_at<P, CTAS>(p, sched, live, rank, i);
       Entries e;
       if (P <= kGradient)  // under the products
         e.seek(p.w, p.g, t.row0 + quarter * 32 + threadIdx.x % 32, live, t.tile * kHeadTile + part * kMine);
@@ -678,11 +692,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) hea
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  pair_sync();  // neither CTA's memory is used by the other any more
+  if (CTAS == 2) pair_sync();  // neither CTA's memory is used by the other any more
   if (threadIdx.x == 0 && s_gave_up) atomicOr(&g_head_fault, 2u);
   if (warp == 1) {
     tc_fence_after();
-    tmem_free(tmem, 512);
+    tmem_free<CTAS>(tmem, 512);
   }
 }
 
@@ -722,7 +736,7 @@ bool maps_for(GemmArgs* a, int dtype) {
   const int planes = head_planes(dtype);
   const int64_t padded = (int64_t)g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
   bool ok = true;
-  // the weight: boxes of 128 rows by 64 of dim (logits), or of 64 rows by 64 (d_hidden)
+  // the weight: boxes of a CTA's share of 256 rows by 64 of dim (logits), or of 64 rows by 64 (d_hidden)
   auto weight = [&](int box_rows) {
     if (w.wpack != nullptr) {
       ok &= matrix_map(&a->b[0], w.wpack, planes * padded, g.dim, w.dim_pad, box_rows);
@@ -750,29 +764,30 @@ bool maps_for(GemmArgs* a, int dtype) {
     }
   } else {
     ok &= matrix_map(&a->a, w.hid, grad_rows, g.dim, w.dim_pad, kBM);
-    weight(kHalf);
+    weight(kBN / g.ctas);
     if (P != kStats) ok &= matrix_map(&a->c[0], w.grad, grad_rows, w.grad_ld, w.grad_ld, 32);
   }
   return ok;
 }
 
-template <int P, int PLANES>
+template <int P, int PLANES, int CTAS>
 cudaError_t launch(const GemmArgs& a, int64_t items, cudaStream_t s) {
   static thread_local int ready_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  auto* kernel = head_product_kernel<P, PLANES, CTAS>;
   if (ready_device != dev) {
     cudaFuncAttributes attr;
-    e = cudaFuncGetAttributes(&attr, head_product_kernel<P, PLANES>);
+    e = cudaFuncGetAttributes(&attr, kernel);
     if (e != cudaSuccess) return e;
     if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;  // the split would wait forever
-    e = cudaFuncSetAttribute(head_product_kernel<P, PLANES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     ready_device = dev;
   }
-  const int blocks = (int)std::min<int64_t>(2 * items, sm_count() / 2 * 2);
-  return launch_chained(head_product_kernel<P, PLANES>, blocks, kGemmThreads, kSmemBytes, s, a);
+  const int blocks = (int)std::min<int64_t>(CTAS * items, a.g.sms / CTAS * CTAS);
+  return launch_chained_clusters(kernel, CTAS, blocks, kGemmThreads, kSmemBytes, s, a);
 }
 
 template <int P>
@@ -790,12 +805,15 @@ cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int 
   a.want_dw = dw;
   a.dh_vec = reinterpret_cast<uintptr_t>(sh.dh) % 16 == 0 && sh.dh_ld * esize_of(dtype) % 16 == 0;
   // row tiles whose packed hidden rows take 64 MiB, half of L2
-  const int64_t mt = g.mpad / kPairM, tiles = hi - lo, nd = (g.dim + kBN - 1) / kBN;
-  a.group = (int)std::max<int64_t>(1, std::min<int64_t>(mt, (64ll << 20) / ((int64_t)kPairM * w.dim_pad * 2 * head_planes(dtype))));
+  const int rows = kBM * g.ctas;
+  const int64_t mt = (g.tokens + rows - 1) / rows, tiles = hi - lo, nd = (g.dim + kBN - 1) / kBN;
+  a.group = (int)std::max<int64_t>(1, std::min<int64_t>(mt, (64ll << 20) / ((int64_t)rows * w.dim_pad * 2 * head_planes(dtype))));
   if (!maps_for<P>(&a, dtype)) return cudaErrorInvalidValue;
-  const int64_t items = P == kBack ? (dh ? mt * nd * w.splits : 0) + (dw ? tiles * nd : 0) : mt * tiles;
+  const int64_t items = P == kBack ? (dh ? mt * nd * w.splits : 0) + (dw ? tiles * (kHeadTile / rows) * nd : 0) : mt * tiles;
   if (items > INT_MAX) return cudaErrorInvalidValue;
-  return dtype == RELAY_BF16 ? launch<P, 1>(a, items, s) : launch<P, kHeadPlanesF32>(a, items, s);
+  if (g.ctas == 1)
+    return dtype == RELAY_BF16 ? launch<P, 1, 1>(a, items, s) : launch<P, kHeadPlanesF32, 1>(a, items, s);
+  return dtype == RELAY_BF16 ? launch<P, 1, 2>(a, items, s) : launch<P, kHeadPlanesF32, 2>(a, items, s);
 }
 
 }  // namespace

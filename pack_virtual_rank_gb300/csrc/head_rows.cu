@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreadsRows)
   __syncthreads();
   total = s_total;
   int packed = s_before;  // live rows before row `base`
-  const int read_end = (total + kHeadRowTile - 1) / kHeadRowTile * kHeadRowTile;
+  const int row_tile = head_row_tile(g), read_end = (total + row_tile - 1) / row_tile * row_tile;
   if (blockIdx.x == 0 && threadIdx.x == 0) *w.n_live = total;
   const int64_t plane = (int64_t)g.mpad * w.dim_pad;
   for (int base = lo; base < hi; base += kThreadsRows) {
@@ -249,8 +249,7 @@ __global__ void __launch_bounds__(kThreadsRows)
     }
     __syncthreads();
   }
-  // places past the last row of the batch: fewer than kHeadRowTile, one per block where there are
-  // enough blocks
+  // places past the last row of the batch
   for (int place = g.tokens + blockIdx.x * kWarps + warp; place < g.mpad; place += gridDim.x * kWarps) {
     if (lane == 0) {
       w.perm[place] = 0;
@@ -349,7 +348,8 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
   dep_launch();
   dep_wait();
   const int live = *w.n_live, row = blockIdx.x;
-  if (row >= (live + kHeadRowTile - 1) / kHeadRowTile * kHeadRowTile) return;
+  const int row_tile = head_row_tile(g);
+  if (row >= (live + row_tile - 1) / row_tile * row_tile) return;
   const int col0 = blockIdx.y * kScaleCols;
   const int cols = g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
   const int64_t plane = (int64_t)g.mpad * w.grad_ld;
@@ -500,7 +500,8 @@ static cudaError_t pack_typed(const HeadGeom& g, const HeadWork& w, bool distill
   // a warp per row; at most 2048 blocks read every row's flag
   constexpr int kWarps = kThreadsRows / 32;
   const int per = ceil_div(ceil_div(g.tokens, 2048), kWarps) * kWarps;
-  const int blocks = ceil_div(g.tokens, per);
+  // (a few more for a small batch: they zero the places past it)
+  const int pad = ceil_div(head_row_tile(g), kWarps), blocks = ceil_div(g.tokens, per) > pad ? ceil_div(g.tokens, per) : pad;
   const int vec = reinterpret_cast<uintptr_t>(hidden) % 16 == 0 && ld * sizeof(T) % 16 == 0;
   return launch_chained(distill ? pack_kernel<T, true> : pack_kernel<T, false>, blocks, kThreadsRows, 0, s, g, w,
                         static_cast<const T*>(hidden), ld, targets, row_weight, loss, static_cast<T*>(dh), dh_ld, per,
