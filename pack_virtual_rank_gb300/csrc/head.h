@@ -102,44 +102,44 @@ struct HeadWork {
 
 // Cuts of the vocabulary for d_hidden, whose tiles alone are too few, or too long beside what else
 // runs, to fill the GPU evenly. Costs are in inner steps of one tile (64 columns, about 0.27 us):
-// the rounds of the GPU's pairs of SMs over d_hidden's tiles, or all the work spread evenly plus the
+// the rounds of the GPU's products over d_hidden's tiles, or all the work spread evenly plus the
 // longest tile at its end, whichever is more; plus writing and reading a cut's fp32 partial sums (8 bytes
 // a value; a step's time moves about 1.8 MB). The live rows are known on the device only, so
-// kernels call this themselves and agree.
+// kernels call this themselves and agree. In float: a few parts in 10^7 decide nothing, and every lane
+// of every kernel gets the same.
 #ifdef __CUDACC__
-constexpr int kHeadOpenSteps = 8;  // steps a tile costs besides its own
-__device__ __forceinline__ int head_long_steps(int tiles, int cuts) {  // a tile of d_hidden
-  return (int)(((uint32_t)tiles * 4 + cuts - 1) / cuts) + kHeadOpenSteps;
+constexpr int kHeadOpenSteps = 4;  // steps a tile costs besides its own
+__device__ __forceinline__ float head_long_steps(int tiles, int cuts) {  // a tile of d_hidden
+  return (float)(((uint32_t)tiles * 4 + cuts - 1) / cuts + kHeadOpenSteps);
 }
-__device__ __forceinline__ int head_short_steps(int live) { return (live + 63) / 64 + kHeadOpenSteps; }  // of d_weight
+__device__ __forceinline__ float head_short_steps(int live) { return (float)((live + 63) / 64 + kHeadOpenSteps); }  // of d_weight
 __device__ __forceinline__ int head_cuts(const HeadGeom& g, const HeadWork& w, int live) {
   // whole warps call it: a lane prices two numbers of cuts (there are at most 64)
-  const int pairs = g.sms / g.ctas, nd = (g.dim + kHeadTile - 1) / kHeadTile, rows = head_row_tile(g);
-  const int64_t items = (int64_t)((live + rows - 1) / rows) * nd;
-  if (w.splits == 1 || items >= 4 * pairs) return 1;
-  const int64_t move = 1 + (int64_t)live * g.dim / 225000;
-  const int dw_steps = w.with_dw ? head_short_steps(live) : 0;
-  const int64_t dw_work = (int64_t)w.tiles_per_piece * (2 / g.ctas) * nd * dw_steps;
-  uint32_t least = ~0u;
+  const int pairs = g.ctas == 1 ? g.sms : g.sms / 2, nd = (g.dim + kHeadTile - 1) / kHeadTile;
+  const int rows = head_row_tile(g);
+  const float items = (float)((live + rows - 1) / rows) * (float)nd;
+  if (w.splits == 1 || items >= 4.0f * (float)pairs) return 1;
+  const float move = 0.2f + (float)live * (float)g.dim * (1.0f / 225000.0f);
+  const float dw_steps = w.with_dw ? head_short_steps(live) : 0.0f;
+  const float dw_work = (float)w.tiles_per_piece * (float)(g.ctas == 1 ? 2 * nd : nd) * dw_steps;
+  const float each = 1.0f / (float)pairs;
+  float least = INFINITY;
   int best = 1;
+#pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int s = 1 + threadIdx.x % 32 + 32 * i;
-    if (s > w.splits) continue;
-    const int steps = head_long_steps(w.tiles_per_piece, s);
-    const int64_t rounds = (int64_t)(((uint32_t)items * s + pairs - 1) / pairs) * steps;
-    // (in float: a few parts in 10^7 decide nothing, and every lane of every kernel gets the same)
-    const int64_t spread = (int64_t)((float)((int64_t)((uint32_t)items * s) * steps + dw_work) / (float)pairs) +
-                           (w.with_dw ? dw_steps : steps);
-    int64_t cost = rounds > spread ? rounds : spread;
-    if (s > 1) cost += s * move;
-    const uint32_t c = cost < 0xfffffffell ? (uint32_t)cost : 0xfffffffeu;
-    if (c < least) {
-      least = c;
+    const float steps = head_long_steps(w.tiles_per_piece, s);
+    const float rounds = ceilf(items * (float)s * each) * steps;
+    const float spread = (items * (float)s * steps + dw_work) * each + (w.with_dw ? dw_steps : steps);
+    const float cost = fmaxf(rounds, spread) + (s > 1 ? (float)s * move : 0.0f);
+    if (s <= w.splits && cost < least) {
+      least = cost;
       best = s;
     }
   }
-  const uint32_t all = __reduce_min_sync(~0u, least);
-  return (int)__reduce_min_sync(~0u, least == all ? (uint32_t)best : ~0u);
+  // positive floats order as integers do
+  const uint32_t all = __reduce_min_sync(~0u, __float_as_uint(least));
+  return (int)__reduce_min_sync(~0u, __float_as_uint(least) == all ? (uint32_t)best : ~0u);
 }
 #endif
 

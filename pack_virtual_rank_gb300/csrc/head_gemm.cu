@@ -85,6 +85,7 @@ struct GemmArgs {
   HeadGeom g;
   HeadWork w;
   HeadShards sh;
+  int32_t maps;      // which of the maps above are in use, in the order a, b, c, hid, dh
   int32_t tile_lo, tile_hi;
   int32_t want_dh, want_dw;
   int32_t first;     // d_hidden: overwrite the partial sums
@@ -148,7 +149,7 @@ __device__ __forceinline__ Schedule schedule(const GemmArgs& p, int live) {
   s.items = s.long_items + short_items;
   s.late = s.long_items % s.pairs;
   if (s.late > 0) {
-    s.lead = min(head_long_steps(tiles, s.cuts) / head_short_steps(live), short_items / (s.pairs - s.late));
+    s.lead = min((int)(head_long_steps(tiles, s.cuts) / head_short_steps(live)), short_items / (s.pairs - s.late));
     s.led = s.lead * (s.pairs - s.late);
   }
   return s;
@@ -622,6 +623,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  if (warp == 2 && threadIdx.x % 32 <= 2 * RELAY_HEAD_MAX_SHARDS + 2) {
+    // the maps' descriptors, on their way before the first load asks for them (a map that is not
+    // used holds zeros, and is not fetched)
+    const int i = threadIdx.x % 32;
+    const CUtensorMap* m = i == 0 ? &p.a : i <= RELAY_HEAD_MAX_SHARDS ? &p.b[i - 1]
+                           : i <= 2 * RELAY_HEAD_MAX_SHARDS ? &p.c[i - 1 - RELAY_HEAD_MAX_SHARDS]
+                           : i == 2 * RELAY_HEAD_MAX_SHARDS + 1 ? &p.hid : &p.dh;
+    if ((p.maps >> i) & 1) map_prefetch(m);
+  }
   if (warp == 1) tmem_alloc<CTAS>(smem_addr(&s_tmem), 512);
   tc_fence_before();
   __syncthreads();
@@ -737,12 +747,18 @@ bool maps_for(GemmArgs* a, int dtype) {
   const int64_t padded = (int64_t)g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
   bool ok = true;
   // the weight: boxes of a CTA's share of 256 rows by 64 of dim (logits), or of 64 rows by 64 (d_hidden)
+  constexpr int kB = 1, kC = kB + RELAY_HEAD_MAX_SHARDS, kHid = kC + RELAY_HEAD_MAX_SHARDS, kDh = kHid + 1;
+  a->maps = 1;
   auto weight = [&](int box_rows) {
     if (w.wpack != nullptr) {
+      a->maps |= 1 << kB;
       ok &= matrix_map(&a->b[0], w.wpack, planes * padded, g.dim, w.dim_pad, box_rows);
     } else {
       for (int s = 0; s < g.A; ++s)
-        if (g.rows[s] > 0) ok &= matrix_map(&a->b[s], a->sh.w[s], g.rows[s], g.dim, a->sh.w_ld, box_rows);
+        if (g.rows[s] > 0) {
+          a->maps |= 1 << (kB + s);
+          ok &= matrix_map(&a->b[s], a->sh.w[s], g.rows[s], g.dim, a->sh.w_ld, box_rows);
+        }
     }
   };
   const int64_t grad_rows = (int64_t)planes * g.mpad;
@@ -750,9 +766,11 @@ bool maps_for(GemmArgs* a, int dtype) {
     ok &= matrix_map(&a->a, w.grad, grad_rows, w.grad_ld, w.grad_ld, kBK);
     if (a->want_dh) {
       weight(kBK);
+      a->maps |= 1 << kDh;
       ok &= matrix_map(&a->dh, w.dh, (int64_t)w.splits * g.mpad, g.dim, w.dh_ld, 32, true);
     }
     if (a->want_dw) {
+      a->maps |= 1 << kHid;
       ok &= matrix_map(&a->hid, w.hid, grad_rows, g.dim, w.dim_pad, kBK);
       a->out_map = 1;
       for (int s = 0; s < g.A; ++s)
@@ -760,12 +778,18 @@ bool maps_for(GemmArgs* a, int dtype) {
           a->out_map &= reinterpret_cast<uintptr_t>(a->sh.dw[s]) % 16 == 0 && a->sh.dw_ld * esize_of(dtype) % 16 == 0;
       if (planes == 1 && a->out_map)
         for (int s = 0; s < g.A; ++s)
-          if (g.rows[s] > 0) ok &= matrix_map(&a->c[s], a->sh.dw[s], g.rows[s], g.dim, a->sh.dw_ld, 32);
+          if (g.rows[s] > 0) {
+            a->maps |= 1 << (kC + s);
+            ok &= matrix_map(&a->c[s], a->sh.dw[s], g.rows[s], g.dim, a->sh.dw_ld, 32);
+          }
     }
   } else {
     ok &= matrix_map(&a->a, w.hid, grad_rows, g.dim, w.dim_pad, kBM);
     weight(kBN / g.ctas);
-    if (P != kStats) ok &= matrix_map(&a->c[0], w.grad, grad_rows, w.grad_ld, w.grad_ld, 32);
+    if (P != kStats) {
+      a->maps |= 1 << kC;
+      ok &= matrix_map(&a->c[0], w.grad, grad_rows, w.grad_ld, w.grad_ld, 32);
+    }
   }
   return ok;
 }

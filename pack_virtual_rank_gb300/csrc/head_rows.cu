@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const HeadG
 // live ones, as far as products read them, become 0.
 constexpr int kScaleVecs = 4;  // 16-byte vectors in flight per thread and plane
 constexpr int kScaleCols = kThreadsRows * 8 * kScaleVecs;
+static_assert(RELAY_HEAD_MAX_TOP <= kThreadsRows && kScaleCols % (32 * kHeadStatTile) == 0, "an entry per thread; whole shares");
 // JOIN 1 (cross entropy), 2 (distillation): the block has the whole row, and does combine_kernel's
 // work for it first.
 template <int PLANES, int JOIN>
@@ -347,39 +348,52 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
   __shared__ float s_lse;
   dep_launch();
   dep_wait();
-  const int live = *w.n_live, row = blockIdx.x;
-  const int row_tile = head_row_tile(g);
-  if (row >= (live + row_tile - 1) / row_tile * row_tile) return;
-  const int col0 = blockIdx.y * kScaleCols;
+  const int row = blockIdx.x, col0 = blockIdx.y * kScaleCols;
   const int cols = g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
   const int64_t plane = (int64_t)g.mpad * w.grad_ld;
   uint16_t* line = w.grad + (int64_t)row * w.grad_ld;
-  const bool on = row < live;
-  const float weight = on ? w.wrow[row] : 0.0f;
-  float lse = on && JOIN == 0 ? w.lse[row] : 0.0f;
+  // everything is asked for before anything is waited for: all of it lies inside the workspace,
+  // whether the row is live or not
   uint4 in[kScaleVecs][PLANES];
   float ref[kScaleVecs];
 #pragma unroll
   for (int k = 0; k < kScaleVecs; ++k) {
     const int col = col0 + (k * kThreadsRows + threadIdx.x) * 8;
-    if (col >= cols || !on) continue;
+    if (col >= cols) continue;
 #pragma unroll
     for (int i = 0; i < PLANES; ++i) in[k][i] = ld_once(line + i * plane + col);
     ref[k] = w.part[(int64_t)(col / kHeadStatTile) * g.mpad + row].x;
   }
+  constexpr int kShares = kScaleCols / kHeadStatTile / 32;  // statistics of a whole row, per lane
+  float2 share[kShares];
+  if (JOIN != 0 && threadIdx.x < 32) {
+#pragma unroll
+    for (int i = 0; i < kShares; ++i) {
+      const int t = threadIdx.x + 32 * i;
+      share[i] = t < cols / kHeadStatTile ? w.part[(int64_t)t * g.mpad + row] : make_float2(-INFINITY, 0.0f);
+    }
+  }
+  const int live = *w.n_live, row_tile = head_row_tile(g);
+  const int64_t at = (int64_t)w.perm[row] * g.top;
+  const bool on = row < live;
+  const float weight = w.wrow[row];
+  float lse = JOIN == 0 ? w.lse[row] : 0.0f;
+  if (row >= (live + row_tile - 1) / row_tile * row_tile) return;
+  // the thread's entry, if any: at most RELAY_HEAD_MAX_TOP of them
+  const bool has = on && (int)threadIdx.x < g.top;
+  const int ent_col = has ? w.ent_col[at + threadIdx.x] : INT_MAX;
+  const float ent_z = has && ent_col != INT_MAX ? w.ent_z[at + threadIdx.x] : 0.0f;
   if (JOIN != 0 && on) {
     if (threadIdx.x < 32) {
       float m = -INFINITY, s = 0.0f;
-      for (int t = threadIdx.x; t < cols / kHeadStatTile; t += 32) {
-        const float2 p = w.part[(int64_t)t * g.mpad + row];
-        join(m, s, p.x, p.y);
-      }
+#pragma unroll
+      for (int i = 0; i < kShares; ++i) join(m, s, share[i].x, share[i].y);
       const float lse2 = join_warp(m, s);
-      row_loss<JOIN == 2>(g, w, row, lse2, loss);
       if (threadIdx.x == 0) s_lse = lse2;
     }
     __syncthreads();
     lse = s_lse;
+    if (threadIdx.x >= kThreadsRows - 32) row_loss<JOIN == 2>(g, w, row, lse, loss);
   }
 #pragma unroll
   for (int k = 0; k < kScaleVecs; ++k) ref[k] -= lse;
@@ -423,13 +437,12 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
   }
   if (!on) return;
   __syncthreads();
-  const int64_t at = (int64_t)w.perm[row] * g.top;
-  for (int k = threadIdx.x; k < g.top; k += kThreadsRows) {
-    const int c = w.ent_col[at + k];
-    if (c < col0 || c >= col0 + kScaleCols || c >= cols || (k > 0 && w.ent_col[at + k - 1] == c)) continue;
+  {
+    const int k = threadIdx.x, c = ent_col;
+    if (c < col0 || c >= col0 + kScaleCols || c >= cols || (k > 0 && w.ent_col[at + k - 1] == c)) return;
     float q = 0.0f;  // an id given several times: its first entry sums them
     for (int j = k; j < g.top && w.ent_col[at + j] == c; ++j) q += w.ent_q[at + j];
-    float v = weight * (exp2f(fmaf(w.ent_z[at + k], 1.4426950408889634f, -lse)) - q);
+    float v = weight * (exp2f(fmaf(ent_z, 1.4426950408889634f, -lse)) - q);
 #pragma unroll
     for (int i = 0; i < PLANES; ++i) {
       const uint32_t r = bf16x2_rn(v, 0.0f) & 0xffffu;
