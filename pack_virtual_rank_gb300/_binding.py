@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -158,6 +159,10 @@ def lib():
     L.relay_balance_loss.restype = i32
     L.relay_router_backward.argtypes = [vp, i64, i32, i64, i32, i32, i32, vp, vp, vp, vp, i64, vp]
     L.relay_router_backward.restype = i32
+    for name in ("forward", "backward", "balance"):
+        fn = getattr(L, f"relay_packed_router_{name}")
+        fn.argtypes = [ctypes.c_char_p]
+        fn.restype = i32
     if L.relay_abi_version() != 1:
         raise RuntimeError("librelay.so ABI version mismatch")
     _lib = L
@@ -478,7 +483,7 @@ def _handle(stream) -> int:
     """The stream's handle; the current stream's for None."""
     if stream is None and _raw_stream is not None and _device is not None:
         return _raw_stream(_device())
-    return _stream(stream)
+    return _stream(stream) or 0
 
 
 def _dtype(x, name: str) -> int:
@@ -621,23 +626,43 @@ def alloc_router_workspace(tokens: int, experts: int, device):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+# The router's calls pass their arguments as one block of 8-byte words: ctypes converts an argument
+# in 0.2 us, so that fifteen of them took as long as the kernel of a small call.
+_pack8, _pack13, _pack15 = (struct.Struct(f"{n}q").pack for n in (8, 13, 15))
+_double_bits = struct.Struct("d")
+_int64 = struct.Struct("q")
+
+
+def _rows(x, name: str):
+    """Address, rows, columns and row stride of a CUDA matrix whose rows are contiguous."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (device memory)")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    t, e = x.shape
+    s0, s1 = x.stride()
+    if s1 != 1 and e > 1:
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    return x.data_ptr(), t, e, s0 if t > 1 else max(s0, e)
+
+
 def relay_router_forward(logits, index, gate, counts, prob_sum, mask=None, normalize: bool = False,
                          workspace=None, stream=None) -> None:
     """Top-k experts of each row of logits [tokens, experts] (k = index.shape[1]), their gates, and
     the per-expert counts and probability sums (see relay.h). mask: bool or uint8 per row."""
     if _torch is None:
         _bind_torch()
-    t, e = logits.shape
-    k = index.shape[1]
+    ptr, t, e, stride = _rows(logits, "logits")
+    tk = (t, index.shape[1])
     if mask is not None:
         mask = _array(mask, "mask", _torch.bool if mask.dtype is _torch.bool else _torch.uint8, (t,))
     if workspace is None:
         workspace = _own_workspace(lambda: alloc_router_workspace(t, e, logits.device), stream)
-    _check(lib().relay_router_forward(
-        _matrix(logits, "logits"), _row_stride(logits), _dtype(logits, "logits"), t, e, k, normalize,
-        mask, _array(index, "index", _int32, (t, k)), _array(gate, "gate", _float32, (t, k)),
+    _check(lib().relay_packed_router_forward(_pack15(
+        ptr, stride, _dtype(logits, "logits"), t, e, tk[1], bool(normalize), mask or 0,
+        _array(index, "index", _int32, tk), _array(gate, "gate", _float32, tk),
         _array(counts, "counts", _int32, (e,)), _array(prob_sum, "prob_sum", _float32, (e,)),
-        workspace.data_ptr(), workspace.numel(), _handle(stream)))
+        workspace.data_ptr(), workspace.numel(), _handle(stream))))
 
 
 def relay_balance_loss(counts, prob_sum, top: int, coef: float, loss, d_prob, stream=None) -> None:
@@ -646,10 +671,10 @@ def relay_balance_loss(counts, prob_sum, top: int, coef: float, loss, d_prob, st
     if _torch is None:
         _bind_torch()
     e = counts.shape
-    _check(lib().relay_balance_loss(
+    _check(lib().relay_packed_router_balance(_pack8(
         _array(counts, "counts", _int32, e), _array(prob_sum, "prob_sum", _float32, e), counts.numel(),
-        top, coef, _array(loss, "loss", _float32, (1,)), _array(d_prob, "d_prob", _float32, e),
-        _handle(stream)))
+        top, _int64.unpack(_double_bits.pack(coef))[0], _array(loss, "loss", _float32, (1,)),
+        _array(d_prob, "d_prob", _float32, e), _handle(stream))))
 
 
 def relay_router_backward(logits, index, d_logits, d_gate=None, d_prob=None, normalize: bool = False,
@@ -657,12 +682,12 @@ def relay_router_backward(logits, index, d_logits, d_gate=None, d_prob=None, nor
     """Gradient of the router's logits from the gates' and the probabilities' (see relay.h)."""
     if _torch is None:
         _bind_torch()
-    t, e = logits.shape
+    ptr, t, e, stride = _rows(logits, "logits")
+    d_ptr, d_t, d_e, d_stride = _rows(d_logits, "d_logits")
     tk = index.shape
-    if d_logits.dtype is not logits.dtype or d_logits.shape != logits.shape or tk[0] != t:
+    if d_logits.dtype is not logits.dtype or d_t != t or d_e != e or len(tk) != 2 or tk[0] != t:
         raise ValueError("d_logits must have the logits' dtype and shape, index a row for each of theirs")
-    _check(lib().relay_router_backward(
-        _matrix(logits, "logits"), _row_stride(logits), _dtype(logits, "logits"), t, e, tk[1], normalize,
-        _array(index, "index", _int32, tk), None if d_gate is None else _array(d_gate, "d_gate", _float32, tk),
-        None if d_prob is None else _array(d_prob, "d_prob", _float32, (e,)), _matrix(d_logits, "d_logits"),
-        _row_stride(d_logits), _handle(stream)))
+    _check(lib().relay_packed_router_backward(_pack13(
+        ptr, stride, _dtype(logits, "logits"), t, e, tk[1], bool(normalize), _array(index, "index", _int32, tk),
+        0 if d_gate is None else _array(d_gate, "d_gate", _float32, tk),
+        0 if d_prob is None else _array(d_prob, "d_prob", _float32, (e,)), d_ptr, d_stride, _handle(stream))))

@@ -22,6 +22,7 @@
 // every value with every chosen index was most of the instructions.
 #include <limits.h>
 #include <math.h>
+#include <string.h>
 
 #include <algorithm>
 #include <string>
@@ -94,6 +95,14 @@ struct Lane {
   static constexpr uint32_t kNegInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
   uint32_t word[kWords];
   __device__ __forceinline__ void load(const T* x, int e0, int experts, int bytes) {
+    if (bytes == 16 && e0 + N <= experts) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(x + e0 + i * kPerWord);
+        word[i] = u.x; word[i + 1] = u.y; word[i + 2] = u.z; word[i + 3] = u.w;
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kWords; ++i) word[i] = kNegInf;
     if (bytes == 16) {
@@ -461,9 +470,11 @@ cudaError_t by_width(int experts, int top, F f) {
 }
 
 // Blocks of the forward pass, whose statistics are joined afterwards: at most four an SM of the
-// GB300's 152 (also with another device current, so that the workspace is one size).
-int64_t forward_blocks(int64_t tokens) {
-  return std::max<int64_t>(1, std::min<int64_t>((tokens + kRouterWarps - 1) / kRouterWarps, 4 * 152));
+// GB300's 152 (also with another device current, so that the workspace is one size). Two rounds
+// of one block are not worth a second launch.
+int64_t forward_blocks(int64_t tokens, int rows) {
+  if (tokens <= 2 * rows) return 1;
+  return std::min<int64_t>((tokens + rows - 1) / rows, 4 * 152);
 }
 
 // Bytes one load of a lane's values may take: rows aligned to them, and made of whole ones.
@@ -519,7 +530,7 @@ int64_t relay_router_workspace_size(int64_t tokens, int experts) {
     bad("tokens or experts out of range");
     return -1;
   }
-  return forward_blocks(tokens) * experts * 8 + 16;
+  return forward_blocks(tokens, kRouterWarps) * experts * 8 + 16;  // a row to a warp: the most blocks
 }
 
 relay_status_t relay_router_forward(const void* logits, int64_t row_stride, relay_dtype_t dtype,
@@ -550,7 +561,12 @@ relay_status_t relay_router_forward(const void* logits, int64_t row_stride, rela
                     span(workspace, need, "workspace", true)};
   st = check_spans(s, 7);
   if (st != RELAY_OK) return st;
-  const int blocks = (int)forward_blocks(tokens);
+  int rows = kRouterWarps;
+  by_width(experts, top, [&](auto, auto l) {
+    rows *= 32 / decltype(l)::value;
+    return cudaSuccess;
+  });
+  const int blocks = (int)forward_blocks(tokens, rows);
   int32_t* part_count = reinterpret_cast<int32_t*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~(uintptr_t)15);
   float* part_prob = reinterpret_cast<float*>(part_count + (int64_t)blocks * experts);
   const ForwardArgs a{logits, row_stride, tokens, experts, top, normalize, load_bytes(logits, row_stride, E, experts),
@@ -615,6 +631,38 @@ relay_status_t relay_router_backward(const void* logits, int64_t row_stride, rel
     return launch_chained(dtype == RELAY_BF16 ? router_backward_kernel<uint16_t, N, L> : router_backward_kernel<float, N, L>,
                           blocks, kRouterThreads, 0, stream, a);
   }));
+}
+
+}  // extern "C"
+
+namespace {
+// A word as an int: out of range is -1, which every check refuses.
+int word(int64_t v) { return v < INT_MIN || v > INT_MAX ? -1 : (int)v; }
+}  // namespace
+
+extern "C" {
+
+// The same calls with their arguments, in order, as one block of 8-byte words (the coefficient as the
+// bits of a double): for a caller whose foreign-function layer pays per argument.
+relay_status_t relay_packed_router_forward(const int64_t* a) {
+  return relay_router_forward(reinterpret_cast<const void*>(a[0]), a[1], (relay_dtype_t)a[2], a[3], word(a[4]), word(a[5]),
+                              (int)a[6], reinterpret_cast<const uint8_t*>(a[7]), reinterpret_cast<int32_t*>(a[8]),
+                              reinterpret_cast<float*>(a[9]), reinterpret_cast<int32_t*>(a[10]),
+                              reinterpret_cast<float*>(a[11]), reinterpret_cast<void*>(a[12]), a[13],
+                              reinterpret_cast<cudaStream_t>(a[14]));
+}
+relay_status_t relay_packed_router_balance(const int64_t* a) {
+  double coef;
+  memcpy(&coef, a + 4, sizeof coef);
+  return relay_balance_loss(reinterpret_cast<const int32_t*>(a[0]), reinterpret_cast<const float*>(a[1]), word(a[2]),
+                            word(a[3]), (float)coef, reinterpret_cast<float*>(a[5]), reinterpret_cast<float*>(a[6]),
+                            reinterpret_cast<cudaStream_t>(a[7]));
+}
+relay_status_t relay_packed_router_backward(const int64_t* a) {
+  return relay_router_backward(reinterpret_cast<const void*>(a[0]), a[1], (relay_dtype_t)a[2], a[3], word(a[4]),
+                               word(a[5]), (int)a[6], reinterpret_cast<const int32_t*>(a[7]),
+                               reinterpret_cast<const float*>(a[8]), reinterpret_cast<const float*>(a[9]),
+                               reinterpret_cast<void*>(a[10]), a[11], reinterpret_cast<cudaStream_t>(a[12]));
 }
 
 }  // extern "C"
