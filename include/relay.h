@@ -506,6 +506,16 @@ relay_status_t relay_device_status(void);
 relay_status_t relay_test_staged_wait(void* dst, const void* src, size_t count,
                                       relay_dtype_t dtype, int extra_bytes, cudaStream_t stream);
 
+/*
+ * relay_test_head_wait -- a test of the bounded waits (500 ms) of the losses' products: a
+ * relay_linear_xent whose barriers expect `extra_bytes` more than their loads bring. With
+ * extra_bytes > 0 the waits run out, the outputs are unspecified, and the next
+ * relay_device_status() reports RELAY_ERR_CUDA; the context stays usable. With 0 it is
+ * an ordinary call.
+ */
+relay_status_t relay_test_head_wait(const relay_head_t* head, const int32_t* targets, float* loss, void* workspace,
+                                    int64_t workspace_bytes, int extra_bytes, cudaStream_t stream);
+
 /* Human-readable text of the last error this thread's calls produced. */
 const char* relay_last_error(void);
 /* How the calling thread's last collective call was launched: "chained: G groups, P

@@ -151,6 +151,8 @@ def lib():
     L.relay_linear_xent.restype = i32
     L.relay_linear_distill.argtypes = [P(RelayHead), vp, i32, vp, i32, f32, vp, vp, vp, i64, vp]
     L.relay_linear_distill.restype = i32
+    L.relay_test_head_wait.argtypes = [P(RelayHead), vp, vp, vp, i64, i32, vp]
+    L.relay_test_head_wait.restype = i32
     L.relay_router_workspace_size.argtypes = [i64, i32]
     L.relay_router_workspace_size.restype = i64
     L.relay_router_forward.argtypes = [vp, i64, i32, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, i64, vp]

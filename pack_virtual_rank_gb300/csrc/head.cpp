@@ -297,6 +297,16 @@ relay_status_t relay_linear_xent(const relay_head_t* head, const int32_t* target
   });
 }
 
+relay_status_t relay_test_head_wait(const relay_head_t* head, const int32_t* targets, float* loss, void* workspace,
+                                    int64_t workspace_bytes, int extra_bytes, cudaStream_t stream) {
+  using namespace relay;
+  if (extra_bytes < 0 || extra_bytes > 65536) return bad("0 <= extra_bytes <= 65536");
+  head_test_extra(extra_bytes);
+  const relay_status_t st = relay_linear_xent(head, targets, nullptr, loss, workspace, workspace_bytes, stream);
+  head_test_extra(0);
+  return st;
+}
+
 relay_status_t relay_linear_distill(const relay_head_t* head, const void* teacher_logits,
                                     relay_dtype_t teacher_dtype, const int32_t* teacher_index,
                                     int top, float temperature, const float* row_weight,

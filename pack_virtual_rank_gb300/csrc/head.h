@@ -176,6 +176,8 @@ cudaError_t head_logits(const HeadGeom& g, const HeadWork& w, const HeadShards& 
 // d_hidden and d_weight of one piece, either or both. first: the first piece; whole: the only one.
 cudaError_t head_back(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo, int tile_hi,
                       bool first, bool whole, bool dh, bool dw, cudaStream_t s);
+// Makes the calling thread's next products wait for `bytes` more than their loads bring.
+void head_test_extra(int bytes);
 // Reads and clears the products' fault word.
 cudaError_t head_read_fault(unsigned* fault);
 

@@ -85,6 +85,7 @@ struct GemmArgs {
   HeadGeom g;
   HeadWork w;
   HeadShards sh;
+  int32_t extra;     // bytes a stage waits for that no load brings (test of the bounded waits)
   int32_t maps;      // which of the maps above are in use, in the order a, b, c, hid, dh
   int32_t tile_lo, tile_hi;
   int32_t want_dh, want_dw;
@@ -235,7 +236,7 @@ __device__ void produce(const GemmArgs& p, const Schedule& sched, int live, int 
         const int pa = PLANES == 1 ? 0 : pair_a(pair), pb = PLANES == 1 ? 0 : pair_b(pair);
         if (!bar_wait(empty + 8 * stage, phase ^ 1, gave_up)) return false;
         const uint32_t bar = pair_full + 8 * stage, sa = ring + stage * S::kStageBytes, sb = sa + S::kABytes;
-        if (rank == 0) bar_expect(full + 8 * stage, CTAS * S::kStageBytes);
+        if (rank == 0) bar_expect(full + 8 * stage, CTAS * S::kStageBytes + p.extra);
         ++issued;
         const int wrow = pb * p.g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;  // plane of a packed weight
         if (P == kBack && t.weight) {
@@ -712,6 +713,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
 
 // ------------------------------------------------------------------ host side --
 
+thread_local int t_extra = 0;
+
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -825,6 +828,7 @@ cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int 
   a.tile_hi = hi;
   a.first = first;
   a.whole = whole;
+  a.extra = t_extra;
   a.want_dh = dh;
   a.want_dw = dw;
   a.dh_vec = reinterpret_cast<uintptr_t>(sh.dh) % 16 == 0 && sh.dh_ld * esize_of(dtype) % 16 == 0;
@@ -855,6 +859,8 @@ cudaError_t head_back(const HeadGeom& g, const HeadWork& w, const HeadShards& sh
                       bool first, bool whole, bool dh, bool dw, cudaStream_t s) {
   return run<kBack>(g, w, sh, dtype, tile_lo, tile_hi, first, whole, dh, dw, s);
 }
+
+void head_test_extra(int bytes) { t_extra = bytes; }
 
 cudaError_t head_read_fault(unsigned* fault) {
   cudaError_t e = cudaMemcpyFromSymbol(fault, g_head_fault, sizeof *fault);

@@ -45,7 +45,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 
 // Every wait of a product ends: when its barrier completes, when another warp of the CTA gave
 // up, or after kWaitNs. The slowest wait of a healthy run is one tile's products.
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kWaitNs = 500000000ull;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   if (bar_try(bar, parity)) return true;
   const uint64_t start = global_ns();
