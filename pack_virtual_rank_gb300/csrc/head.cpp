@@ -66,6 +66,7 @@ relay_status_t check_shape(const relay_head_t* h, int top, HeadGeom* g) {
   g->vocab = (int32_t)vocab;
   g->mpad = (int32_t)up(h->tokens, kHeadRowTile);
   g->tau = g->inv_tau = 1.0f;
+  g->ctas = g->tokens <= kHeadRowTile / 2 ? 1 : 2;  // one CTA's rows: the other would multiply padding
   return RELAY_OK;
 }
 
@@ -114,7 +115,8 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
   ar.tiles_per_piece = tiles;
   if ((dh || dw) && g.mpad > 0) {
     const int64_t cap = h.piece_bytes > 0 ? h.piece_bytes : RELAY_HEAD_PIECE_BYTES;
-    const int64_t per_tile = 2ll * planes * g.mpad * kHeadTile;
+    w.grad_planes = head_grad_planes(h.dtype, g.ctas);
+    const int64_t per_tile = 2ll * w.grad_planes * g.mpad * kHeadTile;
     ar.tiles_per_piece = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, cap / per_tile));
     ar.keep = ar.tiles_per_piece == tiles;
     w.grad_ld = (int64_t)ar.tiles_per_piece * kHeadTile;
@@ -125,6 +127,8 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
       const int64_t one = 4ll * g.mpad * w.dh_ld;
       w.tiles_per_piece = ar.tiles_per_piece;
       w.with_dw = dw;
+      w.whole = ar.keep && reinterpret_cast<uintptr_t>(h.d_hidden) % 16 == 0 &&
+                h.d_hidden_stride * esize_of(h.dtype) % 16 == 0;
       w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(ar.tiles_per_piece, 64), (256ll << 20) / one));
       w.dh = reinterpret_cast<float*>(l.take(one * w.splits));
     }
@@ -211,7 +215,6 @@ relay_status_t run_head(const relay_head_t& h, HeadGeom g, int top, const int32_
                         const void* teacher, int teacher_dtype, const float* row_weight, float* loss,
                         void* workspace, cudaStream_t stream) {
   g.sms = sm_count();
-  g.ctas = g.tokens <= kHeadRowTile / 2 ? 1 : 2;  // one CTA's rows: the other would multiply padding
   const uintptr_t base = (uintptr_t)up((int64_t)reinterpret_cast<uintptr_t>(workspace), 256);
   const Arrangement ar = arrange(h, g, top, base);
   const HeadWork& w = ar.w;
@@ -247,9 +250,9 @@ relay_status_t run_head(const relay_head_t& h, HeadGeom g, int top, const int32_
       RELAY_HEAD_TRY(head_scale(g, w, h.dtype, distill, loss, stream));
     else
       RELAY_HEAD_TRY(head_logits(g, w, sh, h.dtype, t, hi, kHeadGradient, stream));
-    RELAY_HEAD_TRY(head_back(g, w, sh, h.dtype, t, hi, t == 0, ar.keep, dh, dw, stream));
+    RELAY_HEAD_TRY(head_back(g, w, sh, h.dtype, t, hi, t == 0, dh, dw, stream));
   }
-  if (dh) RELAY_HEAD_TRY(head_write_dh(g, w, h.dtype, ar.keep, h.d_hidden, h.d_hidden_stride, stream));
+  if (dh) RELAY_HEAD_TRY(head_write_dh(g, w, h.dtype, h.d_hidden, h.d_hidden_stride, stream));
   return RELAY_OK;
 }
 

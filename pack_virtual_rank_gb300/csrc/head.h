@@ -68,6 +68,10 @@ int head_shard_of_tile(const HeadGeom& g, int tile) {
 // products of parts above 2^-24.
 constexpr int kHeadPlanesF32 = 3;
 inline int head_planes(int dtype) { return dtype == RELAY_F32 ? kHeadPlanesF32 : 1; }
+// Parts the gradient of a logit is held in. One bf16 value is as exact as the bf16 results want where
+// rounding errors average over many rows. Up to 128 rows they do not (a weight row's gradient may be
+// one token's), and d_weight's products wait for its writes, so that a second part there costs little.
+inline int head_grad_planes(int dtype, int ctas) { return dtype == RELAY_F32 ? kHeadPlanesF32 : ctas == 1 ? 2 : 1; }
 
 #ifdef __CUDACC__
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -91,13 +95,15 @@ struct HeadWork {
   float* ent_z;       // [tokens][top] the entries' logits / tau
   float2* part;       // [2 tiles][mpad] (max, sum of exp) of kHeadStatTile columns, log2 units
   float* lse;         // [mpad] log2 units
-  uint16_t* grad;     // [planes][mpad][grad_ld] of one piece: codes or exponentials, then the gradient
+  uint16_t* grad;     // [grad_planes][mpad][grad_ld] of one piece: codes or exponentials, then the gradient
+  int32_t grad_planes;
   int64_t grad_ld;    // columns per row
   float* dh;          // [splits][mpad][dh_ld] fp32 partial sums of d_hidden
   int32_t dh_ld;      // dim rounded up to 4
   int32_t splits;     // most cuts of the vocabulary d_hidden may take
   int32_t tiles_per_piece;
   int32_t with_dw;    // d_weight's tiles run beside d_hidden's
+  int32_t whole;      // one piece, and d_hidden's rows take 16-byte stores: uncut sums go straight there
 };
 
 // Cuts of the vocabulary for d_hidden, whose tiles alone are too few, or too long beside what else
@@ -166,16 +172,16 @@ cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, flo
 // as well: one launch less.
 bool head_scale_joins(const HeadGeom& g);
 cudaError_t head_scale(const HeadGeom& g, const HeadWork& w, int dtype, bool distill, float* loss, cudaStream_t s);
-cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, bool whole, void* d_hidden,
+cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, void* d_hidden,
                           int64_t d_hidden_ld, cudaStream_t s);
 
 // head_gemm.cu
 enum HeadLogits { kHeadStats, kHeadStatsKeep, kHeadGradient };
 cudaError_t head_logits(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
                         int tile_lo, int tile_hi, HeadLogits mode, cudaStream_t s);
-// d_hidden and d_weight of one piece, either or both. first: the first piece; whole: the only one.
+// d_hidden and d_weight of one piece, either or both. first: the first piece.
 cudaError_t head_back(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo, int tile_hi,
-                      bool first, bool whole, bool dh, bool dw, cudaStream_t s);
+                      bool first, bool dh, bool dw, cudaStream_t s);
 // Makes the calling thread's next products wait for `bytes` more than their loads bring.
 void head_test_extra(int bytes);
 // Reads and clears the products' fault word.

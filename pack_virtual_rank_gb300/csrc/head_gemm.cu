@@ -27,6 +27,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device.cuh"
 #include "head.h"
@@ -74,7 +75,7 @@ enum Product { kStats, kStatsKeep, kGradient, kBack };
 // 64-bit value as an fp32 sum. Chains of 32 products (48 for the six products of fp32 parts)
 // are as close as that sum. A result that is rounded to bf16 does not show the drift.
 template <int P, int PLANES>
-constexpr int kChain = PLANES > 1 ? 2 : P == kBack ? INT_MAX : 8;
+constexpr int kChain = PLANES == 3 ? 2 : P == kBack ? INT_MAX : 8;
 
 struct GemmArgs {
   CUtensorMap a;                         // first operand: hidden (logits), gradient
@@ -90,8 +91,7 @@ struct GemmArgs {
   int32_t tile_lo, tile_hi;
   int32_t want_dh, want_dw;
   int32_t first;     // d_hidden: overwrite the partial sums
-  int32_t whole;     // d_hidden: the only piece; an uncut sum goes straight to its row
-  int32_t dh_vec;    // d_hidden's rows take 16-byte stores
+  int32_t whole;     // d_hidden: an uncut sum goes straight to its row (HeadWork.whole)
   int32_t out_map;   // d_weight: its rows can be stored through tensor maps
   int32_t group;     // logits: row tiles walked together before the next column tile
 };
@@ -214,9 +214,18 @@ __device__ __forceinline__ bool for_steps(const GemmArgs& p, const Item& t, F f)
 
 // Pairs of parts whose products make up an fp32 product.
 template <int PLANES>
-constexpr int kPairs = PLANES == 1 ? 1 : 6;
-__device__ __forceinline__ int pair_a(int i) { return (0x200110 >> (4 * (5 - i))) & 15; }  // 2 0 0 1 1 0
-__device__ __forceinline__ int pair_b(int i) { return (0x021010 >> (4 * (5 - i))) & 15; }  // 0 2 1 0 1 0
+constexpr int kPairs = PLANES == 3 ? 6 : PLANES;
+// PLANES 3: 2 0 0 1 1 0 with 0 2 1 0 1 0, small products first. PLANES 2 (gradient only): 1 0 with 0 0
+// for d_weight, and the second alone for d_hidden, whose products are not hidden behind writes: 16 rows,
+// 4096 x 131072 take 645 us with one part, 679 with two for d_weight, 865 with two for both.
+template <int PLANES>
+__device__ __forceinline__ int pair_a(int i) {
+  return PLANES == 1 ? 0 : PLANES == 2 ? 1 - i : (0x200110 >> (4 * (5 - i))) & 15;
+}
+template <int PLANES>
+__device__ __forceinline__ int pair_b(int i) { return PLANES < 3 ? 0 : (0x021010 >> (4 * (5 - i))) & 15; }
+template <int PLANES>
+__device__ __forceinline__ int first_pair(const Item& t) { return PLANES == 2 && !t.weight ? 1 : 0; }
 
 // full: the stage barriers of the pair's first CTA; empty: this CTA's own.
 template <int P, int PLANES, int CTAS>
@@ -232,8 +241,8 @@ __device__ void produce(const GemmArgs& p, const Schedule& sched, int live, int 
   for (int slot = 0, i; ok && (i = sched.at(slot)) >= 0; ++slot) {
     const Item t = item_at<P, CTAS>(p, sched, live, rank, i);
     ok = for_steps<P>(p, t, [&](int k, int k_shard, int k_v) {
-      for (int pair = 0; pair < kPairs<PLANES>; ++pair) {
-        const int pa = PLANES == 1 ? 0 : pair_a(pair), pb = PLANES == 1 ? 0 : pair_b(pair);
+      for (int pair = first_pair<PLANES>(t); pair < kPairs<PLANES>; ++pair) {
+        const int pa = pair_a<PLANES>(pair), pb = pair_b<PLANES>(pair);
         if (!bar_wait(empty + 8 * stage, phase ^ 1, gave_up)) return false;
         const uint32_t bar = pair_full + 8 * stage, sa = ring + stage * S::kStageBytes, sb = sa + S::kABytes;
         if (rank == 0) bar_expect(full + 8 * stage, CTAS * S::kStageBytes + p.extra);
@@ -312,7 +321,7 @@ __device__ void multiply(const GemmArgs& p, const Schedule& sched, int live, uin
         if (!open()) return false;
       }
       const uint32_t acc = tmem + (n & 1) * kBN;
-      for (int pair = 0; pair < kPairs<PLANES>; ++pair) {
+      for (int pair = first_pair<PLANES>(t); pair < kPairs<PLANES>; ++pair) {
         if (!bar_wait(full + 8 * stage, phase, gave_up)) return false;
         tc_fence_after();
         const uint32_t sa = ring + stage * S::kStageBytes;
@@ -320,7 +329,7 @@ __device__ void multiply(const GemmArgs& p, const Schedule& sched, int live, uin
 #pragma unroll
         for (int k = 0; k < kBK / 16; ++k)
           tc_product<CTAS>(acc, da + k * operand_step(a_outer), db + k * operand_step(kBOuter), desc,
-                     in_chain > 0 || pair > 0 || k > 0);
+                     in_chain > 0 || pair > first_pair<PLANES>(t) || k > 0);
         tc_commit<CTAS>(empty + 8 * stage);
         if (++stage == Shape<CTAS>::kStages) {
           stage = 0;
@@ -483,8 +492,8 @@ __device__ __forceinline__ void finish_logits(const GemmArgs& p, const Item& t, 
         sum[j & 3] += v[j];
       }
       if (P == kStatsKeep) {
-#pragma unroll
-        for (int i = 0; i < PLANES; ++i) store_part(out, v, &p.c[0], x, i * p.g.mpad + y, kMine);
+#pragma unroll 1
+        for (int i = 0; i < p.w.grad_planes; ++i) store_part(out, v, &p.c[0], x, i * p.g.mpad + y, kMine);
       }
     }
     p.w.part[(int64_t)(t.tile * 2 + part) * p.g.mpad + row] =
@@ -502,8 +511,8 @@ __device__ __forceinline__ void finish_logits(const GemmArgs& p, const Item& t, 
     for (int j = 0; j < kMine; ++j) v[j] -= j == at ? d : 0.0f;
     e.step();
   }
-#pragma unroll
-  for (int i = 0; i < PLANES; ++i) store_part(out, v, &p.c[0], x, i * p.g.mpad + y, kMine);
+#pragma unroll 1
+  for (int i = 0; i < p.w.grad_planes; ++i) store_part(out, v, &p.c[0], x, i * p.g.mpad + y, kMine);
 }
 
 template <int PLANES>
@@ -532,12 +541,12 @@ __device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t,
     return;
   }
   if (row >= live) return;
-  if (PLANES == 1) {
+  if (PLANES < 3) {
     uint16_t* to = static_cast<uint16_t*>(p.sh.dh) + p.w.perm[row] * p.sh.dh_ld + d0;
 #pragma unroll
     for (int j = 0; j < kMine; j += 8) {
       if (j >= valid) break;
-      if (p.dh_vec && j + 8 <= valid) {
+      if (j + 8 <= valid) {
         *reinterpret_cast<uint4*>(to + j) = TBF16::pack(v + j);
       } else {
 #pragma unroll
@@ -551,7 +560,7 @@ __device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t,
   float* to = static_cast<float*>(p.sh.dh) + p.w.perm[row] * p.sh.dh_ld + d0;
 #pragma unroll
   for (int j = 0; j < kMine; j += 4) {
-    if (p.dh_vec && j + 4 <= valid) {
+    if (j + 4 <= valid) {
       *reinterpret_cast<float4*>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     } else {
 #pragma unroll
@@ -561,40 +570,60 @@ __device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t,
   }
 }
 
+// The staging buffer's 32 rows (128 bytes of each) to rows no tensor map can store: row by row, with
+// neighbouring lanes on neighbouring elements. Rare, and kept out of the unrolled path.
+template <class T>
+__device__ __noinline__ void copy_rows(uint32_t buf, T* to, int64_t ld, int rows, int columns) {
+  __syncwarp();
+  for (int r = 0; r < rows; ++r, to += ld)
+    for (int e = threadIdx.x % 32; e < columns; e += 32) {
+      const uint32_t at = buf + r * 128 + (((e * (int)sizeof(T) / 16) ^ (r & 7)) << 4) + e * (int)sizeof(T) % 16;
+      if constexpr (sizeof(T) == 2) {
+        uint16_t x;
+        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
+        to[e] = x;
+      } else {
+        uint32_t x;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+        to[e] = __uint_as_float(x);
+      }
+    }
+  __syncwarp();
+}
+
 template <int PLANES>
 __device__ __forceinline__ void finish_dweight(const GemmArgs& p, const Item& t, float (&v)[kMine], int quarter,
                                                int part, Stager& out) {
-  const int r0 = t.v0 + quarter * 32, row = r0 + threadIdx.x % 32, d0 = t.col0 + part * kMine;
+  using T = std::conditional_t<PLANES == 3, float, uint16_t>;
+  constexpr int kCols = 128 / (int)sizeof(T);
+  const int r0 = t.v0 + quarter * 32, d0 = t.col0 + part * kMine;
   const int rows = p.g.rows[t.shard], valid = p.g.dim - d0;
   if (r0 >= rows || valid <= 0) return;
   if (t.k_hi == 0) {  // no live row: nothing was multiplied
 #pragma unroll
     for (int j = 0; j < kMine; ++j) v[j] = 0.0f;
   }
-  if (PLANES == 1 && p.out_map) {
-    store_part(out, v, &p.c[t.shard], d0, r0, valid);
-    return;
-  }
-  if (row >= rows) return;
-  const int64_t at = (int64_t)row * p.sh.dw_ld + d0;
-  if (PLANES == 1) {
-    uint16_t* to = static_cast<uint16_t*>(p.sh.dw[t.shard]) + at;
+  // 128 bytes of each of the warp's 32 rows at a time
 #pragma unroll
-    for (int j = 0; j < kMine; ++j)
-      if (j < valid) to[j] = (uint16_t)(bf16x2_rn(v[j], 0.0f) & 0xffffu);
-  } else {
-    float* to = static_cast<float*>(p.sh.dw[t.shard]) + at;
-    const bool vec = p.out_map != 0;
+  for (int c = 0; c < kMine; c += kCols) {
+    if (c >= valid) break;
+    out.open();
 #pragma unroll
-    for (int j = 0; j < kMine; j += 4) {
-      if (vec && j + 4 <= valid) {
-        *reinterpret_cast<float4*>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (PLANES < 3) {
+        const int i = c + 8 * j;
+        out.put(j, bf16x2_rn(v[i], v[i + 1]), bf16x2_rn(v[i + 2], v[i + 3]), bf16x2_rn(v[i + 4], v[i + 5]),
+                bf16x2_rn(v[i + 6], v[i + 7]));
       } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (j + i < valid) to[j + i] = v[j + i];
+        const int i = c + 4 * j;
+        out.put(j, __float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
       }
     }
+    if (p.out_map)
+      out.close(&p.c[t.shard], d0 + c, r0);
+    else
+      copy_rows<T>(out.buf, static_cast<T*>(p.sh.dw[t.shard]) + r0 * p.sh.dw_ld + d0 + c, p.sh.dw_ld, min(32, rows - r0),
+                   min(kCols, valid - c));
   }
 }
 
@@ -764,7 +793,7 @@ bool maps_for(GemmArgs* a, int dtype) {
         }
     }
   };
-  const int64_t grad_rows = (int64_t)planes * g.mpad;
+  const int64_t hid_rows = (int64_t)planes * g.mpad, grad_rows = (int64_t)w.grad_planes * g.mpad;
   if (P == kBack) {
     ok &= matrix_map(&a->a, w.grad, grad_rows, w.grad_ld, w.grad_ld, kBK);
     if (a->want_dh) {
@@ -774,20 +803,20 @@ bool maps_for(GemmArgs* a, int dtype) {
     }
     if (a->want_dw) {
       a->maps |= 1 << kHid;
-      ok &= matrix_map(&a->hid, w.hid, grad_rows, g.dim, w.dim_pad, kBK);
+      ok &= matrix_map(&a->hid, w.hid, hid_rows, g.dim, w.dim_pad, kBK);
       a->out_map = 1;
       for (int s = 0; s < g.A; ++s)
         if (g.rows[s] > 0)
           a->out_map &= reinterpret_cast<uintptr_t>(a->sh.dw[s]) % 16 == 0 && a->sh.dw_ld * esize_of(dtype) % 16 == 0;
-      if (planes == 1 && a->out_map)
+      if (a->out_map)
         for (int s = 0; s < g.A; ++s)
           if (g.rows[s] > 0) {
             a->maps |= 1 << (kC + s);
-            ok &= matrix_map(&a->c[s], a->sh.dw[s], g.rows[s], g.dim, a->sh.dw_ld, 32);
+            ok &= matrix_map(&a->c[s], a->sh.dw[s], g.rows[s], g.dim, a->sh.dw_ld, 32, planes == 3);
           }
     }
   } else {
-    ok &= matrix_map(&a->a, w.hid, grad_rows, g.dim, w.dim_pad, kBM);
+    ok &= matrix_map(&a->a, w.hid, hid_rows, g.dim, w.dim_pad, kBM);
     weight(kBN / g.ctas);
     if (P != kStats) {
       a->maps |= 1 << kC;
@@ -819,7 +848,7 @@ cudaError_t launch(const GemmArgs& a, int64_t items, cudaStream_t s) {
 
 template <int P>
 cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int lo, int hi, bool first,
-                bool whole, bool dh, bool dw, cudaStream_t s) {
+                bool dh, bool dw, cudaStream_t s) {
   GemmArgs a{};
   a.g = g;
   a.w = w;
@@ -827,11 +856,10 @@ cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int 
   a.tile_lo = lo;
   a.tile_hi = hi;
   a.first = first;
-  a.whole = whole;
+  a.whole = w.whole;
   a.extra = t_extra;
   a.want_dh = dh;
   a.want_dw = dw;
-  a.dh_vec = reinterpret_cast<uintptr_t>(sh.dh) % 16 == 0 && sh.dh_ld * esize_of(dtype) % 16 == 0;
   // row tiles whose packed hidden rows take 64 MiB, half of L2
   const int rows = kBM * g.ctas;
   const int64_t mt = (g.tokens + rows - 1) / rows, tiles = hi - lo, nd = (g.dim + kBN - 1) / kBN;
@@ -839,9 +867,15 @@ cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int 
   if (!maps_for<P>(&a, dtype)) return cudaErrorInvalidValue;
   const int64_t items = P == kBack ? (dh ? mt * nd * w.splits : 0) + (dw ? tiles * (kHeadTile / rows) * nd : 0) : mt * tiles;
   if (items > INT_MAX) return cudaErrorInvalidValue;
-  if (g.ctas == 1)
-    return dtype == RELAY_BF16 ? launch<P, 1, 1>(a, items, s) : launch<P, kHeadPlanesF32, 1>(a, items, s);
-  return dtype == RELAY_BF16 ? launch<P, 1, 2>(a, items, s) : launch<P, kHeadPlanesF32, 2>(a, items, s);
+  if constexpr (P == kBack) {
+    if (dtype == RELAY_BF16) return g.ctas == 1 ? launch<P, 2, 1>(a, items, s) : launch<P, 1, 2>(a, items, s);
+    return g.ctas == 1 ? launch<P, kHeadPlanesF32, 1>(a, items, s) : launch<P, kHeadPlanesF32, 2>(a, items, s);
+  }
+  if constexpr (P != kBack) {
+    if (g.ctas == 1)
+      return dtype == RELAY_BF16 ? launch<P, 1, 1>(a, items, s) : launch<P, kHeadPlanesF32, 1>(a, items, s);
+    return dtype == RELAY_BF16 ? launch<P, 1, 2>(a, items, s) : launch<P, kHeadPlanesF32, 2>(a, items, s);
+  }
 }
 
 }  // namespace
@@ -849,15 +883,15 @@ cudaError_t run(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int 
 cudaError_t head_logits(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo,
                         int tile_hi, HeadLogits mode, cudaStream_t s) {
   switch (mode) {
-    case kHeadStats: return run<kStats>(g, w, sh, dtype, tile_lo, tile_hi, false, false, false, false, s);
-    case kHeadStatsKeep: return run<kStatsKeep>(g, w, sh, dtype, tile_lo, tile_hi, false, false, false, false, s);
-    default: return run<kGradient>(g, w, sh, dtype, tile_lo, tile_hi, false, false, false, false, s);
+    case kHeadStats: return run<kStats>(g, w, sh, dtype, tile_lo, tile_hi, false, false, false, s);
+    case kHeadStatsKeep: return run<kStatsKeep>(g, w, sh, dtype, tile_lo, tile_hi, false, false, false, s);
+    default: return run<kGradient>(g, w, sh, dtype, tile_lo, tile_hi, false, false, false, s);
   }
 }
 
 cudaError_t head_back(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, int tile_lo, int tile_hi,
-                      bool first, bool whole, bool dh, bool dw, cudaStream_t s) {
-  return run<kBack>(g, w, sh, dtype, tile_lo, tile_hi, first, whole, dh, dw, s);
+                      bool first, bool dh, bool dw, cudaStream_t s) {
+  return run<kBack>(g, w, sh, dtype, tile_lo, tile_hi, first, dh, dw, s);
 }
 
 void head_test_extra(int bytes) { t_extra = bytes; }

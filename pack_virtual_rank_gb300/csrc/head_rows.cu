@@ -67,7 +67,30 @@ __device__ __forceinline__ void parts_of(float v, uint16_t (&o)[3]) {
 // apart. Columns from dim to pad, and all of them when from is NULL, are 0. vec: 16-byte loads.
 __device__ __forceinline__ void pack_row(uint16_t* to, int64_t, const uint16_t* from, int dim, int pad, bool vec) {
   const int lane = threadIdx.x % 32;
-  const int vecs = from == nullptr ? pad / 8 : vec ? dim / 8 : 0;
+  if (from != nullptr && !vec) {
+    // rows off the 16-byte grid: each output vector out of the two aligned blocks that hold it (a block
+    // is read only where it holds bytes of the row)
+    const uintptr_t at = reinterpret_cast<uintptr_t>(from);
+    const unsigned shift = at & 15u;
+    const unsigned char* base = reinterpret_cast<const unsigned char*>(at - shift);
+    const int bytes = dim * 2 + (int)shift;
+    for (int v = lane; v < pad / 8; v += 32) {
+      const uint4 lo = v * 16 < bytes ? ld_once(base + v * 16) : make_uint4(0, 0, 0, 0);
+      const uint4 hi = shift != 0 && v * 16 + 16 < bytes ? ld_once(base + v * 16 + 16) : make_uint4(0, 0, 0, 0);
+      uint4 x = shift_pair(lo, hi, shift);
+      if (v * 8 + 8 > dim) {  // past the row: 0
+        uint16_t e[8];
+        memcpy(e, &x, 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (v * 8 + i >= dim) e[i] = 0;
+        memcpy(&x, e, 16);
+      }
+      reinterpret_cast<uint4*>(to)[v] = x;
+    }
+    return;
+  }
+  const int vecs = from == nullptr ? pad / 8 : dim / 8;
   for (int v0 = lane; v0 < vecs; v0 += 4 * 32) {
     uint4 x[4];
 #pragma unroll
@@ -424,11 +447,10 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(__fadd_rn(y[j], x[j]), v[j]) * f;
     }
-#pragma unroll
-    for (int i = 0; i < PLANES; ++i) {
+    for (int i = 0; i < w.grad_planes; ++i) {
       const uint4 out = TBF16::pack(v);
       *reinterpret_cast<uint4*>(line + i * plane + col) = out;
-      if (i + 1 == PLANES) break;
+      if (i + 1 == w.grad_planes) break;
       float r[8];
       TBF16::unpack(out, r);
 #pragma unroll
@@ -443,8 +465,7 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
     float q = 0.0f;  // an id given several times: its first entry sums them
     for (int j = k; j < g.top && w.ent_col[at + j] == c; ++j) q += w.ent_q[at + j];
     float v = weight * (exp2f(fmaf(ent_z, 1.4426950408889634f, -lse)) - q);
-#pragma unroll
-    for (int i = 0; i < PLANES; ++i) {
+    for (int i = 0; i < w.grad_planes; ++i) {
       const uint32_t r = bf16x2_rn(v, 0.0f) & 0xffffu;
       line[i * plane + c] = (uint16_t)r;
       v = __fsub_rn(v, __uint_as_float(r << 16));
@@ -456,11 +477,11 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
 // product wrote itself (one cut, one piece) need nothing.
 template <class T>
 __global__ void __launch_bounds__(kThreadsRows)
-    write_dh_kernel(const HeadGeom g, const HeadWork w, T* dh, int64_t ld, int whole, int vec) {
+    write_dh_kernel(const HeadGeom g, const HeadWork w, T* dh, int64_t ld, int vec) {
   dep_launch();
   dep_wait();
   const int live = *w.n_live, cuts = head_cuts(g, w, live);
-  if (whole && cuts == 1) return;
+  if (w.whole && cuts == 1) return;
   const int64_t cut = (int64_t)g.mpad * w.dh_ld;
   constexpr int kLanes = 4;
   const int64_t vecs = vec ? (int64_t)live * (g.dim / kLanes) : 0;
@@ -555,7 +576,7 @@ cudaError_t head_scale(const HeadGeom& g, const HeadWork& w, int dtype, bool dis
   return dtype == RELAY_BF16 ? scale_typed<1>(g, w, distill, loss, s) : scale_typed<kHeadPlanesF32>(g, w, distill, loss, s);
 }
 
-cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, bool whole, void* d_hidden,
+cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, void* d_hidden,
                           int64_t d_hidden_ld, cudaStream_t s) {
   const int64_t work = (int64_t)g.tokens * ceil_div(g.dim, 4);
   const int blocks = (int)(work < 2432ll * kThreadsRows ? (work + kThreadsRows - 1) / kThreadsRows : 2432);  // 16 per SM
@@ -563,9 +584,9 @@ cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, bool 
                   reinterpret_cast<uintptr_t>(d_hidden) % (4 * esize(dtype)) == 0;
   if (dtype == RELAY_BF16)
     return launch_chained(write_dh_kernel<uint16_t>, blocks, kThreadsRows, 0, s, g, w, static_cast<uint16_t*>(d_hidden),
-                          d_hidden_ld, (int)whole, vec);
+                          d_hidden_ld, vec);
   return launch_chained(write_dh_kernel<float>, blocks, kThreadsRows, 0, s, g, w, static_cast<float*>(d_hidden),
-                        d_hidden_ld, (int)whole, vec);
+                        d_hidden_ld, vec);
 }
 
 }  // namespace relay
