@@ -250,3 +250,24 @@ def test_captures_into_a_graph(dtype):
     out = c.finish()
     for name in want:
         assert torch.equal(out[name], want[name]), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [1, 7, 128, 129])
+@pytest.mark.parametrize("offset,extra", [(0, 0), (0, 8), (1, 0)])
+def test_loss_alone(tokens, offset, extra, dtype):
+    """Scoring without gradients, ignored rows full of NaN among the scored ones."""
+    g, h, ws, rw = inputs(tokens, 136, [300, 0, 41], dtype, 12)
+    t = targets(g, tokens, 341, 0.4 if tokens > 1 else 0.0)
+    index = torch.randint(-1, 341, (tokens, 9), generator=g, dtype=torch.int32)
+    index[::4] = -1 if tokens > 1 else 5
+    logits = torch.randn(tokens, 9, generator=g)
+    hard, soft = ref.head(h, ws, t[:, None], None, rw, 1.0), ref.head(h, ws, index, logits, rw, 3.0)
+    dead = (t < 0) | (t >= 341)
+    h1, h2 = h.clone(), h.clone()
+    h1[dead] = math.nan
+    h2[(index < 0).all(dim=1)] = math.inf
+    out = Call(h1, ws, rw, grads=False, offset=offset, extra=extra).xent(t)
+    check(out, hard)
+    assert bool((out["loss"][dead] == 0).all())
+    check(Call(h2, ws, rw, grads=False, offset=offset, extra=extra).distill(logits, index, 3.0), soft)
