@@ -398,7 +398,8 @@ typedef struct relay_head {
 } relay_head_t;
 
 /* Bytes of workspace (device memory, any alignment, contents unspecified before and after)
- * the two calls below need. top: 0 for relay_linear_xent, else the K of
+ * the two calls below need; it depends on the gradients wanted, the strides and the weights' alignment
+ * (rows off a 16-byte boundary, and fp32 rows, are copied). top: 0 for relay_linear_xent, else the K of
  * relay_linear_distill. -1 on an invalid head (relay_last_error says why). */
 int64_t relay_head_workspace_size(const relay_head_t* head, int top);
 

@@ -118,7 +118,7 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
     w.grad_planes = head_grad_planes(h.dtype, g.ctas);
     const int64_t per_tile = 2ll * w.grad_planes * g.mpad * kHeadTile;
     ar.tiles_per_piece = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, cap / per_tile));
-    ar.keep = ar.tiles_per_piece == tiles;
+    ar.keep = ar.tiles_per_piece == tiles && head_scale_fits(g);
     w.grad_ld = (int64_t)ar.tiles_per_piece * kHeadTile;
     w.grad = reinterpret_cast<uint16_t*>(l.take(per_tile * ar.tiles_per_piece));
     if (dh) {
@@ -220,6 +220,10 @@ relay_status_t run_head(const relay_head_t& h, HeadGeom g, int top, const int32_
   const HeadWork& w = ar.w;
   const bool distill = top > 0, dh = h.d_hidden != nullptr, dw = wants_dw(h);
   const int tiles = g.tile0[RELAY_HEAD_MAX_SHARDS];
+  // rows of every plane are numbered in 32 bits
+  const int64_t planes = std::max(head_planes(h.dtype), w.grad_planes);
+  if (planes * g.mpad > INT32_MAX || (w.wpack != nullptr && planes * tiles * kHeadTile > INT32_MAX))
+    return report_error(RELAY_ERR_UNSUPPORTED, "relay_head: more than 2^31 - 1 rows over all parts of an fp32 value");
   HeadShards sh{};
   for (int a = 0; a < h.A; ++a) {
     sh.w[a] = h.weight[a];

@@ -171,6 +171,7 @@ cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, flo
 // Kept exponentials to the gradient. Where a row is short (head_scale_joins) it does head_combine's work
 // as well: one launch less.
 bool head_scale_joins(const HeadGeom& g);
+bool head_scale_fits(const HeadGeom& g);  // in one launch
 cudaError_t head_scale(const HeadGeom& g, const HeadWork& w, int dtype, bool distill, float* loss, cudaStream_t s);
 cudaError_t head_write_dh(const HeadGeom& g, const HeadWork& w, int dtype, void* d_hidden,
                           int64_t d_hidden_ld, cudaStream_t s);

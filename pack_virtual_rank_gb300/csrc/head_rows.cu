@@ -564,6 +564,7 @@ cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, flo
                         32 * kCombineWarps, 0, s, g, w, loss);
 }
 
+bool head_scale_fits(const HeadGeom& g) { return ceil_div(g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile, kScaleCols) <= 65535; }
 bool head_scale_joins(const HeadGeom& g) { return g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile <= kScaleCols; }
 
 template <int PLANES>

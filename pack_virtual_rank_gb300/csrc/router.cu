@@ -519,6 +519,16 @@ relay_status_t check_spans(const Span* s, int n) {
 }
 bool off(const void* p, uintptr_t e) { return reinterpret_cast<uintptr_t>(p) % e != 0; }
 
+// C++ exceptions (an allocation that fails) end here, not in a C caller.
+template <class F>
+relay_status_t guarded(F f) {
+  try {
+    return f();
+  } catch (...) {
+    return RELAY_ERR_CUDA;
+  }
+}
+
 }  // namespace
 }  // namespace relay
 
@@ -527,7 +537,7 @@ extern "C" {
 int64_t relay_router_workspace_size(int64_t tokens, int experts) {
   using namespace relay;
   if (tokens < 0 || tokens > INT32_MAX || experts < 1 || experts > RELAY_ROUTER_MAX_EXPERTS) {
-    bad("tokens or experts out of range");
+    guarded([] { return bad("tokens or experts out of range"); });
     return -1;
   }
   return forward_blocks(tokens, kRouterWarps) * experts * 8 + 16;  // a row to a warp: the most blocks
@@ -539,66 +549,70 @@ relay_status_t relay_router_forward(const void* logits, int64_t row_stride, rela
                                     int32_t* counts, float* prob_sum, void* workspace,
                                     int64_t workspace_bytes, cudaStream_t stream) {
   using namespace relay;
-  relay_status_t st = check_shape(dtype, tokens, experts, top);
-  if (st != RELAY_OK) return st;
-  if (counts == nullptr || prob_sum == nullptr) return bad("counts or prob_sum is NULL");
-  if (tokens > 0 && (logits == nullptr || index == nullptr || gate == nullptr))
-    return bad("logits, index or gate is NULL");
-  if (tokens > 0 && (row_stride < experts || row_stride > (1ll << 31))) return bad("row_stride is less than experts or more than 2^31");
-  const int E = esize_of(dtype);
-  if (off(logits, E) || off(index, 4) || off(gate, 4) || off(counts, 4) || off(prob_sum, 4))
-    return bad("an array is not element-aligned");
-  const int64_t need = relay_router_workspace_size(tokens, experts);
-  if (workspace == nullptr) return bad("workspace is NULL");
-  if (workspace_bytes < need)
-    return bad("the workspace holds " + std::to_string(workspace_bytes) + " bytes, " + std::to_string(need) + " are needed");
-  const Span s[] = {span(logits, tokens ? ((tokens - 1) * row_stride + experts) * E : 0, "logits", false),
-                    span(mask, tokens, "mask", false),
-                    span(index, tokens * top * 4, "index", true),
-                    span(gate, tokens * top * 4, "gate", true),
-                    span(counts, experts * 4, "counts", true),
-                    span(prob_sum, experts * 4, "prob_sum", true),
-                    span(workspace, need, "workspace", true)};
-  st = check_spans(s, 7);
-  if (st != RELAY_OK) return st;
-  int rows = kRouterWarps;
-  by_width(experts, top, [&](auto, auto l) {
-    rows *= 32 / decltype(l)::value;
-    return cudaSuccess;
+  return guarded([&]() -> relay_status_t {
+    relay_status_t st = check_shape(dtype, tokens, experts, top);
+    if (st != RELAY_OK) return st;
+    if (counts == nullptr || prob_sum == nullptr) return bad("counts or prob_sum is NULL");
+    if (tokens > 0 && (logits == nullptr || index == nullptr || gate == nullptr))
+      return bad("logits, index or gate is NULL");
+    if (tokens > 0 && (row_stride < experts || row_stride > (1ll << 31))) return bad("row_stride is less than experts or more than 2^31");
+    const int E = esize_of(dtype);
+    if (off(logits, E) || off(index, 4) || off(gate, 4) || off(counts, 4) || off(prob_sum, 4))
+      return bad("an array is not element-aligned");
+    const int64_t need = relay_router_workspace_size(tokens, experts);
+    if (workspace == nullptr) return bad("workspace is NULL");
+    if (workspace_bytes < need)
+      return bad("the workspace holds " + std::to_string(workspace_bytes) + " bytes, " + std::to_string(need) + " are needed");
+    const Span s[] = {span(logits, tokens ? ((tokens - 1) * row_stride + experts) * E : 0, "logits", false),
+                      span(mask, tokens, "mask", false),
+                      span(index, tokens * top * 4, "index", true),
+                      span(gate, tokens * top * 4, "gate", true),
+                      span(counts, experts * 4, "counts", true),
+                      span(prob_sum, experts * 4, "prob_sum", true),
+                      span(workspace, need, "workspace", true)};
+    st = check_spans(s, 7);
+    if (st != RELAY_OK) return st;
+    int rows = kRouterWarps;
+    by_width(experts, top, [&](auto, auto l) {
+      rows *= 32 / decltype(l)::value;
+      return cudaSuccess;
+    });
+    const int blocks = (int)forward_blocks(tokens, rows);
+    int32_t* part_count = reinterpret_cast<int32_t*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~(uintptr_t)15);
+    float* part_prob = reinterpret_cast<float*>(part_count + (int64_t)blocks * experts);
+    const ForwardArgs a{logits, row_stride, tokens, experts, top, normalize, load_bytes(logits, row_stride, E, experts),
+                        mask, index, gate,
+                        blocks == 1 ? counts : part_count, blocks == 1 ? prob_sum : part_prob};
+    cudaError_t e = by_width(experts, top, [&](auto n, auto l) {
+      constexpr int N = decltype(n)::value, L = decltype(l)::value;
+      const size_t smem = (size_t)(kRouterWarps * (32 / L) + 1) * experts * 4;
+      return launch_chained(dtype == RELAY_BF16 ? router_forward_kernel<uint16_t, N, L> : router_forward_kernel<float, N, L>,
+                            blocks, kRouterThreads, smem, stream, a);
+    });
+    if (e == cudaSuccess && blocks > 1) {
+      e = launch_chained(router_join_kernel, (experts + 7) / 8, 32 * kJoinWarps, 0, stream, part_count, part_prob, blocks,
+                         experts, counts, prob_sum);
+    }
+    return done(e);
   });
-  const int blocks = (int)forward_blocks(tokens, rows);
-  int32_t* part_count = reinterpret_cast<int32_t*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~(uintptr_t)15);
-  float* part_prob = reinterpret_cast<float*>(part_count + (int64_t)blocks * experts);
-  const ForwardArgs a{logits, row_stride, tokens, experts, top, normalize, load_bytes(logits, row_stride, E, experts),
-                      mask, index, gate,
-                      blocks == 1 ? counts : part_count, blocks == 1 ? prob_sum : part_prob};
-  cudaError_t e = by_width(experts, top, [&](auto n, auto l) {
-    constexpr int N = decltype(n)::value, L = decltype(l)::value;
-    const size_t smem = (size_t)(kRouterWarps * (32 / L) + 1) * experts * 4;
-    return launch_chained(dtype == RELAY_BF16 ? router_forward_kernel<uint16_t, N, L> : router_forward_kernel<float, N, L>,
-                          blocks, kRouterThreads, smem, stream, a);
-  });
-  if (e == cudaSuccess && blocks > 1) {
-    e = launch_chained(router_join_kernel, (experts + 7) / 8, 32 * kJoinWarps, 0, stream, part_count, part_prob, blocks,
-                       experts, counts, prob_sum);
-  }
-  return done(e);
 }
 
 relay_status_t relay_balance_loss(const int32_t* counts, const float* prob_sum, int experts, int top,
                                   float coef, float* loss, float* d_prob, cudaStream_t stream) {
   using namespace relay;
-  relay_status_t st = check_shape(RELAY_F32, 0, experts, top);
-  if (st != RELAY_OK) return st;
-  if (counts == nullptr || prob_sum == nullptr || loss == nullptr || d_prob == nullptr)
-    return bad("counts, prob_sum, loss or d_prob is NULL");
-  if (off(counts, 4) || off(prob_sum, 4) || off(loss, 4) || off(d_prob, 4)) return bad("an array is not element-aligned");
-  const Span s[] = {span(counts, experts * 4, "counts", false), span(prob_sum, experts * 4, "prob_sum", false),
-                    span(loss, 4, "loss", true), span(d_prob, experts * 4, "d_prob", true)};
-  st = check_spans(s, 4);
-  if (st != RELAY_OK) return st;
-  return done(launch_chained(balance_kernel, 1, kBalanceThreads, 0, stream, counts, prob_sum, experts, top, coef, loss,
-                             d_prob));
+  return guarded([&]() -> relay_status_t {
+    relay_status_t st = check_shape(RELAY_F32, 0, experts, top);
+    if (st != RELAY_OK) return st;
+    if (counts == nullptr || prob_sum == nullptr || loss == nullptr || d_prob == nullptr)
+      return bad("counts, prob_sum, loss or d_prob is NULL");
+    if (off(counts, 4) || off(prob_sum, 4) || off(loss, 4) || off(d_prob, 4)) return bad("an array is not element-aligned");
+    const Span s[] = {span(counts, experts * 4, "counts", false), span(prob_sum, experts * 4, "prob_sum", false),
+                      span(loss, 4, "loss", true), span(d_prob, experts * 4, "d_prob", true)};
+    st = check_spans(s, 4);
+    if (st != RELAY_OK) return st;
+    return done(launch_chained(balance_kernel, 1, kBalanceThreads, 0, stream, counts, prob_sum, experts, top, coef, loss,
+                               d_prob));
+  });
 }
 
 relay_status_t relay_router_backward(const void* logits, int64_t row_stride, relay_dtype_t dtype,
@@ -606,31 +620,33 @@ relay_status_t relay_router_backward(const void* logits, int64_t row_stride, rel
                                      const int32_t* index, const float* d_gate, const float* d_prob,
                                      void* d_logits, int64_t d_row_stride, cudaStream_t stream) {
   using namespace relay;
-  relay_status_t st = check_shape(dtype, tokens, experts, top);
-  if (st != RELAY_OK) return st;
-  if (tokens == 0) return RELAY_OK;
-  if (logits == nullptr || index == nullptr || d_logits == nullptr) return bad("logits, index or d_logits is NULL");
-  if (row_stride < experts || d_row_stride < experts || row_stride > (1ll << 31) || d_row_stride > (1ll << 31))
-    return bad("a row stride is less than experts or more than 2^31");
-  const int E = esize_of(dtype);
-  if (off(logits, E) || off(d_logits, E) || off(index, 4) || off(d_gate, 4) || off(d_prob, 4))
-    return bad("an array is not element-aligned");
-  const Span s[] = {span(logits, ((tokens - 1) * row_stride + experts) * E, "logits", false),
-                    span(index, tokens * top * 4, "index", false),
-                    span(d_gate, tokens * top * 4, "d_gate", false),
-                    span(d_prob, experts * 4, "d_prob", false),
-                    span(d_logits, ((tokens - 1) * d_row_stride + experts) * E, "d_logits", true)};
-  st = check_spans(s, 5);
-  if (st != RELAY_OK) return st;
-  const BackwardArgs a{logits, d_logits, row_stride, d_row_stride, tokens, experts, top, normalize,
-                       load_bytes(logits, row_stride, E, experts), load_bytes(d_logits, d_row_stride, E, experts),
-                       index, d_gate, d_prob};
-  const int blocks = (int)std::min<int64_t>((tokens + kRouterWarps - 1) / kRouterWarps, 8 * 152);
-  return done(by_width(experts, top, [&](auto n, auto l) {
-    constexpr int N = decltype(n)::value, L = decltype(l)::value;
-    return launch_chained(dtype == RELAY_BF16 ? router_backward_kernel<uint16_t, N, L> : router_backward_kernel<float, N, L>,
-                          blocks, kRouterThreads, 0, stream, a);
-  }));
+  return guarded([&]() -> relay_status_t {
+    relay_status_t st = check_shape(dtype, tokens, experts, top);
+    if (st != RELAY_OK) return st;
+    if (tokens == 0) return RELAY_OK;
+    if (logits == nullptr || index == nullptr || d_logits == nullptr) return bad("logits, index or d_logits is NULL");
+    if (row_stride < experts || d_row_stride < experts || row_stride > (1ll << 31) || d_row_stride > (1ll << 31))
+      return bad("a row stride is less than experts or more than 2^31");
+    const int E = esize_of(dtype);
+    if (off(logits, E) || off(d_logits, E) || off(index, 4) || off(d_gate, 4) || off(d_prob, 4))
+      return bad("an array is not element-aligned");
+    const Span s[] = {span(logits, ((tokens - 1) * row_stride + experts) * E, "logits", false),
+                      span(index, tokens * top * 4, "index", false),
+                      span(d_gate, tokens * top * 4, "d_gate", false),
+                      span(d_prob, experts * 4, "d_prob", false),
+                      span(d_logits, ((tokens - 1) * d_row_stride + experts) * E, "d_logits", true)};
+    st = check_spans(s, 5);
+    if (st != RELAY_OK) return st;
+    const BackwardArgs a{logits, d_logits, row_stride, d_row_stride, tokens, experts, top, normalize,
+                         load_bytes(logits, row_stride, E, experts), load_bytes(d_logits, d_row_stride, E, experts),
+                         index, d_gate, d_prob};
+    const int blocks = (int)std::min<int64_t>((tokens + kRouterWarps - 1) / kRouterWarps, 8 * 152);
+    return done(by_width(experts, top, [&](auto n, auto l) {
+      constexpr int N = decltype(n)::value, L = decltype(l)::value;
+      return launch_chained(dtype == RELAY_BF16 ? router_backward_kernel<uint16_t, N, L> : router_backward_kernel<float, N, L>,
+                            blocks, kRouterThreads, 0, stream, a);
+    }));
+  });
 }
 
 }  // extern "C"
