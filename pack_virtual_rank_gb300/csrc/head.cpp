@@ -98,7 +98,7 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
     pack |= h.rows[a] > 0 && (reinterpret_cast<uintptr_t>(h.weight[a]) % 16 || h.weight_stride % 8);
   Layout l{base};
   HeadWork& w = ar.w;
-  w.dim_pad = (int32_t)up(g.dim, 8);
+  w.dim_pad = (int32_t)up(g.dim, 64);  // rows of whole 128-byte lines: a box row is one line, not two
   w.splits = 1;
   w.n_live = reinterpret_cast<int32_t*>(l.take(4));
   w.perm = reinterpret_cast<int32_t*>(l.take(4ll * g.mpad));

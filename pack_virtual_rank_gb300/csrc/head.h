@@ -87,7 +87,7 @@ struct HeadWork {
   int32_t* perm;      // [mpad] packed row -> row of hidden
   float* wrow;        // [mpad] row weight * tau (0 past the live rows)
   uint16_t* hid;      // [planes][mpad][dim_pad] packed hidden
-  int32_t dim_pad;    // a multiple of 8
+  int32_t dim_pad;    // a multiple of 64
   uint16_t* wpack;    // [planes][tiles * kHeadTile][dim_pad] packed weight, or NULL: read in place
   uint8_t* live;      // [tokens]            (distill)
   int32_t* ent_col;   // [tokens][top] entries' padded columns, ascending; INT32_MAX: absent
