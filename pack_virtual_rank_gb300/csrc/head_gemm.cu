@@ -576,17 +576,28 @@ __device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t,
 template <class T>
 __device__ __noinline__ void copy_rows(uint32_t buf, T* to, int64_t ld, int rows, int columns) {
   __syncwarp();
-  for (int r = 0; r < rows; ++r, to += ld)
-    for (int e = threadIdx.x % 32; e < columns; e += 32) {
-      const uint32_t at = buf + r * 128 + (((e * (int)sizeof(T) / 16) ^ (r & 7)) << 4) + e * (int)sizeof(T) % 16;
-      if constexpr (sizeof(T) == 2) {
-        uint16_t x;
-        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
-        to[e] = x;
-      } else {
-        uint32_t x;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
-        to[e] = __uint_as_float(x);
+  constexpr int kAtOnce = 8;  // rows whose elements are read before any is stored
+  for (int e = threadIdx.x % 32; e < columns; e += 32)
+    for (int r0 = 0; r0 < rows; r0 += kAtOnce) {
+      uint32_t x[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int r = r0 + i;
+        const uint32_t at = buf + r * 128 + (((e * (int)sizeof(T) / 16) ^ (r & 7)) << 4) + e * (int)sizeof(T) % 16;
+        if constexpr (sizeof(T) == 2) {
+          uint16_t h;
+          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h) : "r"(at) : "memory");
+          x[i] = h;
+        } else {
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[i]) : "r"(at) : "memory");
+        }
+      }
+      T* row = to + r0 * ld + e;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i, row += ld) {
+        if (r0 + i >= rows) break;
+        if constexpr (sizeof(T) == 2) *row = (uint16_t)x[i];
+        else *row = __uint_as_float(x[i]);
       }
     }
   __syncwarp();
