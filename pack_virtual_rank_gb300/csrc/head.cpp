@@ -100,7 +100,7 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
   HeadWork& w = ar.w;
   w.dim_pad = (int32_t)up(g.dim, 64);  // rows of whole 128-byte lines: a box row is one line, not two
   w.splits = 1;
-  w.n_live = reinterpret_cast<int32_t*>(l.take(4));
+  w.n_live = reinterpret_cast<int32_t*>(l.take(8));
   w.perm = reinterpret_cast<int32_t*>(l.take(4ll * g.mpad));
   w.wrow = reinterpret_cast<float*>(l.take(4ll * g.mpad));
   w.hid = reinterpret_cast<uint16_t*>(l.take(2ll * planes * g.mpad * w.dim_pad));
@@ -242,7 +242,7 @@ relay_status_t run_head(const relay_head_t& h, HeadGeom g, int top, const int32_
     return RELAY_OK;
   }
   if (distill) RELAY_HEAD_TRY(head_teacher(g, w, teacher, teacher_dtype, entries, stream));
-  RELAY_HEAD_TRY(head_pack(g, w, h.dtype, distill, h.hidden, h.hidden_stride, entries, row_weight, loss,
+  RELAY_HEAD_TRY(head_pack(g, w, h.dtype, h.hidden, h.hidden_stride, entries, teacher, teacher_dtype, row_weight, loss,
                            h.d_hidden, h.d_hidden_stride, stream));
   if (w.wpack != nullptr) RELAY_HEAD_TRY(head_pack_weight(g, w, sh, h.dtype, stream));
   RELAY_HEAD_TRY(head_logits(g, w, sh, h.dtype, 0, tiles, ar.keep ? kHeadStatsKeep : kHeadStats, stream));

@@ -83,7 +83,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 // Everything a call works with on the device.
 struct HeadWork {
-  int32_t* n_live;    // [1]
+  int32_t* n_live;    // [2]: live rows, cuts of the vocabulary for d_hidden
   int32_t* perm;      // [mpad] packed row -> row of hidden
   float* wrow;        // [mpad] row weight * tau (0 past the live rows)
   uint16_t* hid;      // [planes][mpad][dim_pad] packed hidden
@@ -110,9 +110,8 @@ struct HeadWork {
 // runs, to fill the GPU evenly. Costs are in inner steps of one tile (64 columns, about 0.27 us):
 // the rounds of the GPU's products over d_hidden's tiles, or all the work spread evenly plus the
 // longest tile at its end, whichever is more; plus writing and reading a cut's fp32 partial sums (8 bytes
-// a value; a step's time moves about 1.8 MB). The live rows are known on the device only, so
-// kernels call this themselves and agree. In float: a few parts in 10^7 decide nothing, and every lane
-// of every kernel gets the same.
+// a value; a step's time moves about 1.8 MB). The live rows are known on the device only: the packing
+// kernel leaves the number beside theirs.
 #ifdef __CUDACC__
 constexpr int kHeadOpenSteps = 4;  // steps a tile costs besides its own
 __device__ __forceinline__ float head_long_steps(int tiles, int cuts) {  // a tile of d_hidden
@@ -160,10 +159,9 @@ struct HeadShards {
 // head_rows.cu
 cudaError_t head_teacher(const HeadGeom& g, const HeadWork& w, const void* teacher, int teacher_dtype,
                          const int32_t* index, cudaStream_t s);
-cudaError_t head_pack(const HeadGeom& g, const HeadWork& w, int dtype, bool distill,
-                      const void* hidden, int64_t hidden_ld, const int32_t* targets,
-                      const float* row_weight, float* loss, void* d_hidden, int64_t d_hidden_ld,
-                      cudaStream_t s);
+cudaError_t head_pack(const HeadGeom& g, const HeadWork& w, int dtype, const void* hidden, int64_t hidden_ld,
+                      const int32_t* index, const void* teacher, int teacher_dtype, const float* row_weight,
+                      float* loss, void* d_hidden, int64_t d_hidden_ld, cudaStream_t s);
 cudaError_t head_pack_weight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype,
                              cudaStream_t s);
 cudaError_t head_combine(const HeadGeom& g, const HeadWork& w, bool distill, float* loss,

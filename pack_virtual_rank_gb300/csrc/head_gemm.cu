@@ -131,7 +131,7 @@ struct Schedule {
 };
 
 template <int P, int CTAS>
-__device__ __forceinline__ Schedule schedule(const GemmArgs& p, int live) {
+__device__ __forceinline__ Schedule schedule(const GemmArgs& p, int live, int cuts) {
   constexpr int kM = Shape<CTAS>::kM;
   const int mt = (live + kM - 1) / kM, tiles = p.tile_hi - p.tile_lo;
   const int nd = (p.g.dim + kBN - 1) / kBN;
@@ -145,7 +145,7 @@ __device__ __forceinline__ Schedule schedule(const GemmArgs& p, int live) {
   }
   const int short_items = p.want_dw ? tiles * (kHeadTile / kM) * nd : 0;
   if (p.want_dh) {
-    s.cuts = head_cuts(p.g, p.w, live);
+    s.cuts = cuts;
     s.long_items = mt * nd * s.cuts;
   }
   s.items = s.long_items + short_items;
@@ -681,8 +681,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   dep_wait();
-  const int live = *p.w.n_live;
-  const Schedule sched = schedule<P, CTAS>(p, live);  // a pair without a tile passes through
+  const int2 counted = *reinterpret_cast<const int2*>(p.w.n_live);
+  const int live = counted.x;
+  const Schedule sched = schedule<P, CTAS>(p, live, counted.y);  // a pair without a tile passes through
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeedRegs));
     if (threadIdx.x == 0) produce<P, PLANES, CTAS>(p, sched, live, rank, ring, full, empty, &s_gave_up);

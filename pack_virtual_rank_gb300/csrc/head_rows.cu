@@ -142,15 +142,13 @@ __global__ void __launch_bounds__(kThreadsRows)
 }
 
 // One warp per row: the entries' columns in ascending order (by counting, each lane holds up to
-// four), and the teacher's probabilities beside them. An id given twice keeps two entries.
+// four), and the teacher's probabilities beside them. An id given twice keeps two entries. Returns whether
+// the row takes part.
 template <class T>
-__global__ void __launch_bounds__(kThreadsRows) teacher_kernel(const HeadGeom g, const HeadWork w,
-                                                               const T* logits, const int32_t* index) {
+__device__ __forceinline__ bool teacher_row(const HeadGeom& g, const HeadWork& w, const T* logits, const int32_t* index,
+                                            int row) {
   constexpr int kPer = RELAY_HEAD_MAX_TOP / 32;
-  dep_launch();
-  dep_wait();
-  const int row = blockIdx.x * (kThreadsRows / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (row >= g.tokens) return;
+  const int lane = threadIdx.x % 32;
   const int64_t at = (int64_t)row * g.top;
   int col[kPer], rank[kPer];
   float s[kPer];
@@ -195,13 +193,40 @@ __global__ void __launch_bounds__(kThreadsRows) teacher_kernel(const HeadGeom g,
     w.ent_col[at + rank[i]] = col[i];
     w.ent_q[at + rank[i]] = live ? q[i] / sum : 0.0f;
   }
-  if (lane == 0) w.live[row] = live;
+  return live;
+}
+template <class T>
+__global__ void __launch_bounds__(kThreadsRows) teacher_kernel(const HeadGeom g, const HeadWork w,
+                                                               const T* logits, const int32_t* index) {
+  dep_launch();
+  dep_wait();
+  const int row = blockIdx.x * (kThreadsRows / 32) + threadIdx.x / 32;
+  if (row >= g.tokens) return;
+  const bool live = teacher_row(g, w, logits, index, row);
+  if (threadIdx.x % 32 == 0) w.live[row] = live;
 }
 
-template <bool DISTILL>
-__device__ __forceinline__ bool row_live(const HeadGeom& g, const HeadWork& w, const int32_t* targets, int row) {
-  if (DISTILL) return w.live[row] != 0;
-  const int t = targets[row];
+// Where a row's flag comes from: its target; teacher_kernel; or, in a small batch of few entries, its entries,
+// which every block then reads itself: a launch less.
+enum RowSource { kFromTarget, kFromFlag, kFromEntries };
+constexpr int kEntriesTop = 16, kEntriesTokens = 512;
+
+template <RowSource SOURCE, class TT>
+__device__ __forceinline__ bool row_live(const HeadGeom& g, const HeadWork& w, const int32_t* index, const TT* teacher,
+                                         int row) {
+  if (SOURCE == kFromFlag) return w.live[row] != 0;
+  if (SOURCE == kFromEntries) {
+    bool live = false;
+#pragma unroll
+    for (int k = 0; k < kEntriesTop; ++k) {
+      if (k >= g.top) break;
+      const int id = index[row * g.top + k];
+      const float t = load_as_f32(teacher + row * g.top + k);
+      live |= id >= 0 && id < g.vocab && !(t == -INFINITY);  // a NaN is an entry
+    }
+    return live;
+  }
+  const int t = index[row];
   return t >= 0 && t < g.vocab;
 }
 
@@ -209,10 +234,10 @@ __device__ __forceinline__ bool row_live(const HeadGeom& g, const HeadWork& w, c
 // every row's flag, from L2: no second launch, no order between blocks), then a warp per row
 // copies the live ones to their packed places and zeroes the places the others leave free
 // behind the last live row, as far as products read them. Ignored rows get loss 0 and d_hidden 0.
-template <class T, bool DISTILL>
+template <class T, RowSource SOURCE, class TT>
 __global__ void __launch_bounds__(kThreadsRows)
-    pack_kernel(const HeadGeom g, const HeadWork w, const T* hidden, int64_t ld, const int32_t* targets,
-                const float* row_weight, float* loss, T* dh, int64_t dh_ld, int per, int vec) {
+    pack_kernel(const HeadGeom g, const HeadWork w, const T* hidden, int64_t ld, const int32_t* index,
+                const TT* teacher, const float* row_weight, float* loss, T* dh, int64_t dh_ld, int per, int vec) {
   constexpr int kWarps = kThreadsRows / 32;
   __shared__ int s_before, s_total, s_warp[kWarps], s_place[kThreadsRows];
   dep_launch();
@@ -223,7 +248,7 @@ __global__ void __launch_bounds__(kThreadsRows)
   int before = 0, total = 0;
 #pragma unroll 4
   for (int r = threadIdx.x; r < g.tokens; r += kThreadsRows) {
-    const int live = row_live<DISTILL>(g, w, targets, r);
+    const int live = row_live<SOURCE>(g, w, index, teacher, r);
     total += live;
     before += r < lo ? live : 0;
   }
@@ -237,11 +262,17 @@ __global__ void __launch_bounds__(kThreadsRows)
   total = s_total;
   int packed = s_before;  // live rows before row `base`
   const int row_tile = head_row_tile(g), read_end = (total + row_tile - 1) / row_tile * row_tile;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *w.n_live = total;
+  if (blockIdx.x == 0 && warp == 0) {
+    const int cuts = head_cuts(g, w, total);
+    if (lane == 0) {
+      w.n_live[0] = total;
+      w.n_live[1] = cuts;
+    }
+  }
   const int64_t plane = (int64_t)g.mpad * w.dim_pad;
   for (int base = lo; base < hi; base += kThreadsRows) {
     const int mine = base + threadIdx.x;
-    const bool live = mine < hi && row_live<DISTILL>(g, w, targets, mine);
+    const bool live = mine < hi && row_live<SOURCE>(g, w, index, teacher, mine);
     const unsigned votes = __ballot_sync(~0u, live);
     if (lane == 0) s_warp[warp] = __popc(votes);
     __syncthreads();
@@ -254,14 +285,15 @@ __global__ void __launch_bounds__(kThreadsRows)
       w.perm[place] = mine;
       w.wrow[place] = live ? (row_weight ? row_weight[mine] : 1.0f) * g.tau : 0.0f;
       if (!live) loss[mine] = 0.0f;
-      if (!DISTILL && live) {
-        w.ent_col[mine] = column_of(g, targets[mine]);
+      if (SOURCE == kFromTarget && live) {
+        w.ent_col[mine] = column_of(g, index[mine]);
         w.ent_q[mine] = 1.0f;
       }
     }
     __syncthreads();
     for (int i = warp; base + i < hi && i < kThreadsRows; i += kWarps) {
       const int r = base + i, place = s_place[i];
+      if (SOURCE == kFromEntries) teacher_row(g, w, teacher, index, r);
       if (place >= 0) {
         pack_row(w.hid + (int64_t)place * w.dim_pad, plane, hidden + r * ld, g.dim, w.dim_pad, vec);
       } else {
@@ -480,7 +512,7 @@ __global__ void __launch_bounds__(kThreadsRows)
     write_dh_kernel(const HeadGeom g, const HeadWork w, T* dh, int64_t ld, int vec) {
   dep_launch();
   dep_wait();
-  const int live = *w.n_live, cuts = head_cuts(g, w, live);
+  const int live = w.n_live[0], cuts = w.n_live[1];
   if (w.whole && cuts == 1) return;
   const int64_t cut = (int64_t)g.mpad * w.dh_ld;
   constexpr int kLanes = 4;
@@ -519,6 +551,7 @@ int64_t esize(int dtype) { return dtype == RELAY_BF16 ? 2 : 4; }
 
 cudaError_t head_teacher(const HeadGeom& g, const HeadWork& w, const void* teacher, int teacher_dtype,
                          const int32_t* index, cudaStream_t s) {
+  if (g.top <= kEntriesTop && g.tokens <= kEntriesTokens) return cudaSuccess;  // the packing does it
   const int blocks = ceil_div(g.tokens, kThreadsRows / 32);
   if (teacher_dtype == RELAY_BF16)
     return launch_chained(teacher_kernel<uint16_t>, blocks, kThreadsRows, 0, s, g, w,
@@ -527,9 +560,9 @@ cudaError_t head_teacher(const HeadGeom& g, const HeadWork& w, const void* teach
                         index);
 }
 
-template <class T>
-static cudaError_t pack_typed(const HeadGeom& g, const HeadWork& w, bool distill, const void* hidden,
-                              int64_t ld, const int32_t* targets, const float* row_weight, float* loss,
+template <class T, class TT>
+static cudaError_t pack_typed(const HeadGeom& g, const HeadWork& w, const void* hidden, int64_t ld,
+                              const int32_t* index, const void* teacher, const float* row_weight, float* loss,
                               void* dh, int64_t dh_ld, cudaStream_t s) {
   // a warp per row; at most 2048 blocks read every row's flag
   constexpr int kWarps = kThreadsRows / 32;
@@ -537,17 +570,23 @@ static cudaError_t pack_typed(const HeadGeom& g, const HeadWork& w, bool distill
   // (a few more for a small batch: they zero the places past it)
   const int pad = ceil_div(head_row_tile(g), kWarps), blocks = ceil_div(g.tokens, per) > pad ? ceil_div(g.tokens, per) : pad;
   const int vec = reinterpret_cast<uintptr_t>(hidden) % 16 == 0 && ld * sizeof(T) % 16 == 0;
-  return launch_chained(distill ? pack_kernel<T, true> : pack_kernel<T, false>, blocks, kThreadsRows, 0, s, g, w,
-                        static_cast<const T*>(hidden), ld, targets, row_weight, loss, static_cast<T*>(dh), dh_ld, per,
-                        vec);
+  auto* kernel = teacher == nullptr ? pack_kernel<T, kFromTarget, TT>
+                 : g.top <= kEntriesTop && g.tokens <= kEntriesTokens ? pack_kernel<T, kFromEntries, TT>
+                                                                      : pack_kernel<T, kFromFlag, TT>;
+  return launch_chained(kernel, blocks, kThreadsRows, 0, s, g, w, static_cast<const T*>(hidden), ld, index,
+                        static_cast<const TT*>(teacher), row_weight, loss, static_cast<T*>(dh), dh_ld, per, vec);
 }
 
-cudaError_t head_pack(const HeadGeom& g, const HeadWork& w, int dtype, bool distill, const void* hidden,
-                      int64_t hidden_ld, const int32_t* targets, const float* row_weight, float* loss,
-                      void* d_hidden, int64_t d_hidden_ld, cudaStream_t s) {
+cudaError_t head_pack(const HeadGeom& g, const HeadWork& w, int dtype, const void* hidden, int64_t hidden_ld,
+                      const int32_t* index, const void* teacher, int teacher_dtype, const float* row_weight,
+                      float* loss, void* d_hidden, int64_t d_hidden_ld, cudaStream_t s) {
   if (dtype == RELAY_BF16)
-    return pack_typed<uint16_t>(g, w, distill, hidden, hidden_ld, targets, row_weight, loss, d_hidden, d_hidden_ld, s);
-  return pack_typed<float>(g, w, distill, hidden, hidden_ld, targets, row_weight, loss, d_hidden, d_hidden_ld, s);
+    return teacher_dtype == RELAY_BF16
+               ? pack_typed<uint16_t, uint16_t>(g, w, hidden, hidden_ld, index, teacher, row_weight, loss, d_hidden, d_hidden_ld, s)
+               : pack_typed<uint16_t, float>(g, w, hidden, hidden_ld, index, teacher, row_weight, loss, d_hidden, d_hidden_ld, s);
+  return teacher_dtype == RELAY_BF16
+             ? pack_typed<float, uint16_t>(g, w, hidden, hidden_ld, index, teacher, row_weight, loss, d_hidden, d_hidden_ld, s)
+             : pack_typed<float, float>(g, w, hidden, hidden_ld, index, teacher, row_weight, loss, d_hidden, d_hidden_ld, s);
 }
 
 cudaError_t head_pack_weight(const HeadGeom& g, const HeadWork& w, const HeadShards& sh, int dtype, cudaStream_t s) {

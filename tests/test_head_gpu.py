@@ -271,3 +271,23 @@ def test_loss_alone(tokens, offset, extra, dtype):
     check(out, hard)
     assert bool((out["loss"][dead] == 0).all())
     check(Call(h2, ws, rw, grads=False, offset=offset, extra=extra).distill(logits, index, 3.0), soft)
+
+
+@pytest.mark.parametrize("tokens,top", [(512, 16), (513, 16), (512, 17), (30, 2)])
+def test_distill_row_sources(tokens, top):
+    """Small batches of few entries read their entries in the packing kernel, others a kernel before: the
+    same rows take part on both sides of the limit."""
+    g, h, ws, rw = inputs(tokens, 64, [70, 200], "bf16", 13)
+    index = torch.randint(-40, 270, (tokens, top), generator=g, dtype=torch.int32)
+    logits = torch.randn(tokens, top, generator=g)
+    index[5] = -1
+    logits[7] = -math.inf
+    index[8, 1:], logits[8, 0] = 400, -math.inf
+    logits[9, 1:] = -math.inf
+    h2 = h.clone()
+    live = ((index >= 0) & (index < 270) & (logits > -math.inf)).any(dim=1)
+    h2[~live] = math.nan
+    want = ref.head(h, ws, index, logits, rw, 2.0)
+    out = Call(h2, ws, rw).distill(logits, index, 2.0)
+    check(out, want)
+    assert bool((out["loss"][~live] == 0).all())
