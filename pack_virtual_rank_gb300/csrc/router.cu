@@ -202,6 +202,7 @@ __device__ __noinline__ bool choose_exact(const T* x, int experts, int top, bool
 template <class T, int N, int L>
 __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) router_forward_kernel(const ForwardArgs a) {
   constexpr int kRows = 32 / L;
+  constexpr int kTracked = L < 32 ? 3 : 2;  // a lane's best keys kept in order: fewer lanes are chosen from more often
   extern __shared__ float s_prob[];  // [warps * kRows][experts], then the counts [experts]
   int32_t* s_count = reinterpret_cast<int32_t*>(s_prob + kRouterWarps * kRows * a.experts);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane % L, e0 = sub * N;
@@ -228,15 +229,16 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) router_forward
     next.values(v);
     const bool counted = next_counted;
     fetch(row + stride);
-    uint32_t key[N], best = 0, second = 0;
+    uint32_t key[N], best = 0, second = 0, third = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       key[i] = unique_key(v[i], e0 + i);
       if (!full && e0 + i >= a.experts) key[i] = 0u;
+      if (kTracked == 3) third = max(third, min(second, key[i]));
       second = max(second, min(best, key[i]));
       best = max(best, key[i]);
     }
-    if (!counted) best = second = 0;
+    if (!counted) best = second = third = 0;
     uint32_t win = max_row<L>(best);
     bool live = win > (kKeyNegInf | kExpertMask);  // else masked out, or no logit above -inf
     // the largest value: a bf16 key holds all of it
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) router_forward
     }
     sum = sum_row<L>(sum);
     const float inv = 1.0f / sum;
-    bool again = false;   // the lane's second best is its best now
+    int taken = 0;        // of the lane's kTracked best
     bool close = false;   // two of the largest agree in their upper bits
     uint32_t mine = 0;    // lane j: the key chosen j-th
 #pragma unroll 4
@@ -267,14 +269,17 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) router_forward
       uint32_t after = second;
       // the largest after the one just taken; a vote, so that it is a branch and not predicated
       // into every round
-      if (__any_sync(~0u, holder && again)) {
+      if (__any_sync(~0u, holder && taken == kTracked - 1)) {
         uint32_t left = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) left = max(left, key[i] < win ? key[i] : 0u);
-        if (again) after = left;
+        if (taken == kTracked - 1) after = left;
       }
-      if (holder) best = after;
-      again |= holder;
+      if (holder) {
+        best = after;
+        if (kTracked == 3) second = third;
+        taken = min(taken + 1, kTracked - 1);
+      }
       win = max_row<L>(best);
     }
     if (sizeof(T) == 4) {
