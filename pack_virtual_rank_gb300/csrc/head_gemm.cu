@@ -17,9 +17,9 @@
 //
 // Why pairs: a single CTA's 128 x 256 tile reads 48 KiB for 512 cycles of products, and the path from
 // L2 into an SM carries 64 bytes a cycle: the tensor pipe was 69-71% busy at 18 TB/s of such
-// reads. A pair shares the second operand, 32 KiB for the same products, and keeps it 76-79% busy. Up
+// reads. A pair shares the second operand, 32 KiB for the same products, and keeps it 80% busy. Up
 // to 128 rows one CTA works alone (CTAS = 1): half of a pair's product would be padding rows (8 rows,
-// 1024 x 32768: 20 us a call alone, 30 us in pairs).
+// 1024 x 32768: 17 us a call alone, 30 us in pairs).
 //
 // The accumulator puts a row of the tile into one lane, so the softmax statistics of a row are
 // one thread's registers: no shuffles.

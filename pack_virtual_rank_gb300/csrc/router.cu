@@ -645,7 +645,8 @@ relay_status_t relay_router_backward(const void* logits, int64_t row_stride, rel
     const BackwardArgs a{logits, d_logits, row_stride, d_row_stride, tokens, experts, top, normalize,
                          load_bytes(logits, row_stride, E, experts), load_bytes(d_logits, d_row_stride, E, experts),
                          index, d_gate, d_prob};
-    const int blocks = (int)std::min<int64_t>((tokens + kRouterWarps - 1) / kRouterWarps, 8 * 152);
+    // four blocks an SM: one round of resident warps, whose next rows load under the present ones (16: 2% slower)
+  const int blocks = (int)std::min<int64_t>((tokens + kRouterWarps - 1) / kRouterWarps, 4 * 152);
     return done(by_width(experts, top, [&](auto n, auto l) {
       constexpr int N = decltype(n)::value, L = decltype(l)::value;
       return launch_chained(dtype == RELAY_BF16 ? router_backward_kernel<uint16_t, N, L> : router_backward_kernel<float, N, L>,
