@@ -41,18 +41,26 @@ namespace {
 // Bit 1: a wait ran out, the call's outputs are unspecified.
 __device__ unsigned g_head_fault;
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;  // rows of one CTA, columns of the pair, inner step
-// What depends on the number of CTAs that make one product.
-template <int CTAS>
+constexpr int kBM = 128, kBN = 256;  // rows of one CTA, columns of the product
+// What depends on the number of CTAs that make one product and on the parts of its operands. A step is 64
+// elements of the inner dimension; of fp32 operands 32, with all three parts of both in one stage: every
+// part is used two or three times, and bringing it once halves what the path from L2 carries.
+template <int PLANES, int CTAS>
 struct Shape {
   static constexpr int kM = CTAS * kBM;       // rows of the product
   static constexpr int kShare = kBN / CTAS;   // columns (B's rows) one CTA brings
-  static constexpr int kStages = CTAS == 2 ? 6 : 4;
-  static constexpr int kABytes = kBM * kBK * 2, kBBytes = kShare * kBK * 2, kStageBytes = kABytes + kBBytes;
+  static constexpr int kK = PLANES == 3 ? 32 : 64;
+  static constexpr int kLoad = PLANES == 3 ? 3 : 1;  // parts in a stage
+  static constexpr int kAPart = kBM * kK * 2, kBPart = kShare * kK * 2;
+  static constexpr int kABytes = kLoad * kAPart, kStageBytes = kABytes + kLoad * kBPart;
+  static constexpr int kStages = PLANES == 3 ? (CTAS == 2 ? 4 : 2) : CTAS == 2 ? 6 : 4;
 };
-static_assert(Shape<2>::kM == kHeadRowTile && kBN == kHeadTile, "tiles are what rows and columns are padded to");
-constexpr int kRingBytes = Shape<2>::kStages * Shape<2>::kStageBytes;
-static_assert(kRingBytes == Shape<1>::kStages * Shape<1>::kStageBytes, "one ring size");
+static_assert(2 * kBM == kHeadRowTile && kBN == kHeadTile, "tiles are what rows and columns are padded to");
+constexpr int kRingBytes = 192 * 1024;
+template <int PLANES, int CTAS>
+constexpr bool kFits = Shape<PLANES, CTAS>::kStages * Shape<PLANES, CTAS>::kStageBytes <= kRingBytes &&
+                       Shape<PLANES, CTAS>::kStageBytes % 1024 == 0;
+static_assert(kFits<1, 1> && kFits<1, 2> && kFits<3, 1> && kFits<3, 2>, "stages fit the ring, on 1024-byte addresses");
 constexpr int kFinishWarps = 8;                        // warps that turn accumulators into results
 constexpr int kOutWarpBytes = 32 * 64 * 2;             // 32 rows x 64 columns of 16 bits, one per warp
 constexpr int kOutBytes = kFinishWarps * kOutWarpBytes;
@@ -69,17 +77,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 enum Product { kStats, kStatsKeep, kGradient, kBack };
 
-// Inner steps (of 64) summed in tensor memory before the sum moves on into registers. The tensor
+// Inner steps summed in tensor memory before the sum moves on into registers. The tensor
 // cores cut what does not fit 24 bits at every product instead of rounding it, which drifts with
 // the length of the chain: at dim 4096 in one chain the loss was several times as far from its
 // 64-bit value as an fp32 sum. A chain of 48 products leaves it 3.7e-7 off at 2047 x 2048 x 50001 (32
 // products: 2.6e-7 and 1% more time; 64: 5.5e-7 and 1% less; the plain fp32 form 4e-7). A result that
 // is rounded to bf16 does not show the drift.
 template <int P, int PLANES>
-constexpr int kChain = PLANES == 3 ? 2 : P == kBack ? INT_MAX : 12;
+constexpr int kChain = PLANES == 3 ? 4 : P == kBack ? INT_MAX : 12;
 
 struct GemmArgs {
-  CUtensorMap a;                         // first operand: hidden (logits), gradient
+  CUtensorMap a;                         // first operand: hidden (logits), gradient (d_hidden)
+  CUtensorMap aw;                        // the gradient as d_weight's first operand
   CUtensorMap b[RELAY_HEAD_MAX_SHARDS];  // weight shards, or the packed weight
   CUtensorMap hid;                       // hidden as d_weight's second operand
   CUtensorMap c[RELAY_HEAD_MAX_SHARDS];  // results: gradient or codes (logits), d_weight
@@ -88,7 +97,7 @@ struct GemmArgs {
   HeadWork w;
   HeadShards sh;
   int32_t extra;     // bytes a stage waits for that no load brings (test of the bounded waits)
-  int32_t maps;      // which of the maps above are in use, in the order a, b, c, hid, dh
+  int32_t maps;      // which of the maps above are in use, in the order a, b, c, hid, dh, aw
   int32_t tile_lo, tile_hi;
   int32_t want_dh, want_dw;
   int32_t first;     // d_hidden: overwrite the partial sums
@@ -101,7 +110,7 @@ struct GemmArgs {
 struct Item {
   int row0, col0;          // first row of this CTA's half and first column of the tile
   int tile, shard, v0;     // padded column tile, its shard, the shard's weight row it starts at
-  int k_lo, k_hi;          // inner steps of 64 (d_hidden: column tiles)
+  int k_lo, k_hi;          // inner steps (d_hidden: column tiles)
   int split;
   bool weight;             // kBack: a tile of d_weight
 };
@@ -132,7 +141,7 @@ struct Schedule {
 
 template <int P, int CTAS>
 __device__ __forceinline__ Schedule schedule(const GemmArgs& p, int live, int cuts) {
-  constexpr int kM = Shape<CTAS>::kM;
+  constexpr int kM = CTAS * kBM;
   const int mt = (live + kM - 1) / kM, tiles = p.tile_hi - p.tile_lo;
   const int nd = (p.g.dim + kBN - 1) / kBN;
   Schedule s{};
@@ -157,9 +166,9 @@ __device__ __forceinline__ Schedule schedule(const GemmArgs& p, int live, int cu
   return s;
 }
 
-template <int P, int CTAS>
+template <int P, int PLANES, int CTAS>
 __device__ __forceinline__ Item item_at(const GemmArgs& p, const Schedule& sched, int live, int rank, int i) {
-  constexpr int kM = Shape<CTAS>::kM, kPerTile = kHeadTile / kM;
+  constexpr int kM = CTAS * kBM, kPerTile = kHeadTile / kM, kK = Shape<PLANES, CTAS>::kK;
   const int mt = (live + kM - 1) / kM, tiles = p.tile_hi - p.tile_lo;
   const int nd = (p.g.dim + kBN - 1) / kBN;
   Item t{};
@@ -175,7 +184,7 @@ __device__ __forceinline__ Item item_at(const GemmArgs& p, const Schedule& sched
       t.shard = head_shard_of_tile(p.g, t.tile);
       t.v0 = (t.tile - p.g.tile0[t.shard]) * kHeadTile + within;
       t.row0 = (t.tile - p.tile_lo) * kHeadTile + within;
-      t.k_hi = (live + kBK - 1) / kBK;
+      t.k_hi = (live + kK - 1) / kK;
     } else {
       t.split = i % sched.cuts;
       t.row0 = i / sched.cuts * kM + rank * kBM;
@@ -190,13 +199,13 @@ __device__ __forceinline__ Item item_at(const GemmArgs& p, const Schedule& sched
     t.shard = head_shard_of_tile(p.g, t.tile);
     t.v0 = (t.tile - p.g.tile0[t.shard]) * kHeadTile;
     t.col0 = (t.tile - p.tile_lo) * kHeadTile;
-    t.k_hi = (p.g.dim + kBK - 1) / kBK;
+    t.k_hi = (p.g.dim + kK - 1) / kK;
   }
   return t;
 }
 
 // Inner steps of a tile, one call of f(step) each.
-template <int P, class F>
+template <int P, int KK, class F>
 __device__ __forceinline__ bool for_steps(const GemmArgs& p, const Item& t, F f) {
   if (P != kBack || t.weight) {
     for (int k = t.k_lo; k < t.k_hi; ++k)
@@ -205,70 +214,70 @@ __device__ __forceinline__ bool for_steps(const GemmArgs& p, const Item& t, F f)
   }
   for (int tile = t.k_lo; tile < t.k_hi; ++tile) {
     const int shard = head_shard_of_tile(p.g, tile), v0 = (tile - p.g.tile0[shard]) * kHeadTile;
-    for (int k = 0; k < kHeadTile / kBK; ++k) {
-      if (v0 + k * kBK >= p.g.rows[shard]) break;  // padding columns: their gradient is 0
-      if (!f((tile - p.tile_lo) * (kHeadTile / kBK) + k, shard, v0 + k * kBK)) return false;
+    for (int k = 0; k < kHeadTile / KK; ++k) {
+      if (v0 + k * KK >= p.g.rows[shard]) break;  // padding columns: their gradient is 0
+      if (!f((tile - p.tile_lo) * (kHeadTile / KK) + k, shard, v0 + k * KK)) return false;
     }
   }
   return true;
 }
 
-// Pairs of parts whose products make up an fp32 product.
-template <int PLANES>
-constexpr int kPairs = PLANES == 3 ? 6 : PLANES;
-// PLANES 3: 2 0 0 1 1 0 with 0 2 1 0 1 0, small products first. PLANES 2 (gradient only): 1 0 with 0 0
-// for d_weight, and the second alone for d_hidden, whose products are not hidden behind writes: 16 rows,
+// Products of parts that make up an fp32 product, small ones first: 2 0 0 1 1 0 with 0 2 1 0 1 0.
+constexpr int kPairs = 6;
+__device__ __forceinline__ int pair_a(int i) { return (0x200110 >> (4 * (5 - i))) & 15; }
+__device__ __forceinline__ int pair_b(int i) { return (0x021010 >> (4 * (5 - i))) & 15; }
+// Stages a step fills, one part of a two-part gradient (PLANES 2) after the other: both for d_weight, the
+// first part alone for d_hidden, whose products are not hidden behind writes: 16 rows,
 // 4096 x 131072 take 645 us with one part, 679 with two for d_weight, 865 with two for both.
 template <int PLANES>
-__device__ __forceinline__ int pair_a(int i) {
-  return PLANES == 1 ? 0 : PLANES == 2 ? 1 - i : (0x200110 >> (4 * (5 - i))) & 15;
-}
-template <int PLANES>
-__device__ __forceinline__ int pair_b(int i) { return PLANES < 3 ? 0 : (0x021010 >> (4 * (5 - i))) & 15; }
-template <int PLANES>
-__device__ __forceinline__ int first_pair(const Item& t) { return PLANES == 2 && !t.weight ? 1 : 0; }
+__device__ __forceinline__ int fills(const Item& t) { return PLANES == 2 && t.weight ? 2 : 1; }
 
 // full: the stage barriers of the pair's first CTA; empty: this CTA's own.
 template <int P, int PLANES, int CTAS>
 __device__ void produce(const GemmArgs& p, const Schedule& sched, int live, int rank, uint32_t ring, uint32_t full, uint32_t empty,
                         volatile int* gave_up) {
   const uint32_t pair_full = pair_addr(full, 0);
-  using S = Shape<CTAS>;
+  using S = Shape<PLANES, CTAS>;
+  constexpr int kK = S::kK;
   const int share = rank * S::kShare;
   int stage = 0;
   uint32_t phase = 0;
   int64_t issued = 0;
   bool ok = true;
   for (int slot = 0, i; ok && (i = sched.at(slot)) >= 0; ++slot) {
-    const Item t = item_at<P, CTAS>(p, sched, live, rank, i);
-    ok = for_steps<P>(p, t, [&](int k, int k_shard, int k_v) {
-      for (int pair = first_pair<PLANES>(t); pair < kPairs<PLANES>; ++pair) {
-        const int pa = pair_a<PLANES>(pair), pb = pair_b<PLANES>(pair);
+    const Item t = item_at<P, PLANES, CTAS>(p, sched, live, rank, i);
+    ok = for_steps<P, kK>(p, t, [&](int k, int k_shard, int k_v) {
+      for (int fill = fills<PLANES>(t) - 1; fill >= 0; --fill) {  // the smaller part first
         if (!bar_wait(empty + 8 * stage, phase ^ 1, gave_up)) return false;
-        const uint32_t bar = pair_full + 8 * stage, sa = ring + stage * S::kStageBytes, sb = sa + S::kABytes;
+        const uint32_t bar = pair_full + 8 * stage;
         if (rank == 0) bar_expect(full + 8 * stage, CTAS * S::kStageBytes + p.extra);
         ++issued;
-        const int wrow = pb * p.g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;  // plane of a packed weight
-        if (P == kBack && t.weight) {
-          for (int j = 0; j < kBM / 64; ++j)
-            map_load<CTAS>(sa + j * 8192, &p.a, t.row0 + 64 * j, pa * p.g.mpad + k * kBK, bar);
-          for (int j = 0; j < S::kShare / 64; ++j)
-            map_load<CTAS>(sb + j * 8192, &p.hid, t.col0 + share + 64 * j, pb * p.g.mpad + k * kBK, bar);
-        } else if (P == kBack) {
-          for (int j = 0; j < kBM / 64; ++j)
-            map_load<CTAS>(sa + j * 8192, &p.a, k * kBK, pa * p.g.mpad + t.row0 + 64 * j, bar);
-          const bool packed = p.w.wpack != nullptr;
-          const CUtensorMap* m = &p.b[packed ? 0 : k_shard];
-          const int y = packed ? wrow + p.g.tile0[k_shard] * kHeadTile + k_v : k_v;
-          for (int j = 0; j < S::kShare / 64; ++j) map_load<CTAS>(sb + j * 8192, m, t.col0 + share + 64 * j, y, bar);
-        } else {
-          map_load<CTAS>(sa, &p.a, k * kBK, pa * p.g.mpad + t.row0, bar);
-          if (p.w.wpack != nullptr)
-            map_load<CTAS>(sb, &p.b[0], k * kBK, wrow + t.tile * kHeadTile + share, bar);
-          else
-            map_load<CTAS>(sb, &p.b[t.shard], k * kBK, t.v0 + share, bar);
+#pragma unroll
+        for (int part = 0; part < S::kLoad; ++part) {
+          const uint32_t sa = ring + stage * S::kStageBytes + part * S::kAPart;
+          const uint32_t sb = ring + stage * S::kStageBytes + S::kABytes + part * S::kBPart;
+          const int a_row = (part + fill) * p.g.mpad, b_row = part * p.g.mpad;          // planes of rows
+          const int wrow = part * p.g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;         // of the packed weight
+          if (P == kBack && t.weight) {
+            for (int j = 0; j < kBM / 64; ++j)
+              map_load<CTAS>(sa + j * 128 * kK, &p.aw, t.row0 + 64 * j, a_row + k * kK, bar);
+            for (int j = 0; j < S::kShare / 64; ++j)
+              map_load<CTAS>(sb + j * 128 * kK, &p.hid, t.col0 + share + 64 * j, b_row + k * kK, bar);
+          } else if (P == kBack) {
+            map_load<CTAS>(sa, &p.a, k * kK, a_row + t.row0, bar);
+            const bool packed = p.w.wpack != nullptr;
+            const CUtensorMap* m = &p.b[packed ? 0 : k_shard];
+            const int y = packed ? wrow + p.g.tile0[k_shard] * kHeadTile + k_v : k_v;
+            for (int j = 0; j < S::kShare / 64; ++j) map_load<CTAS>(sb + j * 128 * kK, m, t.col0 + share + 64 * j, y, bar);
+          } else {
+            map_load<CTAS>(sa, &p.a, k * kK, a_row + t.row0, bar);
+            if (p.w.wpack != nullptr)
+              map_load<CTAS>(sb, &p.b[0], k * kK, wrow + t.tile * kHeadTile + share, bar);
+            else
+              map_load<CTAS>(sb, &p.b[t.shard], k * kK, t.v0 + share, bar);
+          }
         }
-        if (++stage == Shape<CTAS>::kStages) {
+        if (++stage == S::kStages) {
           stage = 0;
           phase ^= 1;
         }
@@ -281,9 +290,9 @@ __device__ void produce(const GemmArgs& p, const Schedule& sched, int live, int 
   // barriers count both CTAs' loads, and the pair leaves together; what they do not count (a stage
   // only one of the two asked for) lands in microseconds.
   const uint64_t start = global_ns();
-  for (int back = 0; rank == 0 && back < Shape<CTAS>::kStages && back < issued; ++back) {
+  for (int back = 0; rank == 0 && back < S::kStages && back < issued; ++back) {
     if (--stage < 0) {
-      stage = Shape<CTAS>::kStages - 1;
+      stage = S::kStages - 1;
       phase ^= 1;
     }
     while (!bar_try(full + 8 * stage, phase) && global_ns() - start < kWaitNs) {
@@ -298,13 +307,13 @@ template <int P, int PLANES, int CTAS>
 __device__ void multiply(const GemmArgs& p, const Schedule& sched, int live, uint32_t ring, uint32_t full, uint32_t empty,
                          uint32_t acc_full, uint32_t acc_empty, uint32_t drain, uint32_t tmem,
                          volatile int* gave_up) {
-  using S = Shape<CTAS>;
+  using S = Shape<PLANES, CTAS>;
   constexpr bool kBOuter = P == kBack;
   int stage = 0, n = 0;
   uint32_t phase = 0;
   bool ok = true;
   for (int slot = 0, i; ok && (i = sched.at(slot)) >= 0; ++slot) {
-    const Item t = item_at<P, CTAS>(p, sched, live, 0, i);
+    const Item t = item_at<P, PLANES, CTAS>(p, sched, live, 0, i);
     const bool a_outer = P == kBack && t.weight;
     const uint32_t desc = a_outer ? product_desc(S::kM, kBN, true, kBOuter) : product_desc(S::kM, kBN, false, kBOuter);
     int in_chain = 0;
@@ -314,7 +323,7 @@ __device__ void multiply(const GemmArgs& p, const Schedule& sched, int live, uin
       return free;
     };
     if (!(ok = open())) break;
-    ok = for_steps<P>(p, t, [&](int, int, int) {
+    ok = for_steps<P, Shape<PLANES, CTAS>::kK>(p, t, [&](int, int, int) {
       if (in_chain == kChain<P, PLANES>) {
         tc_commit<CTAS>(acc_full + 8 * (n & 1));
         ++n;
@@ -322,17 +331,27 @@ __device__ void multiply(const GemmArgs& p, const Schedule& sched, int live, uin
         if (!open()) return false;
       }
       const uint32_t acc = tmem + (n & 1) * kBN;
-      for (int pair = first_pair<PLANES>(t); pair < kPairs<PLANES>; ++pair) {
+      const int n_fills = fills<PLANES>(t);
+      for (int fill = 0; fill < n_fills; ++fill) {
         if (!bar_wait(full + 8 * stage, phase, gave_up)) return false;
         tc_fence_after();
         const uint32_t sa = ring + stage * S::kStageBytes;
-        const uint64_t da = operand_desc(sa, a_outer), db = operand_desc(sa + S::kABytes, kBOuter);
+        const uint64_t da = operand_desc<S::kK>(sa, a_outer), db = operand_desc<S::kK>(sa + S::kABytes, kBOuter);
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k)
-          tc_product<CTAS>(acc, da + k * operand_step(a_outer), db + k * operand_step(kBOuter), desc,
-                     in_chain > 0 || pair > first_pair<PLANES>(t) || k > 0);
+        for (int k = 0; k < S::kK / 16; ++k) {
+          const uint64_t ka = da + k * operand_step(a_outer), kb = db + k * operand_step(kBOuter);
+          const bool more = in_chain > 0 || fill > 0 || k > 0;
+          if constexpr (PLANES == 3) {
+#pragma unroll
+            for (int pair = 0; pair < kPairs; ++pair)
+              tc_product<CTAS>(acc, ka + pair_a(pair) * (S::kAPart >> 4), kb + pair_b(pair) * (S::kBPart >> 4), desc,
+                               more || pair > 0);
+          } else {
+            tc_product<CTAS>(acc, ka, kb, desc, more);
+          }
+        }
         tc_commit<CTAS>(empty + 8 * stage);
-        if (++stage == Shape<CTAS>::kStages) {
+        if (++stage == S::kStages) {
           stage = 0;
           phase ^= 1;
         }
@@ -641,7 +660,7 @@ __device__ __forceinline__ void finish_dweight(const GemmArgs& p, const Item& t,
 
 template <int P, int PLANES, int CTAS>
 __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __grid_constant__ GemmArgs p) {
-  constexpr int kStages = Shape<CTAS>::kStages;
+  constexpr int kStages = Shape<PLANES, CTAS>::kStages;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   __shared__ uint32_t s_tmem;
@@ -665,13 +684,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == 2 && threadIdx.x % 32 <= 2 * RELAY_HEAD_MAX_SHARDS + 2) {
+  if (warp == 2 && threadIdx.x % 32 <= 2 * RELAY_HEAD_MAX_SHARDS + 3) {
     // the maps' descriptors, on their way before the first load asks for them (a map that is not
     // used holds zeros, and is not fetched)
     const int i = threadIdx.x % 32;
     const CUtensorMap* m = i == 0 ? &p.a : i <= RELAY_HEAD_MAX_SHARDS ? &p.b[i - 1]
                            : i <= 2 * RELAY_HEAD_MAX_SHARDS ? &p.c[i - 1 - RELAY_HEAD_MAX_SHARDS]
-                           : i == 2 * RELAY_HEAD_MAX_SHARDS + 1 ? &p.hid : &p.dh;
+                           : i == 2 * RELAY_HEAD_MAX_SHARDS + 1 ? &p.hid : i == 2 * RELAY_HEAD_MAX_SHARDS + 2 ? &p.dh : &p.aw;
     if ((p.maps >> i) & 1) map_prefetch(m);
   }
   if (warp == 1) tmem_alloc<CTAS>(smem_addr(&s_tmem), 512);
@@ -699,14 +718,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
     bool ok = true;
     const uint32_t first_empty = pair_addr(acc_empty, 0);
     for (int slot = 0, i; ok && (i = sched.at(slot)) >= 0; ++slot) {
-      const Item t = item_at<P, CTAS>(p, sched, live, rank, i);
+      const Item t = item_at<P, PLANES, CTAS>(p, sched, live, rank, i);
       Entries e;
       if (P <= kGradient)  // under the products
         e.seek(p.w, p.g, t.row0 + quarter * 32 + threadIdx.x % 32, live, t.tile * kHeadTile + part * kMine);
       int chains = 1;
       if (kChain<P, PLANES> != INT_MAX) {
         int steps = 0;
-        for_steps<P>(p, t, [&](int, int, int) {
+        for_steps<P, Shape<PLANES, CTAS>::kK>(p, t, [&](int, int, int) {
           ++steps;
           return true;
         });
@@ -772,15 +791,18 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// A bf16 (fp32) matrix [rows][cols], row stride ld elements, read or written in boxes of 64 (32)
-// columns, 128 bytes.
-bool matrix_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f32 = false) {
+// A matrix [rows][cols], row stride ld elements, read or written in boxes: bf16 by 64 columns or fp32 by 32
+// (128 bytes, 128-byte swizzle), or bf16 by 32 (64 bytes, 64-byte swizzle).
+enum BoxKind { kBf16By64, kF32By32, kBf16By32 };
+bool matrix_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+                BoxKind kind = kBf16By64) {
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * (f32 ? 4 : 2)};
-  const cuuint32_t box[2] = {f32 ? 32u : 64u, (cuuint32_t)box_rows}, unit[2] = {1, 1};
-  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, unit,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * (kind == kF32By32 ? 4 : 2)};
+  const cuuint32_t box[2] = {kind == kBf16By64 ? 64u : 32u, (cuuint32_t)box_rows}, unit[2] = {1, 1};
+  return fn(m, kind == kF32By32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void*>(p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            kind == kBf16By32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -790,33 +812,36 @@ bool maps_for(GemmArgs* a, int dtype) {
   const HeadWork& w = a->w;
   const int planes = head_planes(dtype);
   const int64_t padded = (int64_t)g.tile0[RELAY_HEAD_MAX_SHARDS] * kHeadTile;
+  const int step = planes == 3 ? Shape<3, 1>::kK : Shape<1, 1>::kK;
+  const BoxKind inner = planes == 3 ? kBf16By32 : kBf16By64;  // boxes of one inner step
   bool ok = true;
-  // the weight: boxes of a CTA's share of 256 rows by 64 of dim (logits), or of 64 rows by 64 (d_hidden)
-  constexpr int kB = 1, kC = kB + RELAY_HEAD_MAX_SHARDS, kHid = kC + RELAY_HEAD_MAX_SHARDS, kDh = kHid + 1;
+  // the weight: boxes of a CTA's share of 256 rows by a step of dim (logits), or of a step of rows by 64 (d_hidden)
+  constexpr int kB = 1, kC = kB + RELAY_HEAD_MAX_SHARDS, kHid = kC + RELAY_HEAD_MAX_SHARDS, kDh = kHid + 1, kAw = kDh + 1;
   a->maps = 1;
-  auto weight = [&](int box_rows) {
+  auto weight = [&](int box_rows, BoxKind kind) {
     if (w.wpack != nullptr) {
       a->maps |= 1 << kB;
-      ok &= matrix_map(&a->b[0], w.wpack, planes * padded, g.dim, w.dim_pad, box_rows);
+      ok &= matrix_map(&a->b[0], w.wpack, planes * padded, g.dim, w.dim_pad, box_rows, kind);
     } else {
       for (int s = 0; s < g.A; ++s)
         if (g.rows[s] > 0) {
           a->maps |= 1 << (kB + s);
-          ok &= matrix_map(&a->b[s], a->sh.w[s], g.rows[s], g.dim, a->sh.w_ld, box_rows);
+          ok &= matrix_map(&a->b[s], a->sh.w[s], g.rows[s], g.dim, a->sh.w_ld, box_rows, kind);
         }
     }
   };
   const int64_t hid_rows = (int64_t)planes * g.mpad, grad_rows = (int64_t)w.grad_planes * g.mpad;
   if (P == kBack) {
-    ok &= matrix_map(&a->a, w.grad, grad_rows, w.grad_ld, w.grad_ld, kBK);
+    ok &= matrix_map(&a->a, w.grad, grad_rows, w.grad_ld, w.grad_ld, kBM, inner);
     if (a->want_dh) {
-      weight(kBK);
+      weight(step, kBf16By64);
       a->maps |= 1 << kDh;
-      ok &= matrix_map(&a->dh, w.dh, (int64_t)w.splits * g.mpad, g.dim, w.dh_ld, 32, true);
+      ok &= matrix_map(&a->dh, w.dh, (int64_t)w.splits * g.mpad, g.dim, w.dh_ld, 32, kF32By32);
     }
     if (a->want_dw) {
-      a->maps |= 1 << kHid;
-      ok &= matrix_map(&a->hid, w.hid, hid_rows, g.dim, w.dim_pad, kBK);
+      a->maps |= 1 << kHid | 1 << kAw;
+      ok &= matrix_map(&a->hid, w.hid, hid_rows, g.dim, w.dim_pad, step);
+      ok &= matrix_map(&a->aw, w.grad, grad_rows, w.grad_ld, w.grad_ld, step);
       a->out_map = 1;
       for (int s = 0; s < g.A; ++s)
         if (g.rows[s] > 0)
@@ -825,12 +850,12 @@ bool maps_for(GemmArgs* a, int dtype) {
         for (int s = 0; s < g.A; ++s)
           if (g.rows[s] > 0) {
             a->maps |= 1 << (kC + s);
-            ok &= matrix_map(&a->c[s], a->sh.dw[s], g.rows[s], g.dim, a->sh.dw_ld, 32, planes == 3);
+            ok &= matrix_map(&a->c[s], a->sh.dw[s], g.rows[s], g.dim, a->sh.dw_ld, 32, planes == 3 ? kF32By32 : kBf16By64);
           }
     }
   } else {
-    ok &= matrix_map(&a->a, w.hid, hid_rows, g.dim, w.dim_pad, kBM);
-    weight(kBN / g.ctas);
+    ok &= matrix_map(&a->a, w.hid, hid_rows, g.dim, w.dim_pad, kBM, inner);
+    weight(kBN / g.ctas, inner);
     if (P != kStats) {
       a->maps |= 1 << kC;
       ok &= matrix_map(&a->c[0], w.grad, grad_rows, w.grad_ld, w.grad_ld, 32);

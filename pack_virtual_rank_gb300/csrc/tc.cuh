@@ -170,16 +170,19 @@ __device__ __forceinline__ void tmem_load16(uint32_t tmem, float* v) {
       : "memory");
 }
 
-// Shared memory descriptors of 128-byte-swizzled bf16 operands (tiles at 1024-byte addresses).
-//  inner dimension contiguous: rows of 64 elements, 8 rows to a 1024-byte group.
-//  outer dimension contiguous: columns of 64 outer elements by 64 inner rows (8 KiB boxes); groups
-//  of 8 inner rows 1024 bytes apart, boxes of 64 outer elements 8192 bytes apart.
+// Shared memory descriptors of bf16 operands, K inner elements of them to a stage (tiles at 1024-byte addresses).
+//  inner dimension contiguous: rows of K elements with a swizzle of their width (128 or 64 bytes), groups
+//  of 8 rows one behind the other.
+//  outer dimension contiguous: boxes of 64 outer elements (128-byte rows and swizzle) by K inner rows;
+//  groups of 8 inner rows 1024 bytes apart, boxes of 64 outer elements 128 K bytes apart.
+template <int K>
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool outer_contiguous) {
+  static_assert(K == 64 || K == 32, "128 or 64 bytes");
   uint64_t d = (uint64_t)((addr & 0x3ffffu) >> 4);
-  d |= (uint64_t)(outer_contiguous ? 8192 >> 4 : 1) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)(outer_contiguous ? 128 * K >> 4 : 1) << 16;
+  d |= (uint64_t)(outer_contiguous ? 1024 >> 4 : 16 * K >> 4) << 32;
   d |= 1ull << 46;
-  d |= 2ull << 61;
+  d |= (outer_contiguous || K == 64 ? 2ull : 4ull) << 61;
   return d;
 }
 // Descriptor advance (16-byte units) for the next 16 elements of the inner dimension.
