@@ -414,7 +414,8 @@ int64_t relay_head_workspace_size(const relay_head_t* head, int top);
  * Arithmetic: products of the inputs accumulate in fp32; maxima, sums and the loss are
  * fp32. For a bf16 head the gradient of each logit is rounded to bf16 once before its two
  * products, which accumulate in fp32 and are rounded to bf16 once. Every sum has a fixed
- * order: equal calls give equal bits. An infinite or NaN logit gives its row NaN.
+ * order: equal calls give equal bits. A NaN or +infinite logit gives its
+ * row NaN; one of -inf has probability 0.
  * All pointers device memory, element-aligned; outputs overlap nothing else.
  * tokens == 0 writes zeros to d_weight.
  */

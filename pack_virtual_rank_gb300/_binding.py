@@ -525,14 +525,14 @@ def _common_stride(xs, name: str) -> int:
 
 
 def _own_workspace(alloc, stream):
-    """A workspace for one call. The allocator frees it in the order of the current stream, so a
-    call on another stream tells it so."""
-    ws = alloc()
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            raise ValueError("pass a workspace with a raw stream handle")
-        ws.record_stream(stream)
-    return ws
+    """A workspace for one call, allocated (and freed) in the order of the call's stream."""
+    if stream is None:
+        return alloc()
+    if not hasattr(stream, "cuda_stream"):
+        raise ValueError("pass a workspace with a raw stream handle")
+    import torch
+    with torch.cuda.stream(stream):
+        return alloc()
 
 
 def make_head(hidden, weights: Sequence, d_hidden=None, d_weights: Optional[Sequence] = None,
@@ -544,8 +544,10 @@ def make_head(hidden, weights: Sequence, d_hidden=None, d_weights: Optional[Sequ
     weights = list(weights)
     if not 1 <= len(weights) <= HEAD_MAX_SHARDS:
         raise ValueError(f"1 to {HEAD_MAX_SHARDS} weight shards, got {len(weights)}")
+    if _torch is None:
+        _bind_torch()
     h = RelayHead()
-    h.dtype, h.A = dtype_code(hidden.dtype), len(weights)
+    h.dtype, h.A = _dtype(hidden, "hidden"), len(weights)
     h.hidden = _matrix(hidden, "hidden")
     h.tokens, h.dim = hidden.shape
     h.hidden_stride = _row_stride(hidden)

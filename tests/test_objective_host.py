@@ -150,6 +150,8 @@ def test_binding_refuses_host_and_wrong_tensors(relay_lib):
     h, w = torch.zeros(4, 8), torch.zeros(10, 8)
     with pytest.raises(ValueError, match="device memory"):
         rv.make_head(h, [w])
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        rv.make_head(h.half(), [w.half()])
     with pytest.raises(ValueError, match="shards"):
         rv.make_head(h, [])
     with pytest.raises(ValueError, match="device memory"):
