@@ -658,12 +658,12 @@ def relay_router_forward(logits, index, gate, counts, prob_sum, mask=None, norma
         _bind_torch()
     ptr, t, e, stride = _rows(logits, "logits")
     tk = (t, index.shape[1])
-    if mask is not None:
-        mask = _array(mask, "mask", _torch.bool if mask.dtype is _torch.bool else _torch.uint8, (t,))
+    # `mask` stays the tensor: when nothing but the call holds it, the workspace below would take its memory
+    mask_ptr = 0 if mask is None else _array(mask, "mask", _torch.bool if mask.dtype is _torch.bool else _torch.uint8, (t,))
     if workspace is None:
         workspace = _own_workspace(lambda: alloc_router_workspace(t, e, logits.device), stream)
     _check(lib().relay_packed_router_forward(_pack15(
-        ptr, stride, _dtype(logits, "logits"), t, e, tk[1], bool(normalize), mask or 0,
+        ptr, stride, _dtype(logits, "logits"), t, e, tk[1], bool(normalize), mask_ptr,
         _array(index, "index", _int32, tk), _array(gate, "gate", _float32, tk),
         _array(counts, "counts", _int32, (e,)), _array(prob_sum, "prob_sum", _float32, (e,)),
         workspace.data_ptr(), workspace.numel(), _handle(stream))))
