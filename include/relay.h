@@ -444,8 +444,8 @@ relay_status_t relay_linear_distill(const relay_head_t* head, const void* teache
  * ---- Expert router: top-k choice, per-expert counts, balance loss ----
  *
  * relay_router_forward: logits[tokens][experts] (RELAY_F32 or RELAY_BF16, row_stride
- *   elements apart). A row is counted unless mask (NULL: all counted) holds 0 for it or no
- *   logit of it is above -inf.
+ *   elements apart). A row is counted unless mask (NULL: all counted) holds 0 for it or
+ *   every logit of it is -inf.
  *   index[tokens][top] int32: the top largest logits, largest first, ties to the lower
  *     expert; -1 for a row that is not counted. (A row with fewer than `top` logits above
  *     -inf fills up with the lowest experts left, gate 0.)
@@ -456,7 +456,8 @@ relay_status_t relay_linear_distill(const relay_head_t* head, const void* teache
  *     relay_allreduce over them between this call and relay_balance_loss, the balance
  *     loss is that of all ranks' tokens.
  *   1 <= top <= experts, top <= RELAY_ROUTER_MAX_TOP, experts <= RELAY_ROUTER_MAX_EXPERTS.
- *   A NaN logit makes its row's gates and prob_sum NaN; index stays in range and distinct.
+ *   A NaN or +infinite logit makes its row's gates and prob_sum NaN, whatever is beside it;
+ *   index stays in range and distinct, with a NaN below -inf.
  *   Two launches at most. workspace: relay_router_workspace_size bytes, any alignment.
  */
 #define RELAY_ROUTER_MAX_EXPERTS 1024

@@ -169,13 +169,14 @@ struct ForwardArgs {
 };
 
 // Chooses by whole values, NaN below -inf, for the L lanes of a row: lane j gets the j-th expert.
-// Returns whether the row has a logit above -inf. Rare, and kept out of the kernel's registers.
+// Returns whether the row has a logit above -inf, or a NaN: a row that a NaN has reached is counted, and shows
+// it. Rare, and kept out of the kernel's registers.
 template <class T, int N, int L>
 __device__ __noinline__ bool choose_exact(const T* x, int experts, int top, bool counted, int* chosen) {
   const int lane = threadIdx.x % 32, sub = lane % L;
   uint32_t last = ~0u;
   int last_e = -1;
-  bool live = false;
+  bool live = false, nan = false;
   for (int j = 0; j < top; ++j) {
     uint32_t best = 0;
     int best_e = 0;
@@ -183,6 +184,7 @@ __device__ __noinline__ bool choose_exact(const T* x, int experts, int top, bool
       const int e = sub * N + i;
       if (e >= experts) break;
       const float v = ld1(x + e);
+      nan |= v != v;
       const uint32_t k = v != v ? 1u : order_key(v);
       if ((k < last || (k == last && e > last_e)) && k > best) {
         best = k;
@@ -193,7 +195,7 @@ __device__ __noinline__ bool choose_exact(const T* x, int experts, int top, bool
     const unsigned holders = __ballot_sync(~0u, best == win) >> (lane - sub) & (L == 32 ? ~0u : (1u << (L % 32)) - 1);
     last_e = __shfl_sync(~0u, best_e, lane - sub + __ffs(holders) - 1);
     last = win;
-    if (j == 0) live = win > kKeyNegInf;
+    if (j == 0) live = max_row<L>(nan ? ~0u : win) > kKeyNegInf;
     if (sub == j) *chosen = last_e;
   }
   return live;
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) router_forward
     }
     if (!counted) best = second = third = 0;
     uint32_t win = max_row<L>(best);
-    bool live = win > (kKeyNegInf | kExpertMask);  // else masked out, or no logit above -inf
+    bool live = win > (kKeyNegInf | kExpertMask);  // else masked out, or no logit above -inf (NaN: choose_exact)
     // the largest value: a bf16 key holds all of it
     float m;
     if (sizeof(T) == 2) {
