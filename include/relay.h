@@ -415,7 +415,9 @@ int64_t relay_head_workspace_size(const relay_head_t* head, int top);
  * fp32. For a bf16 head the gradient of each logit is rounded to bf16 once before its two
  * products, which accumulate in fp32 and are rounded to bf16 once. Every sum has a fixed
  * order: equal calls give equal bits. A NaN or +infinite logit gives its
- * row NaN; one of -inf has probability 0.
+ * row NaN; one of -inf has probability 0 (a row of nothing else is NaN). An fp32 head multiplies
+ * bf16 parts of its values; it gives such logits as a product of fp32 values does, where the hidden
+ * value that meets an infinite weight is 0 or at least 2^-95.
  * All pointers device memory, element-aligned; outputs overlap nothing else.
  * tokens == 0 writes zeros to d_weight.
  */

@@ -64,8 +64,8 @@ int head_shard_of_tile(const HeadGeom& g, int tile) {
 }
 
 // Matrices the products read are bf16. An fp32 value is held as three bf16 parts that sum to
-// it (to 2^-26 of it), in three planes; a product of two such matrices is the sum of the six
-// products of parts above 2^-24.
+// it (to 2^-26 of it at least), in three planes; a product of two such matrices is the sum of six
+// products of parts. The three left out are at most 1.5e-7 of it (2^-22.7; see the packing for the split).
 constexpr int kHeadPlanesF32 = 3;
 inline int head_planes(int dtype) { return dtype == RELAY_F32 ? kHeadPlanesF32 : 1; }
 // Parts the gradient of a logit is held in. One bf16 value is as exact as the bf16 results want where

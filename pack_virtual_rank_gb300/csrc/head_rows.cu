@@ -50,21 +50,39 @@ __device__ __forceinline__ uint4 ld_once(const void* p) {
   return r;
 }
 
-// The three bf16 parts of an fp32 value. A value that rounds to infinity is cut instead, and an
-// infinity or NaN is its first part alone.
+// The three bf16 parts of an fp32 value; an infinity or NaN is its first part alone. Every part multiplies parts of
+// the other operand (six of the nine products), so what one product says about infinities the others must not
+// contradict: a logit that is -inf has to come out as -inf, not as NaN.
+//
+// `below`: each part is the largest bf16 value below what is left, so that all parts have the value's sign and none
+// is 0 (for a value of 2^-95 at least, whose third part bf16 still holds). Their sum is the value exactly. Hidden is
+// always split so: its parts times an infinite weight, or parts of products that leave fp32's range, are infinite with one
+// sign, and a hidden value of 0 times an infinite weight is NaN as it should be. A weight is split so
+// from 512 on. Smaller ones are rounded: the second part of a weight below 512 is at most 1 and brings no product out of
+// range by itself, and rounded parts keep what the three left-out products amount to at 1.5e-7 of a product (both operands
+// split below: 4e-7, and always towards 0).
+template <bool HIDDEN>
 __device__ __forceinline__ void parts_of(float v, uint16_t (&o)[3]) {
+  const uint32_t u = __float_as_uint(v), size = u & 0x7fffffffu;
+  if (size >= 0x7f800000u) {
+    o[0] = (uint16_t)((v != v ? u | 0x00400000u : u) >> 16);
+    o[1] = o[2] = 0;
+    return;
+  }
+  const bool below = HIDDEN || size >= 0x44000000u;  // 512
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
+    const uint32_t bits = __float_as_uint(v);
     uint32_t r = bf16x2_rn(v, 0.0f) << 16;
-    if ((r & 0x7f800000u) == 0x7f800000u && v == v) r = __float_as_uint(v) & 0xffff0000u;
+    if (i < 2 && below) r = (bits & 0x7fffffffu) == 0 ? bits : (bits - 1) & 0xffff0000u;
     o[i] = (uint16_t)(r >> 16);
-    const float left = __fsub_rn(v, __uint_as_float(r));
-    v = (r & 0x7f800000u) == 0x7f800000u ? 0.0f : left;
+    v = __fsub_rn(v, __uint_as_float(r));
   }
 }
 
 // A warp copies one row to its packed place: bf16 as it is, fp32 in three parts, `plane` elements
 // apart. Columns from dim to pad, and all of them when from is NULL, are 0. vec: 16-byte loads.
+template <bool HIDDEN>
 __device__ __forceinline__ void pack_row(uint16_t* to, int64_t, const uint16_t* from, int dim, int pad, bool vec) {
   const int lane = threadIdx.x % 32;
   if (from != nullptr && !vec) {
@@ -102,6 +120,7 @@ __device__ __forceinline__ void pack_row(uint16_t* to, int64_t, const uint16_t* 
   }
   for (int d = vecs * 8 + lane; d < pad; d += 32) to[d] = d < dim ? from[d] : (uint16_t)0;
 }
+template <bool HIDDEN>
 __device__ __forceinline__ void pack_row(uint16_t* to, int64_t plane, const float* from, int dim, int pad, bool vec) {
   const int lane = threadIdx.x % 32;
   for (int d0 = lane * 8; d0 < pad; d0 += 8 * 32) {  // pad is a multiple of 8
@@ -115,7 +134,7 @@ __device__ __forceinline__ void pack_row(uint16_t* to, int64_t plane, const floa
     }
     uint16_t o[8][3];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) parts_of(x[i], o[i]);
+    for (int i = 0; i < 8; ++i) parts_of<HIDDEN>(x[i], o[i]);
 #pragma unroll
     for (int k = 0; k < 3; ++k)
       *reinterpret_cast<uint4*>(to + k * plane + d0) =
@@ -138,7 +157,7 @@ __global__ void __launch_bounds__(kThreadsRows)
   const int row = blockIdx.x * (kThreadsRows / 32) + threadIdx.x / 32;  // rows: a multiple of 256
   const int a = head_shard_of_tile(g, row / kHeadTile), v = row - g.tile0[a] * kHeadTile;
   const T* from = v < g.rows[a] ? static_cast<const T*>(sh.w[a]) + v * sh.w_ld : nullptr;
-  pack_row(w.wpack + (int64_t)row * w.dim_pad, (int64_t)rows * w.dim_pad, from, g.dim, w.dim_pad, vec);
+  pack_row<false>(w.wpack + (int64_t)row * w.dim_pad, (int64_t)rows * w.dim_pad, from, g.dim, w.dim_pad, vec);
 }
 
 // One warp per row: the entries' columns in ascending order (by counting, each lane holds up to
@@ -295,11 +314,11 @@ __global__ void __launch_bounds__(kThreadsRows)
       const int r = base + i, place = s_place[i];
       if (SOURCE == kFromEntries) teacher_row(g, w, teacher, index, r);
       if (place >= 0) {
-        pack_row(w.hid + (int64_t)place * w.dim_pad, plane, hidden + r * ld, g.dim, w.dim_pad, vec);
+        pack_row<true>(w.hid + (int64_t)place * w.dim_pad, plane, hidden + r * ld, g.dim, w.dim_pad, vec);
       } else {
         if (dh != nullptr) zero_row(dh + r * dh_ld, g.dim);
         if (~place < read_end)
-          pack_row(w.hid + (int64_t)~place * w.dim_pad, plane, static_cast<const T*>(nullptr), g.dim, w.dim_pad, vec);
+          pack_row<true>(w.hid + (int64_t)~place * w.dim_pad, plane, static_cast<const T*>(nullptr), g.dim, w.dim_pad, vec);
       }
     }
     __syncthreads();
@@ -311,7 +330,7 @@ __global__ void __launch_bounds__(kThreadsRows)
       w.wrow[place] = 0.0f;
     }
     if (place < read_end)
-      pack_row(w.hid + (int64_t)place * w.dim_pad, plane, static_cast<const T*>(nullptr), g.dim, w.dim_pad, vec);
+      pack_row<true>(w.hid + (int64_t)place * w.dim_pad, plane, static_cast<const T*>(nullptr), g.dim, w.dim_pad, vec);
   }
 }
 
