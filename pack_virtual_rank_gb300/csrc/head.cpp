@@ -111,7 +111,7 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
   w.ent_q = reinterpret_cast<float*>(l.take(4 * ents));
   w.ent_z = reinterpret_cast<float*>(l.take(4 * ents));
   w.part = reinterpret_cast<float2*>(l.take(8ll * tiles * (kHeadTile / kHeadStatTile) * g.mpad));
-  w.lse = reinterpret_cast<float*>(l.take(4ll * g.mpad));
+  w.lse = reinterpret_cast<float2*>(l.take(8ll * g.mpad));
   ar.tiles_per_piece = tiles;
   if ((dh || dw) && g.mpad > 0) {
     const int64_t cap = h.piece_bytes > 0 ? h.piece_bytes : RELAY_HEAD_PIECE_BYTES;
@@ -327,7 +327,8 @@ relay_status_t relay_linear_distill(const relay_head_t* head, const void* teache
     if (st != RELAY_OK) return st;
     if (teacher_dtype != RELAY_F32 && teacher_dtype != RELAY_BF16)
       return bad("teacher_dtype must be RELAY_F32 or RELAY_BF16");
-    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
+    // its reciprocal is used times log2 e
+    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.4426951f / temperature))
       return bad("temperature must be finite and positive");
     g.tau = temperature;
     g.inv_tau = 1.0f / temperature;

@@ -81,6 +81,14 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 #endif
 
+// Softmax statistics are kept as the largest logit itself and the sum of the exponentials below it, and a logit meets
+// the largest before the temperature and log2 e: the type's lowest and largest values times log2 e leave
+// fp32's range, their differences end at an exponential of 0. A row's log-sum-exp is not joined into
+// one number either: next to a large logit the log of the sum would be lost.
+#ifdef __CUDACC__
+__device__ __forceinline__ float head_log2_scale(const HeadGeom& g) { return g.inv_tau * 1.4426950408889634f; }
+#endif
+
 // Everything a call works with on the device.
 struct HeadWork {
   int32_t* n_live;    // [2]: live rows, cuts of the vocabulary for d_hidden
@@ -92,9 +100,9 @@ struct HeadWork {
   uint8_t* live;      // [tokens]            (distill)
   int32_t* ent_col;   // [tokens][top] entries' padded columns, ascending; INT32_MAX: absent
   float* ent_q;       // [tokens][top]
-  float* ent_z;       // [tokens][top] the entries' logits / tau
-  float2* part;       // [2 tiles][mpad] (max, sum of exp) of kHeadStatTile columns, log2 units
-  float* lse;         // [mpad] log2 units
+  float* ent_z;       // [tokens][top] the entries' logits
+  float2* part;       // [2 tiles][mpad] (largest logit, sum of exp((z - it) / tau)) of kHeadStatTile columns
+  float2* lse;        // [mpad] the row's largest logit, and the log2 of its sum
   uint16_t* grad;     // [grad_planes][mpad][grad_ld] of one piece: codes or exponentials, then the gradient
   int32_t grad_planes;
   int64_t grad_ld;    // columns per row

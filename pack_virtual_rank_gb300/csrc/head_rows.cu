@@ -339,40 +339,42 @@ __global__ void __launch_bounds__(kThreadsRows)
 // stride over the columns and join in shared memory, in a fixed order. Then a warp per row sums
 // its entries.
 constexpr int kCombineWarps = 32;
-__device__ __forceinline__ void join(float& m, float& s, float pm, float ps) {
+__device__ __forceinline__ void join(float& m, float& s, float pm, float ps, float scale) {
   const float top = fmaxf(m, pm);
   // -inf - -inf: a side that holds nothing yet adds nothing
-  s = (m > -INFINITY || s != s ? s * exp2f(m - top) : 0.0f) + (pm > -INFINITY || ps != ps ? ps * exp2f(pm - top) : 0.0f);
+  s = (m > -INFINITY || s != s ? s * exp2f((m - top) * scale) : 0.0f) +
+      (pm > -INFINITY || ps != ps ? ps * exp2f((pm - top) * scale) : 0.0f);
   m = top;
 }
-// Joins the lanes' shares; every lane gets the row's log-sum-exp in log2 units.
-__device__ __forceinline__ float join_warp(float m, float s) {
+// Joins the lanes' shares; every lane gets the row's largest logit and the log2 of its sum.
+__device__ __forceinline__ float2 join_warp(float m, float s, float scale) {
   const int lane = threadIdx.x % 32;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float pm = __shfl_xor_sync(~0u, m, o), ps = __shfl_xor_sync(~0u, s, o);
     // both sides of a pair join in the same order: the lower lane's share first
     float am = lane & o ? pm : m, as = lane & o ? ps : s;
-    join(am, as, lane & o ? m : pm, lane & o ? s : ps);
+    join(am, as, lane & o ? m : pm, lane & o ? s : ps, scale);
     m = am;
     s = as;
   }
-  return m + log2f(s);
+  return make_float2(m, log2f(s));
 }
 // The loss of a packed row, by one warp.
 template <bool DISTILL>
-__device__ __forceinline__ void row_loss(const HeadGeom& g, const HeadWork& w, int row, float lse2, float* loss) {
+__device__ __forceinline__ void row_loss(const HeadGeom& g, const HeadWork& w, int row, float2 lse, float* loss) {
   const int lane = threadIdx.x % 32, r = w.perm[row];
-  const float lse = lse2 * 0.6931471805599453f;
+  const float log_sum = lse.y * 0.6931471805599453f;
   const int64_t at = (int64_t)r * g.top;
   if (!DISTILL) {
-    if (lane == 0) loss[r] = lse - w.ent_z[at];
+    if (lane == 0) loss[r] = (lse.x - w.ent_z[at]) + log_sum;
     return;
   }
   float sum = 0.0f;
   for (int k = lane; k < g.top; k += 32) {
     const float q = w.ent_q[at + k];
-    if (w.ent_col[at + k] != INT_MAX && q != 0.0f) sum += q * (logf(q) - (w.ent_z[at + k] - lse));  // 0 log 0 = 0
+    if (w.ent_col[at + k] != INT_MAX && q != 0.0f)  // 0 log 0 = 0
+      sum += q * (logf(q) + ((lse.x - w.ent_z[at + k]) * g.inv_tau + log_sum));
   }
   sum = warp_sum(sum);
   if (lane == 0) loss[r] = g.tau * g.tau * sum;
@@ -385,6 +387,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const HeadG
   const int live = *w.n_live, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int row = blockIdx.x * 32 + lane, parts = g.tile0[RELAY_HEAD_MAX_SHARDS] * (kHeadTile / kHeadStatTile);
   if ((int)blockIdx.x * 32 >= live) return;
+  const float scale = head_log2_scale(g);
   float m = -INFINITY, s = 0.0f;
   if (row < live)
     for (int t = warp; t < parts; t += 4 * kCombineWarps) {
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const HeadG
         p[i] = t + i * kCombineWarps < parts ? w.part[(int64_t)(t + i * kCombineWarps) * g.mpad + row]
                                              : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) join(m, s, p[i].x, p[i].y);
+      for (int i = 0; i < 4; ++i) join(m, s, p[i].x, p[i].y, scale);
     }
   s_max[warp][lane] = m;
   s_sum[warp][lane] = s;
@@ -402,9 +405,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const HeadG
   // warp i takes row i: lanes are the warps' shares
   const int mine = blockIdx.x * 32 + warp;
   if (mine >= live) return;
-  const float lse2 = join_warp(s_max[lane][warp], s_sum[lane][warp]);
-  if (lane == 0) w.lse[mine] = lse2;
-  row_loss<DISTILL>(g, w, mine, lse2, loss);
+  const float2 lse = join_warp(s_max[lane][warp], s_sum[lane][warp], scale);
+  if (lane == 0) w.lse[mine] = lse;
+  row_loss<DISTILL>(g, w, mine, lse, loss);
 }
 
 // Kept exponentials to the gradient of the logits, in place: each is relative to the maximum of
@@ -419,7 +422,7 @@ static_assert(RELAY_HEAD_MAX_TOP <= kThreadsRows && kScaleCols % (32 * kHeadStat
 // work for it first.
 template <int PLANES, int JOIN>
 __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, const HeadWork w, float* loss) {
-  __shared__ float s_lse;
+  __shared__ float2 s_lse;
   dep_launch();
   dep_wait();
   const int row = blockIdx.x, col0 = blockIdx.y * kScaleCols;
@@ -450,8 +453,8 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
   const int live = *w.n_live, row_tile = head_row_tile(g);
   const int64_t at = (int64_t)w.perm[row] * g.top;
   const bool on = row < live;
-  const float weight = w.wrow[row];
-  float lse = JOIN == 0 ? w.lse[row] : 0.0f;
+  const float weight = w.wrow[row], scale = head_log2_scale(g);
+  float2 lse = JOIN == 0 ? w.lse[row] : make_float2(0.0f, 0.0f);
   if (row >= (live + row_tile - 1) / row_tile * row_tile) return;
   // the thread's entry, if any: at most RELAY_HEAD_MAX_TOP of them
   const bool has = on && (int)threadIdx.x < g.top;
@@ -461,16 +464,16 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
     if (threadIdx.x < 32) {
       float m = -INFINITY, s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kShares; ++i) join(m, s, share[i].x, share[i].y);
-      const float lse2 = join_warp(m, s);
-      if (threadIdx.x == 0) s_lse = lse2;
+      for (int i = 0; i < kShares; ++i) join(m, s, share[i].x, share[i].y, scale);
+      const float2 all = join_warp(m, s, scale);
+      if (threadIdx.x == 0) s_lse = all;
     }
     __syncthreads();
     lse = s_lse;
     if (threadIdx.x >= kThreadsRows - 32) row_loss<JOIN == 2>(g, w, row, lse, loss);
   }
 #pragma unroll
-  for (int k = 0; k < kScaleVecs; ++k) ref[k] -= lse;
+  for (int k = 0; k < kScaleVecs; ++k) ref[k] = fmaf(ref[k] - lse.x, scale, -lse.y);
 #pragma unroll
   for (int k = 0; k < kScaleVecs; ++k) {
     const int col = col0 + (k * kThreadsRows + threadIdx.x) * 8;
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kThreadsRows) scale_kernel(const HeadGeom g, c
     if (c < col0 || c >= col0 + kScaleCols || c >= cols || (k > 0 && w.ent_col[at + k - 1] == c)) return;
     float q = 0.0f;  // an id given several times: its first entry sums them
     for (int j = k; j < g.top && w.ent_col[at + j] == c; ++j) q += w.ent_q[at + j];
-    float v = weight * (exp2f(fmaf(ent_z, 1.4426950408889634f, -lse)) - q);
+    float v = weight * (exp2f(fmaf(ent_z - lse.x, scale, -lse.y)) - q);
     for (int i = 0; i < w.grad_planes; ++i) {
       const uint32_t r = bf16x2_rn(v, 0.0f) & 0xffffu;
       line[i * plane + c] = (uint16_t)r;
