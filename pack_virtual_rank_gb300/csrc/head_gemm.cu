@@ -78,12 +78,15 @@ enum Product { kStats, kStatsKeep, kGradient, kBack };
 
 // Inner steps summed in tensor memory before the sum moves on into registers. The tensor
 // cores cut what does not fit 24 bits at every product instead of rounding it, which drifts with
-// the length of the chain: at dim 4096 in one chain the loss was several times as far from its
-// 64-bit value as an fp32 sum. A chain of 48 products leaves it 3.7e-7 off at 2047 x 2048 x 50001 (32
-// products: 2.6e-7 and 1% more time; 64: 5.5e-7 and 1% less; the plain fp32 form 4e-7). A result that
-// is rounded to bf16 does not show the drift.
+// the length of the chain: a product costs a sum of one sign about 1e-7 of it. At dim 4096 in one chain the loss was
+// several times as far from its 64-bit value as an fp32 sum. A chain of 48 products leaves it 3.7e-7 off at
+// 2047 x 2048 x 50001 (32 products: 2.6e-7 and 1% more time; 64: 5.5e-7 and 1% less; the plain fp32 form 4e-7). The
+// gradients of a bf16 head move on every 256 products: over 8192 products of one sign (131072 tokens, or as many
+// columns) their mean is then 0.6e-5 and 1.4e-5 low, where one chain was 8.0e-4 and 7.8e-4 low, half of what rounding to bf16
+// does, and always towards 0. It takes 1% more time at 2047 x 2048 x 50001 (610 -> 616 us) and 3% at
+// 8192 x 4096 x 131072 (18.5 -> 19.0 ms); 384 products: 2.5e-5, 0.5% faster.
 template <int P, int PLANES>
-constexpr int kChain = PLANES == 3 ? 4 : P == kBack ? INT_MAX : 12;
+constexpr int kChain = PLANES == 3 ? 4 : P == kBack ? 64 : 12;
 
 struct GemmArgs {
   CUtensorMap a;                         // first operand: hidden (logits), gradient (d_hidden)
@@ -219,6 +222,20 @@ __device__ __forceinline__ bool for_steps(const GemmArgs& p, const Item& t, F f)
     }
   }
   return true;
+}
+
+// How many they are.
+template <int P, int KK>
+__device__ __forceinline__ int count_steps(const GemmArgs& p, const Item& t) {
+  if (P != kBack || t.weight) return t.k_hi - t.k_lo;
+  int steps = 0;
+  for (int tile = t.k_lo; tile < t.k_hi;) {  // a shard at a time: only its last tile has fewer
+    const int shard = head_shard_of_tile(p.g, tile), end = min(t.k_hi, p.g.tile0[shard + 1]);
+    const int v0 = (tile - p.g.tile0[shard]) * kHeadTile, v1 = (end - p.g.tile0[shard]) * kHeadTile;
+    steps += (min(v1, p.g.rows[shard]) - v0 + KK - 1) / KK;
+    tile = end;
+  }
+  return steps;
 }
 
 // Products of parts that make up an fp32 product, small ones first: 2 0 0 1 1 0 with 0 2 1 0 1 0.
@@ -736,22 +753,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
       Entries e;
       if (P <= kGradient)  // under the products
         e.seek(p.w, p.g, t.row0 + quarter * 32 + threadIdx.x % 32, live, t.tile * kHeadTile + part * kMine);
-      int chains = 1;
-      if (kChain<P, PLANES> != INT_MAX) {
-        int steps = 0;
-        for_steps<P, Shape<PLANES, CTAS>::kK>(p, t, [&](int, int, int) {
-          ++steps;
-          return true;
-        });
-        chains = max(1, (steps + kChain<P, PLANES> - 1) / kChain<P, PLANES>);
-      }
+      const int steps = count_steps<P, Shape<PLANES, CTAS>::kK>(p, t);
+      const int chains = max(1, (steps + kChain<P, PLANES> - 1) / kChain<P, PLANES>);
       float v[kMine];
       for (int c = 0; c < chains; ++c, ++n) {
         const int half = n & 1;
         if (!(ok = __all_sync(~0u, bar_wait(acc_full + 8 * half, (n >> 1) & 1, &s_gave_up)))) break;
         tc_fence_after();
         const uint32_t acc = tmem + half * kBN + part * kMine + ((uint32_t)(quarter * 32) << 16);
-        if (kChain<P, PLANES> == INT_MAX || c == 0) {
+        if (c == 0) {
 #pragma unroll
           for (int j = 0; j < kMine; j += 16) tmem_load16(acc + j, v + j);
         } else {
