@@ -48,6 +48,7 @@ def _stale() -> bool:
                                                        os.path.join(CSRC, "head.h"),
                                                        os.path.join(CSRC, "tc.cuh"),
                                                        os.path.join(CSRC, "launch.cuh"),
+                                                       os.path.join(CSRC, "spans.h"),
                                                        os.path.join(INCLUDE, "relay.h"), __file__]
     return any(os.path.getmtime(d) > t for d in deps)
 

@@ -20,6 +20,7 @@
 
 #include "head.h"
 #include "program.h"
+#include "spans.h"
 
 namespace relay {
 namespace {
@@ -137,8 +138,8 @@ Arrangement arrange(const relay_head_t& h, const HeadGeom& g, int top, uintptr_t
   return ar;
 }
 
-struct Span {
-  uintptr_t lo, hi;
+struct Named {
+  Span span;
   std::string what;
 };
 
@@ -147,15 +148,12 @@ relay_status_t check_buffers(const relay_head_t& h, const HeadGeom& g, int top, 
                              const float* loss, const void* workspace, int64_t workspace_bytes,
                              int64_t need) {
   const int64_t E = esize_of(h.dtype);
-  std::vector<Span> in, out;
-  auto put = [&](std::vector<Span>& v, const void* p, int64_t bytes, const std::string& what) {
-    if (p != nullptr && bytes > 0) {
-      const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-      v.push_back(Span{lo, lo + (uintptr_t)bytes, what});
-    }
+  std::vector<Named> in, out;
+  auto matrix = [&](std::vector<Named>& v, const void* p, int64_t rows, int64_t ld, const std::string& what) {
+    v.push_back(Named{matrix_span(p, rows, g.dim * E, ld * E), what});
   };
-  auto matrix = [&](std::vector<Span>& v, const void* p, int64_t rows, int64_t ld, const std::string& what) {
-    if (rows > 0) put(v, p, ((rows - 1) * ld + g.dim) * E, what);
+  auto put = [&](std::vector<Named>& v, const void* p, int64_t bytes, const std::string& what) {
+    v.push_back(Named{array_span(p, bytes), what});
   };
   auto aligned = [](const void* p, int64_t e) { return reinterpret_cast<uintptr_t>(p) % e == 0; };
   const bool dw = wants_dw(h);
@@ -197,9 +195,9 @@ relay_status_t check_buffers(const relay_head_t& h, const HeadGeom& g, int top, 
   put(out, workspace, workspace_bytes, "workspace");
   for (size_t i = 0; i < out.size(); ++i) {
     for (size_t j = i + 1; j < out.size(); ++j)
-      if (out[i].lo < out[j].hi && out[j].lo < out[i].hi) return bad(out[i].what + " overlaps " + out[j].what);
-    for (const Span& s : in)
-      if (out[i].lo < s.hi && s.lo < out[i].hi) return bad(out[i].what + " overlaps " + s.what);
+      if (overlap(out[i].span, out[j].span)) return bad(out[i].what + " overlaps " + out[j].what);
+    for (const Named& s : in)
+      if (overlap(out[i].span, s.span)) return bad(out[i].what + " overlaps " + s.what);
   }
   return RELAY_OK;
 }

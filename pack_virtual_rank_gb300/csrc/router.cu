@@ -30,6 +30,7 @@
 #include "device.cuh"
 #include "launch.cuh"
 #include "program.h"
+#include "spans.h"
 
 namespace relay {
 namespace {
@@ -508,19 +509,19 @@ relay_status_t check_shape(relay_dtype_t dtype, int64_t tokens, int experts, int
   return RELAY_OK;
 }
 
-struct Span {
-  uintptr_t lo, hi;
+struct Array {
+  Span span;
   const char* what;
   bool out;
 };
-Span span(const void* p, int64_t bytes, const char* what, bool out) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Span{lo, lo + (uintptr_t)(p != nullptr ? bytes : 0), what, out};
+Array array(const void* p, int64_t bytes, const char* what, bool out) { return Array{array_span(p, bytes), what, out}; }
+Array matrix(const void* p, int64_t rows, int64_t width, int64_t pitch, const char* what, bool out) {
+  return Array{matrix_span(p, rows, width, pitch), what, out};
 }
-relay_status_t check_spans(const Span* s, int n) {
+relay_status_t check_overlaps(const Array* s, int n) {
   for (int i = 0; i < n; ++i)
     for (int j = i + 1; j < n; ++j)
-      if ((s[i].out || s[j].out) && s[i].lo < s[j].hi && s[j].lo < s[i].hi)
+      if ((s[i].out || s[j].out) && overlap(s[i].span, s[j].span))
         return bad(std::string(s[i].what) + " overlaps " + s[j].what);
   return RELAY_OK;
 }
@@ -570,14 +571,14 @@ relay_status_t relay_router_forward(const void* logits, int64_t row_stride, rela
     if (workspace == nullptr) return bad("workspace is NULL");
     if (workspace_bytes < need)
       return bad("the workspace holds " + std::to_string(workspace_bytes) + " bytes, " + std::to_string(need) + " are needed");
-    const Span s[] = {span(logits, tokens ? ((tokens - 1) * row_stride + experts) * E : 0, "logits", false),
-                      span(mask, tokens, "mask", false),
-                      span(index, tokens * top * 4, "index", true),
-                      span(gate, tokens * top * 4, "gate", true),
-                      span(counts, experts * 4, "counts", true),
-                      span(prob_sum, experts * 4, "prob_sum", true),
-                      span(workspace, need, "workspace", true)};
-    st = check_spans(s, 7);
+    const Array s[] = {matrix(logits, tokens, experts * E, row_stride * E, "logits", false),
+                      array(mask, tokens, "mask", false),
+                      array(index, tokens * top * 4, "index", true),
+                      array(gate, tokens * top * 4, "gate", true),
+                      array(counts, experts * 4, "counts", true),
+                      array(prob_sum, experts * 4, "prob_sum", true),
+                      array(workspace, need, "workspace", true)};
+    st = check_overlaps(s, 7);
     if (st != RELAY_OK) return st;
     int rows = kRouterWarps;
     by_width(experts, top, [&](auto, auto l) {
@@ -613,9 +614,9 @@ relay_status_t relay_balance_loss(const int32_t* counts, const float* prob_sum, 
     if (counts == nullptr || prob_sum == nullptr || loss == nullptr || d_prob == nullptr)
       return bad("counts, prob_sum, loss or d_prob is NULL");
     if (off(counts, 4) || off(prob_sum, 4) || off(loss, 4) || off(d_prob, 4)) return bad("an array is not element-aligned");
-    const Span s[] = {span(counts, experts * 4, "counts", false), span(prob_sum, experts * 4, "prob_sum", false),
-                      span(loss, 4, "loss", true), span(d_prob, experts * 4, "d_prob", true)};
-    st = check_spans(s, 4);
+    const Array s[] = {array(counts, experts * 4, "counts", false), array(prob_sum, experts * 4, "prob_sum", false),
+                      array(loss, 4, "loss", true), array(d_prob, experts * 4, "d_prob", true)};
+    st = check_overlaps(s, 4);
     if (st != RELAY_OK) return st;
     return done(launch_chained(balance_kernel, 1, kBalanceThreads, 0, stream, counts, prob_sum, experts, top, coef, loss,
                                d_prob));
@@ -637,12 +638,12 @@ relay_status_t relay_router_backward(const void* logits, int64_t row_stride, rel
     const int E = esize_of(dtype);
     if (off(logits, E) || off(d_logits, E) || off(index, 4) || off(d_gate, 4) || off(d_prob, 4))
       return bad("an array is not element-aligned");
-    const Span s[] = {span(logits, ((tokens - 1) * row_stride + experts) * E, "logits", false),
-                      span(index, tokens * top * 4, "index", false),
-                      span(d_gate, tokens * top * 4, "d_gate", false),
-                      span(d_prob, experts * 4, "d_prob", false),
-                      span(d_logits, ((tokens - 1) * d_row_stride + experts) * E, "d_logits", true)};
-    st = check_spans(s, 5);
+    const Array s[] = {matrix(logits, tokens, experts * E, row_stride * E, "logits", false),
+                      array(index, tokens * top * 4, "index", false),
+                      array(d_gate, tokens * top * 4, "d_gate", false),
+                      array(d_prob, experts * 4, "d_prob", false),
+                      matrix(d_logits, tokens, experts * E, d_row_stride * E, "d_logits", true)};
+    st = check_overlaps(s, 5);
     if (st != RELAY_OK) return st;
     const BackwardArgs a{logits, d_logits, row_stride, d_row_stride, tokens, experts, top, normalize,
                          load_bytes(logits, row_stride, E, experts), load_bytes(d_logits, d_row_stride, E, experts),
