@@ -535,6 +535,13 @@ def _own_workspace(alloc, stream):
         return alloc()
 
 
+def _space(x):
+    """Address and bytes of a workspace (any type)."""
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor (device memory)")
+    return x.data_ptr(), x.numel() * x.element_size()
+
+
 def make_head(hidden, weights: Sequence, d_hidden=None, d_weights: Optional[Sequence] = None,
               piece_bytes: int = 0) -> RelayHead:
     """Describe an output projection for relay_linear_xent and relay_linear_distill:
@@ -601,7 +608,7 @@ def relay_linear_xent(head: RelayHead, targets, loss, row_weight=None, workspace
     _check(lib().relay_linear_xent(
         ctypes.byref(head), _array(targets, "targets", _int32, t),
         None if row_weight is None else _array(row_weight, "row_weight", _float32, t),
-        _array(loss, "loss", _float32, t), workspace.data_ptr(), workspace.numel(), _handle(stream)))
+        _array(loss, "loss", _float32, t), *_space(workspace), _handle(stream)))
 
 
 def relay_linear_distill(head: RelayHead, teacher_logits, teacher_index, temperature: float, loss,
@@ -618,7 +625,7 @@ def relay_linear_distill(head: RelayHead, teacher_logits, teacher_index, tempera
         ctypes.byref(head), _array(teacher_logits, "teacher_logits", teacher_logits.dtype, t + (top,)),
         code, _array(teacher_index, "teacher_index", _int32, t + (top,)), top, temperature,
         None if row_weight is None else _array(row_weight, "row_weight", _float32, t),
-        _array(loss, "loss", _float32, t), workspace.data_ptr(), workspace.numel(), _handle(stream)))
+        _array(loss, "loss", _float32, t), *_space(workspace), _handle(stream)))
 
 
 def alloc_router_workspace(tokens: int, experts: int, device):
@@ -666,7 +673,7 @@ def relay_router_forward(logits, index, gate, counts, prob_sum, mask=None, norma
         ptr, stride, _dtype(logits, "logits"), t, e, tk[1], bool(normalize), mask_ptr,
         _array(index, "index", _int32, tk), _array(gate, "gate", _float32, tk),
         _array(counts, "counts", _int32, (e,)), _array(prob_sum, "prob_sum", _float32, (e,)),
-        workspace.data_ptr(), workspace.numel(), _handle(stream))))
+        *_space(workspace), _handle(stream))))
 
 
 def relay_balance_loss(counts, prob_sum, top: int, coef: float, loss, d_prob, stream=None) -> None:
