@@ -542,6 +542,12 @@ def _space(x):
     return x.data_ptr(), x.numel() * x.element_size()
 
 
+def _columns(x, name: str) -> int:
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, a row of choices for each token, got {tuple(x.shape)}")
+    return x.shape[1]
+
+
 def make_head(hidden, weights: Sequence, d_hidden=None, d_weights: Optional[Sequence] = None,
               piece_bytes: int = 0) -> RelayHead:
     """Describe an output projection for relay_linear_xent and relay_linear_distill:
@@ -617,7 +623,7 @@ def relay_linear_distill(head: RelayHead, teacher_logits, teacher_index, tempera
     teacher_index (outside the vocabulary: no entry), with the gradients the head asks for."""
     if _torch is None:
         _bind_torch()
-    t, top = (head.tokens,), teacher_index.shape[1]
+    t, top = (head.tokens,), _columns(teacher_index, "teacher_index")
     if workspace is None:
         workspace = _own_workspace(lambda: alloc_head_workspace(head, loss.device, top), stream)
     code = _dtype(teacher_logits, "teacher_logits")
@@ -664,7 +670,7 @@ def relay_router_forward(logits, index, gate, counts, prob_sum, mask=None, norma
     if _torch is None:
         _bind_torch()
     ptr, t, e, stride = _rows(logits, "logits")
-    tk = (t, index.shape[1])
+    tk = (t, _columns(index, "index"))
     # `mask` stays the tensor: when nothing but the call holds it, the workspace below would take its memory
     mask_ptr = 0 if mask is None else _array(mask, "mask", _torch.bool if mask.dtype is _torch.bool else _torch.uint8, (t,))
     if workspace is None:
@@ -695,9 +701,9 @@ def relay_router_backward(logits, index, d_logits, d_gate=None, d_prob=None, nor
         _bind_torch()
     ptr, t, e, stride = _rows(logits, "logits")
     d_ptr, d_t, d_e, d_stride = _rows(d_logits, "d_logits")
-    tk = index.shape
-    if d_logits.dtype is not logits.dtype or d_t != t or d_e != e or len(tk) != 2 or tk[0] != t:
-        raise ValueError("d_logits must have the logits' dtype and shape, index a row for each of theirs")
+    tk = (t, _columns(index, "index"))
+    if d_logits.dtype is not logits.dtype or d_t != t or d_e != e:
+        raise ValueError("d_logits must have the logits' dtype and shape")
     _check(lib().relay_packed_router_backward(_pack13(
         ptr, stride, _dtype(logits, "logits"), t, e, tk[1], bool(normalize), _array(index, "index", _int32, tk),
         0 if d_gate is None else _array(d_gate, "d_gate", _float32, tk),

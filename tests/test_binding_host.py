@@ -51,3 +51,16 @@ def test_workspace_is_measured_in_bytes(relay_lib, call):
     """One that is too small is refused by the library with its size in bytes, whatever its type."""
     with pytest.raises(rv.RelayError, match="the workspace holds 24 bytes"):
         call(dev(3, dtype=torch.float64))
+
+
+def test_choices_have_to_be_a_matrix(relay_lib):
+    """One index per row, or none, is no matrix of choices: refused by name, like every other shape."""
+    flat = dev(6, dtype=torch.int32)
+    with pytest.raises(ValueError, match="teacher_index must be a matrix"):
+        rv.relay_linear_distill(head(), dev(6), flat, 1.0, dev(6), stream=0)
+    with pytest.raises(ValueError, match="index must be a matrix"):
+        rv.relay_router_forward(dev(6, 8), flat, dev(6), dev(8, dtype=torch.int32), dev(8), stream=0)
+    with pytest.raises(ValueError, match="index must be a matrix"):
+        rv.relay_router_backward(dev(6, 8), flat, dev(6, 8), stream=0)
+    with pytest.raises(ValueError, match="d_logits must have the logits' dtype and shape"):
+        rv.relay_router_backward(dev(6, 8), dev(6, 2, dtype=torch.int32), dev(6, 7), stream=0)
