@@ -491,6 +491,14 @@ relay_status_t run_multi(relay_coll_t coll, int num_groups, const size_t* counts
 }  // namespace
 
 relay_status_t report_error(relay_status_t st, const std::string& msg) { return fail(st, msg); }
+relay_status_t report_exception() noexcept {
+  g_last_error.clear();
+  try {
+    g_last_error = "out of host memory";
+  } catch (...) {
+  }
+  return RELAY_ERR_CUDA;
+}
 
 }  // namespace relay
 

@@ -258,18 +258,6 @@ relay_status_t run_head(const relay_head_t& h, HeadGeom g, int top, const int32_
   return RELAY_OK;
 }
 
-// C++ exceptions (an allocation that fails) end here, not in a C caller.
-template <class F>
-relay_status_t guarded(F f) {
-  try {
-    return f();
-  } catch (const std::exception& e) {
-    return report_error(RELAY_ERR_CUDA, std::string("relay_head: ") + e.what());
-  } catch (...) {
-    return RELAY_ERR_CUDA;
-  }
-}
-
 }  // namespace
 }  // namespace relay
 
@@ -305,11 +293,13 @@ relay_status_t relay_linear_xent(const relay_head_t* head, const int32_t* target
 relay_status_t relay_test_head_wait(const relay_head_t* head, const int32_t* targets, float* loss, void* workspace,
                                     int64_t workspace_bytes, int extra_bytes, cudaStream_t stream) {
   using namespace relay;
-  if (extra_bytes < 0 || extra_bytes > 65536) return bad("0 <= extra_bytes <= 65536");
-  head_test_extra(extra_bytes);
-  const relay_status_t st = relay_linear_xent(head, targets, nullptr, loss, workspace, workspace_bytes, stream);
-  head_test_extra(0);
-  return st;
+  return guarded([&]() -> relay_status_t {
+    if (extra_bytes < 0 || extra_bytes > 65536) return bad("0 <= extra_bytes <= 65536");
+    head_test_extra(extra_bytes);
+    const relay_status_t st = relay_linear_xent(head, targets, nullptr, loss, workspace, workspace_bytes, stream);
+    head_test_extra(0);
+    return st;
+  });
 }
 
 relay_status_t relay_linear_distill(const relay_head_t* head, const void* teacher_logits,

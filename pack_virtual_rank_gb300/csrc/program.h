@@ -194,6 +194,18 @@ int sm_count();
 // Record `msg` as this thread's last error and return `st` -- abi.cpp.
 relay_status_t report_error(relay_status_t st, const std::string& msg);
 
+// C++ exceptions (an allocation that fails) end here, not in a C caller. The text then has to fit the string it
+// replaces, or it is none.
+relay_status_t report_exception() noexcept;
+template <class F>
+relay_status_t guarded(F f) noexcept {
+  try {
+    return f();
+  } catch (...) {
+    return report_exception();
+  }
+}
+
 // Tile size in elements for a payload of esize bytes (shared by host tiling and the
 // kernel).
 constexpr int kThreads = 256;

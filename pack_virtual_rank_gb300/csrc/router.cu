@@ -527,16 +527,6 @@ relay_status_t check_overlaps(const Array* s, int n) {
 }
 bool off(const void* p, uintptr_t e) { return reinterpret_cast<uintptr_t>(p) % e != 0; }
 
-// C++ exceptions (an allocation that fails) end here, not in a C caller.
-template <class F>
-relay_status_t guarded(F f) {
-  try {
-    return f();
-  } catch (...) {
-    return RELAY_ERR_CUDA;
-  }
-}
-
 }  // namespace
 }  // namespace relay
 
