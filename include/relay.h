@@ -373,9 +373,23 @@ relay_status_t relay_allreduce_noalloc(void* const* send, void* const* recv, siz
  * logits z[n][v] = hidden[n] . weight[v]. The vocabulary is the concatenation of A shards;
  * shard a holds rows[a] rows of the weight (and of its gradient) in rank a's memory. The
  * hidden rows are the whole batch's, once (after an all-gather every rank holds the same).
- * The logits are never kept: the calls work on pieces of the vocabulary of at most
- * piece_bytes, and hold one value per logit of a piece. When the whole batch's logits are
- * one piece, the second logits product of the gradient is saved.
+ * The logits of the batch are not held all at once: the gradients work on pieces of the vocabulary of at
+ * most piece_bytes, and the workspace holds a value per logit of a piece (2 bytes for a bf16 head, 4 up to 128
+ * rows; 6 for an fp32 head). A batch whose logits all fit one piece keeps their exponentials there,
+ * and its logits are multiplied once; otherwise they are multiplied a second time, piece by piece. A loss
+ * without gradients holds none.
+ *
+ * The default of piece_bytes is a budget of memory, under 1% of the GPU's 284 GB. What it decides (ms a call with both
+ * gradients, bf16 unless said; kept / multiplied again in pieces of 1 GiB or less):
+ *   2048 x 4096 x 131072 (0.5 GiB of exponentials)   4.1 / 5.3
+ *   4096 x 2048 x 131072 (1 GiB)                     4.4 / 5.4
+ *   8192 x 4096 x 131072 (2 GiB, what the default just holds)   18.7 / 22.7
+ *   32768 x 2048 x 50000 (3.1 GiB)                   14.9 / 17.3
+ *   16384 x 4096 x 128256 (3.9 GiB)                  37.7 / 44.8
+ *   2048 x 2048 x 65536 fp32 (0.75 GiB)              5.6 / 7.1
+ * Keeping is worth 14 to 23% of a call at every size; the size of a piece that is not kept hardly
+ * matters (0.5 to 2 GiB: within 4%). A caller with the memory to spare passes a piece_bytes that its batch
+ * fits.
  */
 #define RELAY_HEAD_MAX_SHARDS 8
 #define RELAY_HEAD_MAX_TOP 128
@@ -413,7 +427,8 @@ int64_t relay_head_workspace_size(const relay_head_t* head, int top);
  *     L = sum_n row_weight[n] * loss[n] and overwrite d_hidden and d_weight.
  * Arithmetic: products of the inputs accumulate in fp32; maxima, sums and the loss are
  * fp32. For a bf16 head the gradient of each logit is rounded to bf16 once before its two
- * products, which accumulate in fp32 and are rounded to bf16 once. Every sum has a fixed
+ * products (up to 128 rows d_weight's takes it as two bf16 parts, 16 bits), which accumulate in fp32 and are
+ * rounded to bf16 once. Every sum has a fixed
  * order: equal calls give equal bits. A NaN or +infinite logit gives its
  * row NaN; one of -inf has probability 0 (a row of nothing else is NaN). An fp32 head multiplies
  * bf16 parts of its values; it gives such logits as a product of fp32 values does, where the hidden

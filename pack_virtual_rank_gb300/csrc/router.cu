@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) router_forward
   }
 }
 
-// Joins the blocks' partial sums: a block takes 32 experts, its warps stride over the partials.
+// Joins the blocks' partial sums: a block takes eight experts, its warps stride over the partials.
 constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps)
     router_join_kernel(const int32_t* part_count, const float* part_prob, int blocks, int experts,
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   __shared__ int32_t s_c[kJoinWarps][33];
   dep_launch();
   dep_wait();
-  // eight experts to a block: a warp reads four blocks' partials at a time
+  // a warp reads four blocks' partials at a time
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, e = blockIdx.x * 8 + lane % 8;
   float p = 0.0f;
   int32_t c = 0;
@@ -638,8 +638,11 @@ relay_status_t relay_router_backward(const void* logits, int64_t row_stride, rel
     const BackwardArgs a{logits, d_logits, row_stride, d_row_stride, tokens, experts, top, normalize,
                          load_bytes(logits, row_stride, E, experts), load_bytes(d_logits, d_row_stride, E, experts),
                          index, d_gate, d_prob};
-    // four blocks an SM: one round of resident warps, whose next rows load under the present ones (16: 2% slower)
-  const int blocks = (int)std::min<int64_t>((tokens + kRouterWarps - 1) / kRouterWarps, 4 * 152);
+    // Four blocks an SM, whose warps load their next rows under the present ones (16 an SM: 2% slower at 131072 x 256
+    // fp32). They are all resident where a thread has 64 registers at most: bf16 up to 256 experts, fp32 from 129 to
+    // 256. fp32 up to 128 experts has 71 (three blocks an SM), 257 to 512 experts 91 (fp32) and 78, more 141 and 128:
+    // there the last blocks start when the first end.
+    const int blocks = (int)std::min<int64_t>((tokens + kRouterWarps - 1) / kRouterWarps, 4 * 152);
     return done(by_width(experts, top, [&](auto n, auto l) {
       constexpr int N = decltype(n)::value, L = decltype(l)::value;
       return launch_chained(dtype == RELAY_BF16 ? router_backward_kernel<uint16_t, N, L> : router_backward_kernel<float, N, L>,
