@@ -621,7 +621,7 @@ __device__ __forceinline__ void finish_dhidden(const GemmArgs& p, const Item& t,
   }
 }
 
-// The staging buffer's 32 rows (128 bytes of each) to rows no tensor map can store: row by row, with
+// The staging buffer's 32 rows (128 bytes of each) to columns no tensor map can store: row by row, with
 // neighbouring lanes on neighbouring elements. Rare, and kept out of the unrolled path.
 template <class T>
 __device__ __noinline__ void copy_rows(uint32_t buf, T* to, int64_t ld, int rows, int columns) {
@@ -681,7 +681,9 @@ __device__ __forceinline__ void finish_dweight(const GemmArgs& p, const Item& t,
         out.put(j, __float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
       }
     }
-    if (p.out_map)
+    // a store through the map writes 16 bytes at a time, also where the row ends inside them: the last columns of
+    // such rows are stored by hand
+    if (p.out_map && (valid - c >= kCols || (valid - c) * (int)sizeof(T) % 16 == 0))
       out.close(&p.c[t.shard], d0 + c, r0);
     else
       copy_rows<T>(out.buf, static_cast<T*>(p.sh.dw[t.shard]) + r0 * p.sh.dw_ld + d0 + c, p.sh.dw_ld, min(32, rows - r0),
