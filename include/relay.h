@@ -448,7 +448,7 @@ relay_status_t relay_linear_xent(const relay_head_t* head, const int32_t* target
  *   teacher_logits[tokens][top], teacher_dtype RELAY_F32 or RELAY_BF16.
  *   q[n] = softmax over the row's entries of teacher_logits / temperature;
  *   loss[n] = temperature^2 * sum_k q log(q / p), p = softmax(z / temperature) over the
- *     whole vocabulary; temperature finite and > 0; 1 <= top <= RELAY_HEAD_MAX_TOP.
+ *     whole vocabulary; temperature finite and above 4.3e-39; 1 <= top <= RELAY_HEAD_MAX_TOP.
  * Everything else is as for relay_linear_xent.
  */
 relay_status_t relay_linear_distill(const relay_head_t* head, const void* teacher_logits,
