@@ -505,6 +505,37 @@ relay_status_t relay_router_backward(const void* logits, int64_t row_stride, rel
                                      cudaStream_t stream);
 
 /*
+ * ---- All gradients at once: their norm, and clipping ----
+ *
+ * A list of n tensors in device memory: grad[i] holds count[i] elements of dtype[i] (RELAY_F32 or RELAY_BF16), contiguous;
+ * count 0 is an empty tensor. The arrays are read during the call alone.
+ *
+ * relay_grad_norm -- norm[0] (fp32) = sqrt of the sum of all elements' squares, 0 for an empty list. The sum is
+ *   exact to fp32's rounding over the whole range of finite values, in a fixed order. A NaN or an infinity shows in norm. A tensor
+ *   given twice counts twice. Norms of several lists (ranks) join by the same call over their norms.
+ *   Two launches (one for up to 128 KiB) for 512 tensors, one more for each 512 beyond.
+ *   workspace: relay_grad_workspace_size bytes, any alignment.
+ *
+ * relay_grad_clip -- out[i] = grad[i] * min(1, max_norm / (norm[0] + 1e-6)), rounded once to the tensor's dtype. out NULL, or
+ *   with grad[i]'s own address: in place. norm[0] is read on the device, after what precedes the call on the stream. With
+ *   nothing to clip, or a norm that is NaN or infinite, the values stay as they are (the caller sees it
+ *   in norm). max_norm finite and above 0. No tensor that is written may overlap another. The list is walked from its end: right after
+ *   relay_grad_norm over the same list its last 100 MB are still in L2.
+ */
+#define RELAY_GRADS_MAX (1 << 20)
+typedef struct relay_grads {
+  int32_t n;
+  void* const* grad;
+  const size_t* count;
+  const int32_t* dtype;
+} relay_grads_t;
+int64_t relay_grad_workspace_size(const relay_grads_t* grads);
+relay_status_t relay_grad_norm(const relay_grads_t* grads, float* norm, void* workspace, int64_t workspace_bytes,
+                               cudaStream_t stream);
+relay_status_t relay_grad_clip(const relay_grads_t* grads, const relay_grads_t* out, const float* norm, float max_norm,
+                               cudaStream_t stream);
+
+/*
  * relay_device_status -- reads and clears the device's fault word. Passes whose sources
  * sit off the 16-byte grid stage each tile's source bytes in shared memory with a bulk
  * copy and wait for it on an mbarrier (the schedule's strided pack/unpack, item 7). That

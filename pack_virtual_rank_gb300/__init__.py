@@ -20,4 +20,5 @@ from ._binding import (  # noqa: F401
     relay_helper_contract_size, relay_copy,
     HEAD_MAX_SHARDS, HEAD_MAX_TOP, ROUTER_MAX_EXPERTS, ROUTER_MAX_TOP, RelayHead, make_head,
     relay_head_workspace_size, alloc_head_workspace, relay_linear_xent, relay_linear_distill,
-    alloc_router_workspace, relay_router_forward, relay_balance_loss, relay_router_backward)
+    alloc_router_workspace, relay_router_forward, relay_balance_loss, relay_router_backward,
+    RelayGrads, make_grads, alloc_grad_workspace, relay_grad_norm, relay_grad_clip)

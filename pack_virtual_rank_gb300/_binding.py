@@ -81,6 +81,12 @@ class RelayHead(ctypes.Structure):
                 ("d_weight_stride", ctypes.c_int64), ("piece_bytes", ctypes.c_int64)]
 
 
+class RelayGrads(ctypes.Structure):
+    """A list of tensors in device memory (relay_grads_t); build it with ``make_grads``."""
+    _fields_ = [("n", ctypes.c_int32), ("grad", ctypes.POINTER(ctypes.c_void_p)),
+                ("count", ctypes.POINTER(ctypes.c_size_t)), ("dtype", ctypes.POINTER(ctypes.c_int32))]
+
+
 _lib = None
 
 
@@ -165,6 +171,12 @@ def lib():
         fn = getattr(L, f"relay_packed_router_{name}")
         fn.argtypes = [ctypes.c_char_p]
         fn.restype = i32
+    L.relay_grad_workspace_size.argtypes = [P(RelayGrads)]
+    L.relay_grad_workspace_size.restype = i64
+    L.relay_grad_norm.argtypes = [P(RelayGrads), vp, vp, i64, vp]
+    L.relay_grad_norm.restype = i32
+    L.relay_grad_clip.argtypes = [P(RelayGrads), P(RelayGrads), vp, f32, vp]
+    L.relay_grad_clip.restype = i32
     if L.relay_abi_version() != 1:
         raise RuntimeError("librelay.so ABI version mismatch")
     _lib = L
@@ -708,3 +720,55 @@ def relay_router_backward(logits, index, d_logits, d_gate=None, d_prob=None, nor
         ptr, stride, _dtype(logits, "logits"), t, e, tk[1], bool(normalize), _array(index, "index", _int32, tk),
         0 if d_gate is None else _array(d_gate, "d_gate", _float32, tk),
         0 if d_prob is None else _array(d_prob, "d_prob", _float32, (e,)), d_ptr, d_stride, _handle(stream))))
+
+
+# ------------------------------------------------------------- all gradients at once --
+
+def make_grads(tensors: Sequence) -> RelayGrads:
+    """Describe a list of contiguous CUDA tensors (fp32 and bf16, any shapes) for relay_grad_norm and
+    relay_grad_clip. The tensors must outlive the list (it keeps references), and it can be used for any
+    number of calls."""
+    if _torch is None:
+        _bind_torch()
+    tensors = list(tensors)
+    for i, x in enumerate(tensors):
+        if not x.is_cuda or not x.is_contiguous():
+            raise ValueError(f"tensors[{i}] must be a contiguous CUDA tensor (device memory)")
+    n = len(tensors)
+    g = RelayGrads()
+    g.n = n
+    g._arrays = ((ctypes.c_void_p * max(n, 1))(*[x.data_ptr() for x in tensors]),
+                 (ctypes.c_size_t * max(n, 1))(*[x.numel() for x in tensors]),
+                 (ctypes.c_int32 * max(n, 1))(*[_dtype(x, f"tensors[{i}]") for i, x in enumerate(tensors)]))
+    g.grad = ctypes.cast(g._arrays[0], ctypes.POINTER(ctypes.c_void_p))
+    g.count = ctypes.cast(g._arrays[1], ctypes.POINTER(ctypes.c_size_t))
+    g.dtype = ctypes.cast(g._arrays[2], ctypes.POINTER(ctypes.c_int32))
+    g._tensors = tensors
+    return g
+
+
+def alloc_grad_workspace(grads: RelayGrads, device):
+    """Workspace of relay_grad_norm."""
+    import torch
+    n = int(lib().relay_grad_workspace_size(ctypes.byref(grads)))
+    if n < 0:
+        raise RelayError(ERR_INVALID_ARGUMENT, lib().relay_last_error().decode(errors="replace"))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def relay_grad_norm(grads: RelayGrads, norm, workspace=None, stream=None) -> None:
+    """norm[0] = the 2-norm over all tensors of the list (see relay.h)."""
+    if _torch is None:
+        _bind_torch()
+    if workspace is None:
+        workspace = _own_workspace(lambda: alloc_grad_workspace(grads, norm.device), stream)
+    _check(lib().relay_grad_norm(ctypes.byref(grads), _array(norm, "norm", _float32, (1,)), *_space(workspace),
+                                 _handle(stream)))
+
+
+def relay_grad_clip(grads: RelayGrads, norm, max_norm: float, out: Optional[RelayGrads] = None, stream=None) -> None:
+    """Scale every tensor by min(1, max_norm / (norm[0] + 1e-6)), in place or into the tensors of `out`."""
+    if _torch is None:
+        _bind_torch()
+    _check(lib().relay_grad_clip(ctypes.byref(grads), None if out is None else ctypes.byref(out),
+                                 _array(norm, "norm", _float32, (1,)), max_norm, _handle(stream)))

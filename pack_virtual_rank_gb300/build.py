@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librelay.so")
 
 SOURCES = ["plan.cpp", "program.cpp", "chain.cpp", "abi.cpp", "head.cpp", "passes.cu", "chain_kernel.cu",
-           "noalloc.cu", "head_rows.cu", "head_gemm.cu", "router.cu"]
+           "noalloc.cu", "head_rows.cu", "head_gemm.cu", "router.cu", "grads.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
