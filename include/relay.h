@@ -505,6 +505,70 @@ relay_status_t relay_router_backward(const void* logits, int64_t row_stride, rel
                                      cudaStream_t stream);
 
 /*
+ * ---- Products in 8-bit floating point, a scale for each block of 128 ----
+ *
+ * Values are e4m3 (1 byte, largest 448) times an fp32 scale. A row-scaled matrix [rows][depth] has a scale for each 128
+ * neighbours of a row, scale[blocks of depth][rows] (rows contiguous); a tile-scaled one [cols][depth] a scale for each 128 x
+ * 128, scale[blocks of cols][blocks of depth]. Blocks start at multiples of 128; the last of a dimension may be short.
+ * Row strides are multiples of 16 (bytes), addresses of 8-bit matrices on 16-byte boundaries.
+ *
+ * Groups (experts): offset[groups + 1] int32 in device memory, ascending; group g holds rows offset[g] .. offset[g + 1] - 1 of
+ * the rows, which stand sorted by group. A group may be empty; rows before offset[0] and from offset[groups] on are
+ * neither read nor written. Offsets outside [0, rows] or out of order give unspecified results, and no access out of range.
+ *
+ * relay_quantize_fp8 -- x[batch][rows][cols] (RELAY_F32 or RELAY_BF16; the batch's matrices one behind the other,
+ *   rows * x_stride elements apart) to 8 bits, as it lies (q, scale), transposed (qt, scale_t), or both. Scales are powers of two,
+ *   the least that bring a block's largest magnitude to 448 or below (2^-126 at least; 1 for a block of zeros), so a value is rounded
+ *   once, to nearest-even. A block that holds a NaN or an infinity has scale NaN.
+ *   tiles / tiles_t: 0 row-scaled, 1 tile-scaled (of qt: rows are x's columns). A batch other than 1 has tiles only.
+ *   With groups, qt's rows (length relay_fp8_depth) hold the groups one behind the other, each filled up with zeros to a
+ *   multiple of 128; q is by x's own rows and has no tiles.
+ *
+ * relay_matmul_fp8 -- by_depth 0: out[r][n] = sum_d a[r][d] b[g(r)][n][d]: a row-scaled [rows][depth], b tile-scaled
+ *     [groups][cols][depth] (its matrices one behind the other), g(r) the row's group; groups 0 and offset NULL: one b for all rows.
+ *   by_depth 1: out[g][r][n] = sum over group g's part of the depth of a[r][d] b[n][d]: a row-scaled [rows][depth], b
+ *     tile-scaled [cols][depth], depth laid out as qt's above (`depth` its whole length); out[groups][rows][cols], zeros for an
+ *     empty group; groups 0: one group of any depth. This is a weight's gradient: a = the output's gradient, b = the input, both transposed.
+ *   Products of a block of 128 accumulate in the tensor cores (fp32), the blocks in fp32 by fused multiply-adds with the
+ *   two scales' product (which has to be in fp32's range); out is rounded once to RELAY_F32 or RELAY_BF16. Equal calls give equal bits.
+ *   One launch. Scales may be any fp32 values. depth 0 gives zeros.
+ * An input's gradient is the product with the transposed weight: quantize the weight once as it lies and transposed (the tiles'
+ * scales and values are the same).
+ */
+#define RELAY_FP8_MAX_ROWS (1 << 22)
+#define RELAY_FP8_MAX_GROUPS 1024
+typedef struct relay_fp8_quantize {
+  const void* x;
+  int64_t x_stride;            /* elements, >= cols */
+  int64_t batch, rows, cols;   /* batch 1 .. RELAY_FP8_MAX_GROUPS; rows, cols <= RELAY_FP8_MAX_ROWS; cols >= 1 */
+  void* q;                     /* NULL: not wanted */
+  int64_t q_stride;            /* bytes */
+  float* scale;
+  void* qt;                    /* NULL: not wanted */
+  int64_t qt_stride;
+  float* scale_t;
+  const int32_t* offset;       /* NULL: no groups */
+  int32_t groups, dtype, tiles, tiles_t;
+} relay_fp8_quantize_t;
+typedef struct relay_fp8_matmul {
+  const void* a;
+  int64_t a_stride;            /* bytes */
+  const float* a_scale;        /* [blocks of depth][rows] */
+  const void* b;
+  int64_t b_stride;
+  const float* b_scale;
+  void* out;
+  int64_t out_stride;          /* elements */
+  int64_t rows, cols, depth;
+  const int32_t* offset;       /* NULL: no groups */
+  int32_t groups, out_dtype, by_depth, reserved;
+} relay_fp8_matmul_t;
+/* Length of the transposed rows: rows, or with groups 128 * (rows / 128 + min(groups, rows)): room for any offsets. */
+int64_t relay_fp8_depth(int64_t rows, int groups);
+relay_status_t relay_quantize_fp8(const relay_fp8_quantize_t* what, cudaStream_t stream);
+relay_status_t relay_matmul_fp8(const relay_fp8_matmul_t* what, cudaStream_t stream);
+
+/*
  * ---- All gradients at once: their norm, and clipping ----
  *
  * A list of n tensors in device memory: grad[i] holds count[i] elements of dtype[i] (RELAY_F32 or RELAY_BF16), contiguous;
@@ -566,6 +630,9 @@ relay_status_t relay_test_staged_wait(void* dst, const void* src, size_t count,
  */
 relay_status_t relay_test_head_wait(const relay_head_t* head, const int32_t* targets, float* loss, void* workspace,
                                     int64_t workspace_bytes, int extra_bytes, cudaStream_t stream);
+
+/* relay_test_fp8_wait -- the same for relay_matmul_fp8. */
+relay_status_t relay_test_fp8_wait(const relay_fp8_matmul_t* what, int extra_bytes, cudaStream_t stream);
 
 /* Human-readable text of the last error this thread's calls produced. */
 const char* relay_last_error(void);

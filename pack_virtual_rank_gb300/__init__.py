@@ -21,4 +21,5 @@ from ._binding import (  # noqa: F401
     HEAD_MAX_SHARDS, HEAD_MAX_TOP, ROUTER_MAX_EXPERTS, ROUTER_MAX_TOP, RelayHead, make_head,
     relay_head_workspace_size, alloc_head_workspace, relay_linear_xent, relay_linear_distill,
     alloc_router_workspace, relay_router_forward, relay_balance_loss, relay_router_backward,
-    RelayGrads, make_grads, alloc_grad_workspace, relay_grad_norm, relay_grad_clip)
+    RelayGrads, make_grads, alloc_grad_workspace, relay_grad_norm, relay_grad_clip,
+    FP8_BLOCK, FP8_MAX_ROWS, FP8_MAX_GROUPS, fp8_depth, alloc_fp8, relay_quantize_fp8, relay_matmul_fp8)

@@ -68,6 +68,9 @@ HEAD_MAX_SHARDS = 8
 HEAD_MAX_TOP = 128
 ROUTER_MAX_EXPERTS = 1024
 ROUTER_MAX_TOP = 32
+FP8_BLOCK = 128            # values that share a scale
+FP8_MAX_ROWS = 1 << 22
+FP8_MAX_GROUPS = 1024
 
 
 class RelayHead(ctypes.Structure):
@@ -177,6 +180,14 @@ def lib():
     L.relay_grad_norm.restype = i32
     L.relay_grad_clip.argtypes = [P(RelayGrads), P(RelayGrads), vp, f32, vp]
     L.relay_grad_clip.restype = i32
+    L.relay_fp8_depth.argtypes = [i64, i32]
+    L.relay_fp8_depth.restype = i64
+    for name in ("relay_quantize_fp8", "relay_matmul_fp8"):
+        fn = getattr(L, name)
+        fn.argtypes = [ctypes.c_char_p, vp]
+        fn.restype = i32
+    L.relay_test_fp8_wait.argtypes = [ctypes.c_char_p, i32, vp]
+    L.relay_test_fp8_wait.restype = i32
     if L.relay_abi_version() != 1:
         raise RuntimeError("librelay.so ABI version mismatch")
     _lib = L
@@ -720,6 +731,125 @@ def relay_router_backward(logits, index, d_logits, d_gate=None, d_prob=None, nor
         ptr, stride, _dtype(logits, "logits"), t, e, tk[1], bool(normalize), _array(index, "index", _int32, tk),
         0 if d_gate is None else _array(d_gate, "d_gate", _float32, tk),
         0 if d_prob is None else _array(d_prob, "d_prob", _float32, (e,)), d_ptr, d_stride, _handle(stream))))
+
+
+# --------------------------------------------------------------- products in 8 bits --
+
+def fp8_depth(rows: int, groups: int = 0) -> int:
+    """Length of the transposed rows of relay_quantize_fp8: rows, or with groups room for each of them to start a
+    block of 128."""
+    n = int(lib().relay_fp8_depth(rows, groups))
+    if n < 0:
+        raise RelayError(ERR_INVALID_ARGUMENT, lib().relay_last_error().decode(errors="replace"))
+    return n
+
+
+def alloc_fp8(rows: int, cols: int, device, tiles: bool = False, batch: Optional[int] = None):
+    """An 8-bit matrix [rows, cols] (or a batch of them) whose row stride the products accept, and its scales:
+    [blocks of cols, rows], or with tiles [blocks of rows, blocks of cols] (with a batch in front)."""
+    import torch
+    lead = () if batch is None else (batch,)
+    if batch is not None and not tiles:
+        raise ValueError("a batch of matrices has tiles")
+    kb = -(-cols // FP8_BLOCK)
+    q = torch.empty(lead + (rows, max(-(-cols // 16) * 16, 16)), dtype=torch.float8_e4m3fn, device=device)[..., :cols]
+    shape = lead + (-(-rows // FP8_BLOCK), kb) if tiles else (kb, rows)
+    return q, torch.empty(shape, dtype=torch.float32, device=device)
+
+
+def _batched(x, name: str):
+    """Address, batch, rows, columns and row stride of a CUDA matrix, or of matrices one behind the other."""
+    if x.dim() == 2:
+        ptr, r, c, ld = _rows(x, name)
+        return ptr, 1, r, c, ld
+    if x.dim() != 3 or not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA matrix, or a batch of them (device memory)")
+    n, r, c = x.shape
+    sn, sr, sc = x.stride()
+    ld = sr if r > 1 else (max(sn, c) if n > 1 else max(sr, c))
+    if (c > 1 and sc != 1) or (n > 1 and sn != r * ld):
+        raise ValueError(f"{name} must have contiguous rows, its matrices one behind the other")
+    return x.data_ptr(), n, r, c, ld
+
+
+def _fp8(x, name: str):
+    if x.dtype is not _torch.float8_e4m3fn:
+        raise ValueError(f"{name} must be float8_e4m3fn, got {x.dtype}")
+    return _batched(x, name)
+
+
+def _scales(x, name: str, shape) -> int:
+    """A leading dimension of 1 may be there or not."""
+    if x.dim() == len(shape) + 1 and x.shape[0] == 1:
+        x = x[0]
+    elif len(shape) == x.dim() + 1 and shape[0] == 1:
+        shape = shape[1:]
+    return _array(x, name, _float32, shape)
+
+
+def _offset(offset):
+    if offset is None:
+        return 0, 0
+    if offset.dim() != 1 or offset.shape[0] < 2:
+        raise ValueError(f"offset must be int32 [groups + 1], got {tuple(offset.shape)}")
+    return _array(offset, "offset", _int32, offset.shape), offset.shape[0] - 1
+
+
+_pack_fp8 = struct.Struct("12q4i").pack
+
+
+def relay_quantize_fp8(x, q=None, scale=None, qt=None, scale_t=None, tiles: bool = False, tiles_t: bool = False,
+                       offset=None, stream=None) -> None:
+    """x [rows, cols] (or a batch of matrices) to 8 bits with a power of two for each block of 128: as it lies (q,
+    scale), transposed (qt, scale_t), or both; allocate them with alloc_fp8. offset (int32, device memory): the rows
+    belong to groups, each of which starts a block of qt's rows of length fp8_depth(rows, groups) (see relay.h)."""
+    if _torch is None:
+        _bind_torch()
+    ptr, n, r, c, ld = _batched(x, "x")
+    off, groups = _offset(offset)
+    rb, cb = -(-r // FP8_BLOCK), -(-c // FP8_BLOCK)
+    if q is None and qt is None:
+        raise ValueError("neither q nor qt is given")
+    q_ptr = s_ptr = q_ld = qt_ptr = st_ptr = qt_ld = 0
+    if q is not None:
+        q_ptr, q_n, q_r, q_c, q_ld = _fp8(q, "q")
+        if (q_n, q_r, q_c) != (n, r, c) or scale is None:
+            raise ValueError(f"q must have x's shape, and come with scale: got {tuple(q.shape)}")
+        s_ptr = _scales(scale, "scale", (n, rb, cb) if tiles else (cb, r))
+    if qt is not None:
+        qt_ptr, q_n, q_r, q_c, qt_ld = _fp8(qt, "qt")
+        depth = r if groups == 0 else fp8_depth(r, groups)
+        if (q_n, q_r, q_c) != (n, c, depth) or scale_t is None:
+            raise ValueError(f"qt must be {(n, c, depth)}, and come with scale_t: got {tuple(qt.shape)}")
+        db = -(-depth // FP8_BLOCK)
+        st_ptr = _scales(scale_t, "scale_t", (n, cb, db) if tiles_t else (db, c))
+    _check(lib().relay_quantize_fp8(_pack_fp8(ptr, ld, n, r, c, q_ptr, q_ld, s_ptr, qt_ptr, qt_ld, st_ptr, off, groups,
+                                              _dtype(x, "x"), bool(tiles), bool(tiles_t)), _handle(stream)))
+
+
+def _matmul_fp8_words(a, a_scale, b, b_scale, out, offset, by_depth) -> bytes:
+    if _torch is None:
+        _bind_torch()
+    a_ptr, a_n, r, d, a_ld = _fp8(a, "a")
+    b_ptr, b_n, n, b_d, b_ld = _fp8(b, "b")
+    off, groups = _offset(offset)
+    kb, nb, many = -(-d // FP8_BLOCK), -(-n // FP8_BLOCK), max(groups, 1)
+    if a_n != 1 or b_d != d or b_n != (1 if by_depth else many):
+        raise ValueError(f"a must be [rows, depth] and b [{'' if by_depth or not groups else 'groups, '}cols, depth]: "
+                         f"got {tuple(a.shape)} and {tuple(b.shape)} for {groups} groups")
+    out_ptr, o_n, o_r, o_c, o_ld = _batched(out, "out")
+    if (o_n, o_r, o_c) != (many if by_depth else 1, r, n):
+        raise ValueError(f"out must be {(many, r, n) if by_depth else (r, n)}, got {tuple(out.shape)}")
+    return _pack_fp8(a_ptr, a_ld, _scales(a_scale, "a_scale", (kb, r)), b_ptr, b_ld,
+                     _scales(b_scale, "b_scale", (b_n, nb, kb)), out_ptr, o_ld, r, n, d, off, groups, _dtype(out, "out"),
+                     bool(by_depth), 0)
+
+
+def relay_matmul_fp8(a, a_scale, b, b_scale, out, offset=None, by_depth: bool = False, stream=None) -> None:
+    """out[r, n] = sum_d a[r, d] b[n, d] of 8-bit matrices: a row-scaled, b tile-scaled (see relay_quantize_fp8). With
+    offset, rows belong to groups and meet their group's b [groups, cols, depth]; with by_depth the groups are
+    stretches of the depth, and out is [groups, rows, cols] (see relay.h)."""
+    _check(lib().relay_matmul_fp8(_matmul_fp8_words(a, a_scale, b, b_scale, out, offset, by_depth), _handle(stream)))
 
 
 # ------------------------------------------------------------- all gradients at once --

@@ -10,6 +10,7 @@
 #include <string>
 #include <vector>
 
+#include "fp8.h"
 #include "head.h"
 #include "program.h"
 
@@ -793,6 +794,10 @@ relay_status_t relay_device_status(void) {
     return fail(RELAY_ERR_CUDA,
                 "a bounded wait in a product of relay_linear_xent or relay_linear_distill gave up; "
                 "the call's outputs are unspecified");
+  const cudaError_t fe = fp8_read_fault(&fault);
+  if (fe != cudaSuccess) return fail(RELAY_ERR_CUDA, cudaGetErrorString(fe));
+  if (fault)
+    return fail(RELAY_ERR_CUDA, "a bounded wait in relay_matmul_fp8 gave up; the call's output is unspecified");
   return RELAY_OK;
 }
 

@@ -32,6 +32,7 @@
 #include "device.cuh"
 #include "head.h"
 #include "launch.cuh"
+#include "maps.h"
 #include "program.h"
 #include "tc.cuh"
 
@@ -801,21 +802,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) head_product_kernel(const __g
 // ------------------------------------------------------------------ host side --
 
 thread_local int t_extra = 0;
-
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return static_cast<EncodeFn>(nullptr);
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  return fn;
-}
 
 // A matrix [rows][cols], row stride ld elements, read or written in boxes: bf16 by 64 columns or fp32 by 32
 // (128 bytes, 128-byte swizzle), or bf16 by 32 (64 bytes, 64-byte swizzle).
