@@ -31,8 +31,21 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive_pair(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// PAIR: what ordinary stores of the other CTA wrote before its arrival is seen, too. Where a barrier stands for loads by tensor
+// maps, products or this CTA's own stores, that is not needed.
+template <bool PAIR = true>
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
+  if constexpr (!PAIR) {
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  }
   asm volatile(
       "{\n.reg .pred p;\n"
       "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
@@ -46,14 +59,17 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // Every wait of a product ends: when its barrier completes, when another warp of the CTA gave
 // up, or after kWaitNs. The slowest wait of a healthy run is one tile's products.
 constexpr uint64_t kWaitNs = 500000000ull;
+template <bool PAIR = true>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  if (bar_try(bar, parity)) return true;
-  const uint64_t start = global_ns();
+  if (bar_try<PAIR>(bar, parity)) return true;
+  uint64_t start = 0;  // the clock is read once a wait has become a long one
   for (uint32_t i = 1;; ++i) {
-    if (bar_try(bar, parity)) return true;
+    if (bar_try<PAIR>(bar, parity)) return true;
     if (i % 64 == 0) {
       if (*gave_up) return false;
-      if (global_ns() - start > kWaitNs) {
+      const uint64_t now = global_ns();
+      if (start == 0) start = now;
+      if (now - start > kWaitNs) {
         *gave_up = 1;
         return false;
       }
