@@ -505,6 +505,51 @@ relay_status_t relay_router_backward(const void* logits, int64_t row_stride, rel
                                      cudaStream_t stream);
 
 /*
+ * ---- Expert router with scores, a bias for balance and groups of experts ----
+ *
+ * relay_grouped_router_forward: rows as in relay_router_forward, chosen otherwise.
+ *   score s: softmax over the row's logits, or 1 / (1 + exp(-x)) of each.
+ *   choice value c = s + bias (bias[experts] fp32, NULL: 0); an expert whose logit or bias is -inf cannot be chosen.
+ *   With kept < groups: groups of experts / groups neighbours; a group's value is the sum of its group_sum (1 or 2) largest
+ *     choice values (of those that can be chosen); the `kept` largest groups stay, ties to the lower.
+ *   index[tokens][top]: the top largest choice values of the groups that stay, largest first, ties to the lower expert;
+ *     -1 where fewer can be chosen. Both choices are by exact values: what fp32 cannot tell apart is compared in 64 bits.
+ *   gate[tokens][top] = scale * s, or with normalize != 0 scale * s / the sum of the row's chosen s (0 where that is 0); 0 at -1. The
+ *     bias is in the choice alone.
+ *   counts[experts] int32: rows that chose the expert. prob_sum[experts] fp32: the sum over rows of s divided by the row's sum of
+ *     s. Both as relay_router_forward's: summed over ranks by relay_allreduce, taken by relay_balance_loss (counts also by
+ *     relay_router_bias_update). A row that mask leaves out, or of which no expert can be chosen, has index -1 and gate 0 and is in
+ *     neither.
+ *   A NaN logit makes its row's gates and prob_sum NaN; index stays in range and distinct, with a NaN below what else can be chosen.
+ *   Scores are fp32: one below 2^-126 is 0. bias values are finite or -inf.
+ *   1 <= groups <= RELAY_ROUTER_MAX_GROUPS, a divisor of experts; with kept < groups at most RELAY_ROUTER_MAX_GROUPED experts;
+ *   top <= RELAY_ROUTER_MAX_TOP and the experts of the kept groups. Two launches at most. workspace: relay_router_workspace_size bytes.
+ *
+ * relay_grouped_router_backward: d_logits from d_gate (NULL: 0) and d_prob (NULL: 0, the derivative by one token's share of each
+ *   expert: relay_balance_loss's). index is the forward's; entries of -1 have no gradient, rows whose first is -1 are 0. Of `how` it
+ *   takes score, experts, top, normalize and scale. The choice and the bias have no gradient.
+ *
+ * relay_router_bias_update: bias_out[e] = bias[e] + rate where counts[e] is below the mean of counts, - rate where it is above,
+ *   bias[e] where it is the mean. In place with bias_out = bias.
+ */
+#define RELAY_ROUTER_MAX_GROUPS 32
+#define RELAY_ROUTER_MAX_GROUPED 512
+enum { RELAY_SCORE_SOFTMAX = 0, RELAY_SCORE_SIGMOID = 1 };
+typedef struct relay_routing {
+  int32_t score, experts, groups, kept, top, group_sum, normalize;
+  float scale;
+} relay_routing_t;
+relay_status_t relay_grouped_router_forward(const relay_routing_t* how, const void* logits, int64_t row_stride,
+                                            relay_dtype_t dtype, int64_t tokens, const float* bias, const uint8_t* mask,
+                                            int32_t* index, float* gate, int32_t* counts, float* prob_sum, void* workspace,
+                                            int64_t workspace_bytes, cudaStream_t stream);
+relay_status_t relay_grouped_router_backward(const relay_routing_t* how, const void* logits, int64_t row_stride,
+                                             relay_dtype_t dtype, int64_t tokens, const int32_t* index, const float* d_gate,
+                                             const float* d_prob, void* d_logits, int64_t d_row_stride, cudaStream_t stream);
+relay_status_t relay_router_bias_update(const int32_t* counts, const float* bias, int experts, float rate, float* bias_out,
+                                        cudaStream_t stream);
+
+/*
  * ---- Products in 8-bit floating point, a scale for each block of 128 ----
  *
  * Values are e4m3 (1 byte, largest 448) times an fp32 scale. A row-scaled matrix [rows][depth] has a scale for each 128

@@ -22,4 +22,5 @@ from ._binding import (  # noqa: F401
     relay_head_workspace_size, alloc_head_workspace, relay_linear_xent, relay_linear_distill,
     alloc_router_workspace, relay_router_forward, relay_balance_loss, relay_router_backward,
     RelayGrads, make_grads, alloc_grad_workspace, relay_grad_norm, relay_grad_clip,
-    FP8_BLOCK, FP8_MAX_ROWS, FP8_MAX_GROUPS, fp8_depth, alloc_fp8, relay_quantize_fp8, relay_matmul_fp8)
+    ROUTER_MAX_GROUPS, ROUTER_MAX_GROUPED, relay_grouped_router_forward, relay_grouped_router_backward,
+    relay_router_bias_update, FP8_BLOCK, FP8_MAX_ROWS, FP8_MAX_GROUPS, fp8_depth, alloc_fp8, relay_quantize_fp8, relay_matmul_fp8)

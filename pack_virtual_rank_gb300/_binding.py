@@ -68,6 +68,9 @@ HEAD_MAX_SHARDS = 8
 HEAD_MAX_TOP = 128
 ROUTER_MAX_EXPERTS = 1024
 ROUTER_MAX_TOP = 32
+ROUTER_MAX_GROUPS = 32
+ROUTER_MAX_GROUPED = 512
+SCORES = {"softmax": 0, "sigmoid": 1}
 FP8_BLOCK = 128            # values that share a scale
 FP8_MAX_ROWS = 1 << 22
 FP8_MAX_GROUPS = 1024
@@ -180,6 +183,12 @@ def lib():
     L.relay_grad_norm.restype = i32
     L.relay_grad_clip.argtypes = [P(RelayGrads), P(RelayGrads), vp, f32, vp]
     L.relay_grad_clip.restype = i32
+    for name in ("forward", "backward"):
+        fn = getattr(L, f"relay_packed_grouped_{name}")
+        fn.argtypes = [ctypes.c_char_p, ctypes.c_char_p]
+        fn.restype = i32
+    L.relay_router_bias_update.argtypes = [vp, vp, i32, f32, vp, vp]
+    L.relay_router_bias_update.restype = i32
     L.relay_fp8_depth.argtypes = [i64, i32]
     L.relay_fp8_depth.restype = i64
     for name in ("relay_quantize_fp8", "relay_matmul_fp8"):
@@ -731,6 +740,66 @@ def relay_router_backward(logits, index, d_logits, d_gate=None, d_prob=None, nor
         ptr, stride, _dtype(logits, "logits"), t, e, tk[1], bool(normalize), _array(index, "index", _int32, tk),
         0 if d_gate is None else _array(d_gate, "d_gate", _float32, tk),
         0 if d_prob is None else _array(d_prob, "d_prob", _float32, (e,)), d_ptr, d_stride, _handle(stream))))
+
+
+# ------------------------------------------------- router with scores, bias and groups --
+
+_pack_routing = struct.Struct("7if").pack
+_pack10 = struct.Struct("10q").pack
+
+
+def _routing(score, experts, groups, kept, top, group_sum, normalize, scale) -> bytes:
+    if score not in SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return _pack_routing(SCORES[score], experts, groups, groups if kept is None else kept, top, group_sum, bool(normalize), scale)
+
+
+def relay_grouped_router_forward(logits, index, gate, counts, prob_sum, bias=None, mask=None, groups: int = 1,
+                                 kept: Optional[int] = None, group_sum: int = 2, score: str = "sigmoid",
+                                 normalize: bool = True, scale: float = 1.0, workspace=None, stream=None) -> None:
+    """Top-k experts of each row of logits [tokens, experts] (k = index.shape[1]) by score + bias among the `kept` (None:
+    all) best of `groups` groups, their gates (scores alone, renormalized and scaled), the per-expert counts and
+    the sums of the scores' shares (see relay.h). workspace: alloc_router_workspace. mask: bool or uint8 per row."""
+    if _torch is None:
+        _bind_torch()
+    ptr, t, e, stride = _rows(logits, "logits")
+    tk = (t, _columns(index, "index"))
+    how = _routing(score, e, groups, kept, tk[1], group_sum, normalize, scale)
+    # `mask` stays the tensor: when nothing but the call holds it, the workspace below would take its memory
+    mask_ptr = 0 if mask is None else _array(mask, "mask", _torch.bool if mask.dtype is _torch.bool else _torch.uint8, (t,))
+    if workspace is None:
+        workspace = _own_workspace(lambda: alloc_router_workspace(t, e, logits.device), stream)
+    _check(lib().relay_packed_grouped_forward(how, _pack13(
+        ptr, stride, _dtype(logits, "logits"), t, 0 if bias is None else _array(bias, "bias", _float32, (e,)), mask_ptr,
+        _array(index, "index", _int32, tk), _array(gate, "gate", _float32, tk), _array(counts, "counts", _int32, (e,)),
+        _array(prob_sum, "prob_sum", _float32, (e,)), *_space(workspace), _handle(stream))))
+
+
+def relay_grouped_router_backward(logits, index, d_logits, d_gate=None, d_prob=None, score: str = "sigmoid",
+                                  normalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """Gradient of the logits of relay_grouped_router_forward from the gates' and the shares' (see relay.h)."""
+    if _torch is None:
+        _bind_torch()
+    ptr, t, e, stride = _rows(logits, "logits")
+    d_ptr, d_t, d_e, d_stride = _rows(d_logits, "d_logits")
+    tk = (t, _columns(index, "index"))
+    if d_logits.dtype is not logits.dtype or d_t != t or d_e != e:
+        raise ValueError("d_logits must have the logits' dtype and shape")
+    _check(lib().relay_packed_grouped_backward(_routing(score, e, 1, 1, tk[1], 1, normalize, scale), _pack10(
+        ptr, stride, _dtype(logits, "logits"), t, _array(index, "index", _int32, tk),
+        0 if d_gate is None else _array(d_gate, "d_gate", _float32, tk),
+        0 if d_prob is None else _array(d_prob, "d_prob", _float32, (e,)), d_ptr, d_stride, _handle(stream))))
+
+
+def relay_router_bias_update(counts, bias, rate: float, out=None, stream=None) -> None:
+    """Raise the bias of experts chosen less often than the mean by `rate`, lower that of those chosen more often; in
+    place, or into `out`."""
+    if _torch is None:
+        _bind_torch()
+    e = counts.shape
+    b = _array(bias, "bias", _float32, e)
+    _check(lib().relay_router_bias_update(_array(counts, "counts", _int32, e), b, counts.numel(), rate,
+                                          b if out is None else _array(out, "out", _float32, e), _handle(stream)))
 
 
 # --------------------------------------------------------------- products in 8 bits --

@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librelay.so")
 
 SOURCES = ["plan.cpp", "program.cpp", "chain.cpp", "abi.cpp", "head.cpp", "passes.cu", "chain_kernel.cu",
-           "noalloc.cu", "head_rows.cu", "head_gemm.cu", "router.cu", "grads.cu", "fp8_quantize.cu", "fp8_matmul.cu"]
+           "noalloc.cu", "head_rows.cu", "head_gemm.cu", "router.cu", "grouped_router.cu", "grads.cu", "fp8_quantize.cu", "fp8_matmul.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -50,6 +50,7 @@ def _stale() -> bool:
                                                        os.path.join(CSRC, "launch.cuh"),
                                                        os.path.join(CSRC, "spans.h"),
                                                        os.path.join(CSRC, "maps.h"),
+                                                       os.path.join(CSRC, "router.cuh"),
                                                        os.path.join(CSRC, "fp8.h"),
                                                        os.path.join(INCLUDE, "relay.h"), __file__]
     return any(os.path.getmtime(d) > t for d in deps)
