@@ -5,9 +5,10 @@
 // A power of two makes the division exact: q is rounded once, and the same block quantized along the other dimension
 // has the same values. A block holds 128 neighbours of a row, or 128 x 128.
 //
-// Bound by memory: a CTA reads 128 x 128 values once, keeps them in registers (64 a thread: eight rows of eight columns), and
-// writes what is asked for of the tile, its transpose, and both's scales. The transpose goes through shared memory as
-// 8-byte pieces of eight rows, placed so that neither side meets a bank twice.
+// Bound by memory: a CTA reads 128 x 128 values once, keeps them in registers as they lie (64 a thread: eight rows of eight
+// columns; bf16 in 32 registers, so that four CTAs an SM keep enough reads on their way), and writes what is asked for of the
+// tile, its transpose, and both's scales. The transpose goes through shared memory as 8-byte pieces of eight rows, placed
+// so that neither side meets a bank twice.
 #include <algorithm>
 #include <string>
 
@@ -72,20 +73,40 @@ __device__ __forceinline__ void store_bytes(uint8_t* to, uint2 b, int n) {
   for (int i = 0; i < n; ++i) to[i] = (uint8_t)(all >> (8 * i));
 }
 
+// Eight neighbours of a row as they lie. Magnitudes compare as integers, two bf16 at once.
 template <class T>
-struct Payload;
+struct Eight;
 template <>
-struct Payload<float> {
+struct Eight<float> {
   using P = TF32;
+  static constexpr int kWords = 8;
+  static __device__ __forceinline__ uint32_t magnitude(uint32_t w) { return w & 0x7fffffffu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t fold(uint32_t a) { return a; }  // as fp32 bits
+  static __device__ __forceinline__ uint32_t column(const uint32_t (&m)[8], int k) { return m[k]; }
+  static __device__ __forceinline__ float value(const uint32_t (&w)[8], int k) { return __uint_as_float(w[k]); }
+  static __device__ __forceinline__ void set(uint32_t (&w)[8], int k, float v) { w[k] = __float_as_uint(v); }
 };
 template <>
-struct Payload<uint16_t> {
+struct Eight<uint16_t> {
   using P = TBF16;
+  static constexpr int kWords = 4;
+  static __device__ __forceinline__ uint32_t magnitude(uint32_t w) { return w & 0x7fff7fffu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+  static __device__ __forceinline__ uint32_t fold(uint32_t a) { return max(a << 16, a & 0xffff0000u); }
+  static __device__ __forceinline__ uint32_t column(const uint32_t (&m)[4], int k) { return k % 2 ? m[k / 2] & 0xffff0000u : m[k / 2] << 16; }
+  static __device__ __forceinline__ float value(const uint32_t (&w)[4], int k) { return __uint_as_float(column(w, k)); }
+  static __device__ __forceinline__ void set(uint32_t (&w)[4], int k, float v) {
+    const uint32_t b = __float_as_uint(v) >> 16;  // v is a bf16 value
+    w[k / 2] = k % 2 ? (w[k / 2] & 0xffffu) | b << 16 : (w[k / 2] & 0xffff0000u) | b;
+  }
 };
 
 template <class T>
-__global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const QuantArgs a) {
-  using P = typename Payload<T>::P;
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) fp8_quantize_kernel(const QuantArgs a) {
+  using V = Eight<T>;
+  using P = typename V::P;
+  constexpr int W = V::kWords;
   __shared__ __align__(16) uint8_t s_t[kBlock * kBlock];
   __shared__ uint32_t s_col[kQuantThreads / 32][kBlock];
   __shared__ uint32_t s_top[kQuantThreads / 32];
@@ -122,37 +143,46 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const Quant
     r_end = min(hi, r0 + kBlock);
   }
   const T* x = static_cast<const T*>(a.x) + (int64_t)batch * a.rows * a.ld;
-  float v[8][8];
+  uint32_t v[8][W];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + row8 + i, c = c0 + col8;
     const T* from = x + (int64_t)r * a.ld + c;
     if (r < r_end && a.vectors && c + 8 <= a.cols) {
 #pragma unroll
-      for (int k = 0; k < 8; k += P::kLanes) P::unpack(ld_stream_v4(from + k), &v[i][k]);
+      for (int k = 0; k < W; k += 4) {
+        const uint4 u = ld_stream_v4(reinterpret_cast<const uint32_t*>(from) + k);
+        v[i][k] = u.x; v[i][k + 1] = u.y; v[i][k + 2] = u.z; v[i][k + 3] = u.w;
+      }
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] = r < r_end && c + k < a.cols ? P::template load1<false>(from + k) : 0.0f;
+      for (int k = 0; k < W; ++k) v[i][k] = 0;
+      if (r < r_end) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + k < a.cols) V::set(v[i], k, P::template load1<false>(from + k));
+      }
     }
   }
-  auto bits = [](float f) { return __float_as_uint(f) & 0x7fffffffu; };
   const bool need_cols = a.qt != nullptr && !a.tiles_t, need_tile = (a.q != nullptr && a.tiles) || (a.qt != nullptr && a.tiles_t);
-  uint32_t row_top[8], all = 0;
+  uint32_t all = 0;
+  if (need_cols || need_tile) {
+    uint32_t m[W];  // of the thread's columns
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    row_top[i] = 0;
+    for (int j = 0; j < W; ++j) {
+      m[j] = V::magnitude(v[0][j]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) row_top[i] = max(row_top[i], bits(v[i][k]));
-    all = max(all, row_top[i]);
-  }
-  if (need_cols) {
+      for (int i = 1; i < 8; ++i) m[j] = V::larger(m[j], V::magnitude(v[i][j]));
+      all = j == 0 ? m[j] : V::larger(all, m[j]);
+    }
+    all = V::fold(all);
+    if (need_cols) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      uint32_t t = 0;
+      for (int j = 0; j < W; ++j) m[j] = V::larger(m[j], __shfl_xor_sync(~0u, m[j], 16));
+      if (lane < 16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t = max(t, bits(v[i][k]));
-      t = max(t, __shfl_xor_sync(~0u, t, 16));
-      if (lane < 16) s_col[warp][col8 + k] = t;
+        for (int k = 0; k < 8; ++k) s_col[warp][col8 + k] = V::column(m, k);
+      }
     }
   }
   if (need_tile) {
@@ -176,7 +206,10 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const Quant
       const int r = r0 + row8 + i;
       float inverse = tile_inverse;
       if (!a.tiles) {
-        uint32_t t = row_top[i];
+        uint32_t t = V::magnitude(v[i][0]);
+#pragma unroll
+        for (int j = 1; j < W; ++j) t = V::larger(t, V::magnitude(v[i][j]));
+        t = V::fold(t);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(~0u, t, o));
         const float s = scale_of(t, &inverse);
@@ -184,7 +217,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const Quant
       }
       float y[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = v[i][k] * inverse;
+      for (int k = 0; k < 8; ++k) y[k] = V::value(v[i], k) * inverse;
       if (r < r_end) store_bytes(a.q + ((int64_t)batch * a.rows + r) * a.q_ld + c0 + col8, e4m3x8(y), a.cols - c0 - col8);
     }
   }
@@ -201,7 +234,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const Quant
     }
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = v[i][k] * inverse;
+    for (int i = 0; i < 8; ++i) y[i] = V::value(v[i], k) * inverse;
     // eight rows of a column: 8 bytes, at another place in each group of eight columns
     *reinterpret_cast<uint2*>(s_t + (col8 + k) * kBlock + (piece ^ (col8 / 8)) * 8) = e4m3x8(y);
   }
