@@ -500,14 +500,14 @@ def relay_copy(dst, src, max_ctas: int = 0, stream=None) -> None:
 # What these calls ask torch for on every call, looked up once: small calls cost more host time
 # than kernel time.
 _torch = None
-_float32 = _int32 = _raw_stream = _device = None
+_float32 = _int32 = _e4m3 = _raw_stream = _device = None
 _code: dict = {}
 
 
 def _bind_torch() -> None:
-    global _torch, _float32, _int32, _raw_stream, _device
+    global _torch, _float32, _int32, _e4m3, _raw_stream, _device
     import torch
-    _torch, _float32, _int32 = torch, torch.float32, torch.int32
+    _torch, _float32, _int32, _e4m3 = torch, torch.float32, torch.int32, torch.float8_e4m3fn
     _code.update({torch.float32: F32, torch.bfloat16: BF16})
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _device = getattr(torch._C, "_cuda_getDevice", None)
@@ -828,31 +828,30 @@ def alloc_fp8(rows: int, cols: int, device, tiles: bool = False, batch: Optional
 
 def _batched(x, name: str):
     """Address, batch, rows, columns and row stride of a CUDA matrix, or of matrices one behind the other."""
-    if x.dim() == 2:
-        ptr, r, c, ld = _rows(x, name)
-        return ptr, 1, r, c, ld
-    if x.dim() != 3 or not x.is_cuda:
+    shape, strides = x.shape, x.stride()
+    if not x.is_cuda or not 2 <= len(shape) <= 3:
         raise ValueError(f"{name} must be a CUDA matrix, or a batch of them (device memory)")
-    n, r, c = x.shape
-    sn, sr, sc = x.stride()
-    ld = sr if r > 1 else (max(sn, c) if n > 1 else max(sr, c))
-    if (c > 1 and sc != 1) or (n > 1 and sn != r * ld):
+    r, c = shape[-2:]
+    n, sn = (1, 0) if len(shape) == 2 else (shape[0], strides[0])
+    ld = strides[-2] if r > 1 else max(sn, c) if n > 1 else max(strides[-2], c)
+    if (c > 1 and strides[-1] != 1) or (n > 1 and sn != r * ld):
         raise ValueError(f"{name} must have contiguous rows, its matrices one behind the other")
     return x.data_ptr(), n, r, c, ld
 
 
 def _fp8(x, name: str):
-    if x.dtype is not _torch.float8_e4m3fn:
+    if x.dtype is not _e4m3:
         raise ValueError(f"{name} must be float8_e4m3fn, got {x.dtype}")
     return _batched(x, name)
 
 
 def _scales(x, name: str, shape) -> int:
     """A leading dimension of 1 may be there or not."""
-    if x.dim() == len(shape) + 1 and x.shape[0] == 1:
-        x = x[0]
-    elif len(shape) == x.dim() + 1 and shape[0] == 1:
-        shape = shape[1:]
+    if x.shape != shape:
+        if x.dim() == len(shape) + 1 and x.shape[0] == 1:
+            x = x[0]
+        elif len(shape) == x.dim() + 1 and shape[0] == 1:
+            shape = shape[1:]
     return _array(x, name, _float32, shape)
 
 
@@ -943,6 +942,7 @@ def make_grads(tensors: Sequence) -> RelayGrads:
     g.count = ctypes.cast(g._arrays[1], ctypes.POINTER(ctypes.c_size_t))
     g.dtype = ctypes.cast(g._arrays[2], ctypes.POINTER(ctypes.c_int32))
     g._tensors = tensors
+    g._ref = ctypes.byref(g)
     return g
 
 
@@ -961,7 +961,7 @@ def relay_grad_norm(grads: RelayGrads, norm, workspace=None, stream=None) -> Non
         _bind_torch()
     if workspace is None:
         workspace = _own_workspace(lambda: alloc_grad_workspace(grads, norm.device), stream)
-    _check(lib().relay_grad_norm(ctypes.byref(grads), _array(norm, "norm", _float32, (1,)), *_space(workspace),
+    _check(lib().relay_grad_norm(grads._ref, _array(norm, "norm", _float32, (1,)), *_space(workspace),
                                  _handle(stream)))
 
 
@@ -969,5 +969,5 @@ def relay_grad_clip(grads: RelayGrads, norm, max_norm: float, out: Optional[Rela
     """Scale every tensor by min(1, max_norm / (norm[0] + 1e-6)), in place or into the tensors of `out`."""
     if _torch is None:
         _bind_torch()
-    _check(lib().relay_grad_clip(ctypes.byref(grads), None if out is None else ctypes.byref(out),
+    _check(lib().relay_grad_clip(grads._ref, None if out is None else out._ref,
                                  _array(norm, "norm", _float32, (1,)), max_norm, _handle(stream)))
