@@ -11,8 +11,10 @@
 // The choice is by exact values: of two near ones the larger, of equal ones the lower expert. Without a bias the order
 // of c is that of x, and the keys are router.cu's. With one, c is computed in fp32, and a key is 22 bits of its distance below the
 // row's largest, in steps of 2^-21 of the largest score (2 of it in all; what is further below is only known to be). Where two
-// neighbours in the choice, or the last group that stays and the first that does not, are nearer than fp32's error
-// allows, and not equal in logit and bias, the row is chosen again in 64 bits (choose_slow): one row in some hundred.
+// neighbours in the choice are nearer than fp32's error allows, and not equal in logit and bias (one row in some hundred), the
+// chosen and a few candidates more are ranked by their values in 64 bits, one to a lane; groups as near to one another are compared
+// by the 64-bit values of their largest. What that does not settle is chosen again in 64 bits as a whole (choose_slow). (All near rows chosen again as a whole: 99 us at
+// 65536 x 256 bf16, eight groups, where 63 us are what the rest takes.)
 //
 // Bound by instruction issue, as router.cu's choice is; the backward pass by memory.
 #include <float.h>
@@ -255,6 +257,30 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 3 : 1) grouped_forwar
         const float most = key_value(max_row<L>(!stays && at.group < a.groups ? order_key(value) : kKeyNegInf));
         error = key_value(max_row<L>(order_key(error)));
         close = most > -INFINITY && !(least - most > error);
+        if (__any_sync(~0u, counted && close)) {
+          if (SIGMOID || !biased) {
+            // the groups' values in 64 bits, from the experts that may be their largest (a softmax's without its sum)
+            const float from = (a.group_sum > 1 && two > -INFINITY ? two : one) - (biased ? error : 0.0f);  // logits are exact
+            uint32_t may = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) may |= (uint32_t)(c[i] >= from && c[i] > -INFINITY) << i;
+            double first = -INFINITY, second = -INFINITY;
+            const T* xr = x + (row < a.tokens ? row : 0) * a.ld;
+            while (may != 0) {
+              const int e = at.e0 + __ffs(may) - 1;
+              may &= may - 1;
+              const double v = (double)ld1(xr + e);
+              const double score = SIGMOID ? 1.0 / (1.0 + exp(-v)) + (biased ? (double)a.bias[e] : 0.0) : exp(v - m);
+              second = larger(second, smaller(first, score));
+              first = larger(first, score);
+            }
+            __syncwarp();
+            join_two(first, second, a.lanes);
+            if (a.group_sum > 1 && second > -INFINITY) first += second;
+            stays = groups_before(a, first, at.group, lane0) < a.kept && at.group < a.groups;
+            close = false;
+          }  // the softmax's sum is wanted in 64 bits: choose_slow
+        }
       }
     }
     // keys
@@ -287,8 +313,7 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 3 : 1) grouped_forwar
     uint32_t win = max_row<L>(best);
     int taken = 0;      // of the lane's kTracked best
     uint32_t mine = 0;  // lane j: the key chosen j-th, 0 when there are no more
-#pragma unroll 4
-    for (int j = 0; j < a.top; ++j) {
+    auto choose = [&](int j) {
       const bool holder = best == win;
       if (sub == j) mine = win;
       uint32_t after = second;
@@ -305,28 +330,57 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 3 : 1) grouped_forwar
         taken = min(taken + 1, kTracked - 1);
       }
       win = max_row<L>(best);
-    }
+    };
+#pragma unroll 4
+    for (int j = 0; j < a.top; ++j) choose(j);
     const T* xr = x + (row < a.tokens ? row : 0) * a.ld;
+    int place = sub;  // of the lane's key in the choice
     if (biased || sizeof(T) == 4) {
+      // keys that do not tell which is larger
+      auto alike = [&](uint32_t k, uint32_t below) {
+        return biased ? (float)((k >> 10) - (below >> 10)) <= far : (k ^ below) <= kExpertMask;
+      };
       const uint32_t down = __shfl_down_sync(~0u, mine, 1, L), after = sub + 1 == a.top ? win : down;
-      bool near = false;
-      if (sub < a.top && mine != 0 && after != 0)
-        near = biased ? (float)((mine >> 10) - (after >> 10)) <= far : (mine ^ after) <= kExpertMask;
+      bool near = sub < a.top && mine != 0 && after != 0 && alike(mine, after);
       if (near) {  // equal ones are in the order of their experts
         const int e = key_expert(mine), f = key_expert(after);
         near = ld1(xr + e) != ld1(xr + f) || (biased && a.bias[e] != a.bias[f]);
       }
-      close |= near;
+      if (__any_sync(~0u, counted && near)) {
+        if (SIGMOID || !biased) {
+          // a few more candidates, ranked by their exact values
+          const int many = min(L, a.top + 4);
+          for (int j = a.top; j < many; ++j) choose(j);
+          const uint32_t last = __shfl_sync(~0u, mine, lane0 + a.top - 1);
+          close |= last != 0 && win != 0 && alike(last, win);  // not enough of them
+          double value = -INFINITY;
+          if (mine != 0) {
+            const double v = (double)ld1(xr + key_expert(mine));
+            value = biased ? 1.0 / (1.0 + exp(-v)) + (double)a.bias[key_expert(mine)] : v;
+          }
+          place = mine != 0 ? 0 : sub < a.top ? sub : 32;
+          for (int j = 0; j < many; ++j) {
+            const double v = __shfl_sync(~0u, value, lane0 + j);
+            const uint32_t k = __shfl_sync(~0u, mine, lane0 + j);
+            if (mine != 0 && k != 0) place += v > value || (v == value && key_expert(k) < key_expert(mine));
+          }
+        } else {
+          close |= near;  // the softmax's sum is wanted in 64 bits
+        }
+      }
     }
-    int chosen = mine != 0 ? key_expert(mine) : -1;
-    if (__any_sync(~0u, counted && (close || total != total)))
+    int chosen = mine != 0 && place < a.top ? key_expert(mine) : -1;
+    bool live = __shfl_sync(~0u, mine, lane0) != 0;  // something was chosen
+    if (__any_sync(~0u, counted && (close || total != total))) {
       chosen = choose_slow<T, N, L, SIGMOID>(a, xr, counted, sub);
-    const bool live = __shfl_sync(~0u, chosen, lane0) >= 0;  // something was chosen
+      place = sub;
+      live = __shfl_sync(~0u, chosen, lane0) >= 0;
+    }
     if (live) {
 #pragma unroll
       for (int i = 0; i < N; ++i) psum[i] = SIGMOID ? fmaf(s[i], inv, psum[i]) : psum[i] + s[i];
     }
-    const bool chose = sub < a.top && chosen >= 0;
+    const bool chose = chosen >= 0;
     // the scores of the chosen, to fp32's rounding
     float own = 0.0f;
     if (chose) {
@@ -339,9 +393,9 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 3 : 1) grouped_forwar
     }
     own *= a.scale;
     if (total != total) own = total;
-    if (sub < a.top && row < a.tokens) {
-      a.index[row * a.top + sub] = chosen;
-      a.gate[row * a.top + sub] = chose ? own : 0.0f;
+    if (place < a.top && row < a.tokens) {
+      a.index[row * a.top + place] = chosen;
+      a.gate[row * a.top + place] = chose ? own : 0.0f;
       if (chose) atomicAdd(&s_count[chosen], 1);  // integers: any order gives the same sum
     }
   }
@@ -568,7 +622,8 @@ relay_status_t relay_grouped_router_forward(const relay_routing_t* how, const vo
     // where all groups stay there is nothing to choose between them
     const int groups = how->kept < how->groups ? how->groups : 1, size = experts / groups;
     const Width w = width_of(groups, size, top);
-    const int blocks = (int)forward_blocks(tokens, kRouterWarps * (32 / std::max(w.lanes, 1)));
+    // as many blocks as are resident at once (three an SM of 8 values a lane, one of more), within the workspace's number
+    const int blocks = (int)std::min<int64_t>(w.values > 8 ? 152 : 3 * 152, forward_blocks(tokens, kRouterWarps * (32 / std::max(w.lanes, 1))));
     int32_t* part_count = reinterpret_cast<int32_t*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~(uintptr_t)15);
     float* part_prob = reinterpret_cast<float*>(part_count + (int64_t)blocks * experts);
     GroupArgs a{};
