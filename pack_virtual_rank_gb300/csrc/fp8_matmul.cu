@@ -734,7 +734,7 @@ cudaError_t launch(ProductArgs p, const relay_fp8_matmul_t& w, int splits, cudaS
                       !bytes_map(&p.b, w.b, b_rows, w.depth, w.b_stride, kHalf)))
     return cudaErrorInvalidValue;
   const int64_t tiles = most_tiles(w, S::kRows, S::kCols);
-  if (tiles * 8 > INT_MAX / 2) return cudaErrorInvalidConfiguration;
+  if (tiles * 8 > INT_MAX) return cudaErrorInvalidConfiguration;  // 2^28 tiles: refused before
   p.splits = splits;
   const int blocks = CTAS == 2 ? (int)std::min<int64_t>(2 * tiles, sm_count() / 2 * 2) : (int)(tiles * splits);
   return launch_chained_clusters(kernel, CTAS == 2 ? 2 : splits, blocks, kProductThreads, kFixed + 2 * (p.groups + 1) * 4, s, p);
@@ -782,8 +782,7 @@ Plan choose(const relay_fp8_matmul_t& w) {
   return best;
 }
 
-cudaError_t run(const ProductArgs& p, const relay_fp8_matmul_t& w, cudaStream_t s) {
-  const Plan c = choose(w);
+cudaError_t run(const ProductArgs& p, const relay_fp8_matmul_t& w, const Plan& c, cudaStream_t s) {
   if (c.pair) return launch<2, 256>(p, w, 1, s);
   switch (c.rows) {
     case 16: return launch<1, 16>(p, w, c.splits, s);
@@ -856,7 +855,10 @@ relay_status_t relay_matmul_fp8(const relay_fp8_matmul_t* w, cudaStream_t stream
     p.wide_out = w->out_dtype == RELAY_F32;
     p.vectors = !off(w->out, 16) && w->out_stride * E % 16 == 0;
     p.extra = t_extra;
-    const cudaError_t e = run(p, *w, stream);
+    const Plan plan = choose(*w);
+    const int64_t tiles = plan.pair ? most_tiles(*w, 256, 256) : most_tiles(*w, plan.rows, kHalf);
+    if (tiles * 8 > INT_MAX) return report_error(RELAY_ERR_UNSUPPORTED, "relay_matmul_fp8: more than 2^28 tiles of out");
+    const cudaError_t e = run(p, *w, plan, stream);
     if (e != cudaSuccess) return report_error(RELAY_ERR_CUDA, std::string("relay_matmul_fp8: ") + cudaGetErrorString(e));
     return RELAY_OK;
   });

@@ -206,6 +206,37 @@ def test_product_by_depth(lengths, rows, cols):
         at = end
 
 
+@pytest.mark.parametrize("rows,cols,depth", [(20, 300, 40), (300, 130, 1000)])
+def test_product_by_depth_without_groups(rows, cols, depth):
+    """The whole depth is one group, of any length."""
+    a, a_s, b, b_s = operands(rows, cols, depth)
+    out = torch.full((1, rows, cols), 9.0, device="cuda")
+    rv.relay_matmul_fp8(a, a_s, b, b_s, out, by_depth=True)
+    check(out[0], a, a_s, b, b_s)
+    flat = torch.full((rows, cols), 9.0, device="cuda")
+    rv.relay_matmul_fp8(a, a_s, b, b_s, flat, by_depth=True)
+    assert torch.equal(flat, out[0])
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 values in an operand and in the result."""
+    rows, cols, depth = 270000, 8192, 128
+    a, a_s, b, b_s = operands(rows, cols, depth)
+    out = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    rv.relay_matmul_fp8(a, a_s, b, b_s, out)
+    rv.device_status()
+    for part in (slice(0, 50), slice(262100, 262200), slice(rows - 40, rows)):
+        check(out[part], a[part], a_s[:, part], b, b_s)
+    del out
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-1] = torch.arange(cols, device="cuda") % 256 - 128
+    q, s = q_of(rows, cols)
+    rv.relay_quantize_fp8(x, q, s)
+    want, want_s = ref.quantize(x[-1:].cpu(), False)
+    assert same_values(q[-1:], want) and torch.equal(s[:, -1:].cpu().double(), want_s)
+    assert bool((q[-2].view(torch.uint8) == 0).all())
+
+
 @pytest.mark.parametrize("rows", [4, 60, 200])
 def test_offsets_that_are_wrong_stay_in_range(rows):
     """Unspecified results, no access out of range: what lies around the output stays."""

@@ -55,6 +55,13 @@ def test_product_refusals(relay_lib, change, words):
     refused(call("relay_matmul_fp8", PROD, **change), words)
 
 
+def test_more_tiles_than_are_numbered(relay_lib):
+    n = 2 ** 22
+    st, text = call("relay_matmul_fp8", PROD, rows=n, cols=n, out_stride=n, a=1 << 50, b=1 << 51, a_scale=1 << 52, b_scale=1 << 53,
+                    out=1 << 54)
+    assert st == rv.ERR_UNSUPPORTED and "2^28 tiles" in text
+
+
 def test_nothing_to_do(relay_lib):
     assert call("relay_quantize_fp8", QUANT, rows=0)[0] == rv.OK
     assert call("relay_quantize_fp8", QUANT, batch=0, tiles=1, tiles_t=1)[0] == rv.OK

@@ -183,3 +183,15 @@ def test_more_bytes_than_32_bits_number():
     rv.relay_grad_clip(rv.make_grads([x]), norm, want / 2)
     half = torch.tensor(0.5, dtype=torch.bfloat16).item()
     assert bool((x[:-3] == half).all()) and bool((x[-3:] == 50.0).all())
+
+
+def test_many_empty_tensors_between_others():
+    full = [torch.randn(40000, device="cuda"), torch.randn(9, device="cuda").bfloat16()]
+    empty = [torch.empty(0, device="cuda")] * 600
+    for xs in (empty + full, full[:1] + empty + full[1:] + empty, empty + full[:1] + empty + full[1:] + empty):
+        norm = torch.full((1,), 7.0, device="cuda")
+        rv.relay_grad_norm(rv.make_grads(xs), norm)
+        assert abs(norm.item() - norm_of(full)) <= NORM * norm_of(full)
+        outs = [torch.zeros_like(x) for x in xs]
+        rv.relay_grad_clip(rv.make_grads(xs), norm, 0.5, out=rv.make_grads(outs))
+        check_clip(xs, outs, norm_of(full), 0.5)
