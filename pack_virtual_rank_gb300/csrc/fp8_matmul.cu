@@ -376,7 +376,7 @@ __device__ void produce(const ProductArgs& p, int rank, uint32_t ring, const Bar
     const CUtensorMap* first = S::kPair ? &p.a : &p.b;
     const CUtensorMap* second = S::kPair ? &p.b : &p.a;
     for (int k = t.k_lo; k < t.k_hi; ++k) {
-      if (!(ok = bar_wait<false>(bar.empty + 8 * stage, phase ^ 1, gave_up))) break;
+      if (!(ok = __all_sync(~0u, bar_wait<false>(bar.empty + 8 * stage, phase ^ 1, gave_up)))) break;  // the warp as one
       if (elected()) {
         if (CTAS == 1 || rank == 0) bar_expect(bar.full + 8 * stage, CTAS * S::kStageBytes + p.extra);
         const uint32_t at = ring + stage * S::kStageBytes, on = pair_full + 8 * stage;
@@ -417,8 +417,8 @@ __device__ void multiply(uint32_t ring, const Bars& bar, uint32_t tmem, volatile
   for (Tile t = next(); ok && t.group >= 0; t = next()) {
     for (int k = t.k_lo; k < t.k_hi; ++k, ++n) {
       const uint32_t part = n % S::kAcc;
-      if (!(ok = bar_wait<false>(bar.acc_empty + 8 * part, ((n / S::kAcc) & 1) ^ 1, gave_up))) break;
-      if (!(ok = bar_wait<false>(bar.full + 8 * stage, phase, gave_up))) break;
+      const bool free = bar_wait<false>(bar.acc_empty + 8 * part, ((n / S::kAcc) & 1) ^ 1, gave_up);
+      if (!(ok = __all_sync(~0u, bar_wait<false>(bar.full + 8 * stage, phase, gave_up) && free))) break;  // the warp as one
       tc_fence_after();
       if (elected()) {
         const uint32_t at = ring + stage * S::kStageBytes;
