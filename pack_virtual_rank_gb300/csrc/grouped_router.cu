@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 3 : 1) grouped_forwar
     if (r < a.tokens) next.load(x + r * a.ld, at.e0, at.end, a.bytes);
   };
   fetch(row);
+  const bool full = a.size == N * a.lanes && a.groups * a.lanes == L;  // every lane has N experts
   for (; row - lane / L < a.tokens; row += stride) {
     float c[N], s[N];
     next.values(c);
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 3 : 1) grouped_forwar
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (at.e0 + i >= at.end) c[i] = -INFINITY;  // also where a row's load brought more than the lane's own
+      if (!full && at.e0 + i >= at.end) c[i] = -INFINITY;  // also where a row's load brought more than the lane's own
       s[i] = SIGMOID ? sigmoid_near(c[i]) : exp_below(c[i], m);
       if (!SIGMOID && c[i] == -INFINITY) s[i] = 0.0f;
       total += s[i];
@@ -296,8 +297,9 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 3 : 1) grouped_forwar
       close |= !(most < INFINITY);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float below = fmaf(c[i] - most, steps, 4194303.0f);
-        key[i] = c[i] == -INFINITY || !stays ? 0u : (uint32_t)fmaxf(below, 1.0f) << 10 | (kExpertMask - (uint32_t)(at.e0 + i));
+        // added to 2^23 the steps are the fraction's low bits; what is above them leaves by the shift
+        const float below = fmaxf(fmaf(c[i] - most, steps, 4194303.0f), 1.0f) + 8388608.0f;
+        key[i] = c[i] == -INFINITY || !stays ? 0u : __float_as_uint(below) << 10 | (kExpertMask - (uint32_t)(at.e0 + i));
       }
     } else {
 #pragma unroll
@@ -431,7 +433,7 @@ __device__ __forceinline__ float sigmoid_slope(float x, float* slope) {
 }
 
 template <class T, int N, int L>
-__global__ void __launch_bounds__(kRouterThreads) sigmoid_backward_kernel(const SigmoidArgs a) {
+__global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) sigmoid_backward_kernel(const SigmoidArgs a) {
   constexpr int kRows = 32 / L;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane % L, e0 = sub * N;
   dep_launch();
@@ -482,8 +484,9 @@ __global__ void __launch_bounds__(kRouterThreads) sigmoid_backward_kernel(const 
     const float own_s = holds ? sigmoid_slope(own, &own_slope) : 0.0f;
     if (!holds) q = own_slope = 0.0f;
     if (a.normalize) {
-      const float z = sum_row<L>(own_s), zi = z == 0.0f ? 0.0f : 1.0f / z;
-      q = (q - sum_row<L>(own_s * q) * zi) * zi;
+      // a row's only chosen expert has a share of exactly 1: its difference is 0
+      const float z = sum_row<L>(own_s), zi = z == 0.0f ? 0.0f : 1.0f / z, share = own_s == z ? 1.0f : own_s * zi;
+      q = (q - sum_row<L>(share * q)) * zi;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = live ? v[i] * ((g[i] - dot) * inv) : 0.0f;

@@ -270,3 +270,11 @@ def run_rank(x, k, bias, how):
            torch.empty(e, dtype=torch.int32, device="cuda"), torch.empty(e, device="cuda"))
     rv.relay_grouped_router_forward(x.cuda(), *out, bias=bias.cuda(), **how)
     return out
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_a_single_renormalized_gate_has_no_gradient(score):
+    """Its gate is the scale, whatever the logits: the gradient is 0, not what rounding leaves of a difference."""
+    x, d = torch.randn(300, 24), torch.randn(300, 1)
+    out = run(x, 1, torch.randn(24) * 0.1, d_gate=d, score=score, normalize=True, scale=2.5)
+    assert bool((out["gate"] == 2.5).all()) and bool((out["d_logits"] == 0).all())
