@@ -73,6 +73,27 @@ __device__ __forceinline__ void store_bytes(uint8_t* to, uint2 b, int n) {
   for (int i = 0; i < n; ++i) to[i] = (uint8_t)(all >> (8 * i));
 }
 
+// Eight rows of eight bytes to eight columns.
+__device__ __forceinline__ void turn4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  const uint32_t e = __byte_perm(a, b, 0x5140), f = __byte_perm(c, d, 0x5140), g = __byte_perm(a, b, 0x7362), h = __byte_perm(c, d, 0x7362);
+  a = __byte_perm(e, f, 0x5410);
+  b = __byte_perm(e, f, 0x7632);
+  c = __byte_perm(g, h, 0x5410);
+  d = __byte_perm(g, h, 0x7632);
+}
+__device__ __forceinline__ void turn(uint2 (&r)[8]) {
+  turn4(r[0].x, r[1].x, r[2].x, r[3].x);
+  turn4(r[4].x, r[5].x, r[6].x, r[7].x);
+  turn4(r[0].y, r[1].y, r[2].y, r[3].y);
+  turn4(r[4].y, r[5].y, r[6].y, r[7].y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // the corners change places
+    const uint32_t t = r[i].y;
+    r[i].y = r[4 + i].x;
+    r[4 + i].x = t;
+  }
+}
+
 // Eight neighbours of a row as they lie. Magnitudes compare as integers, two bf16 at once.
 template <class T>
 struct Eight;
@@ -102,7 +123,9 @@ struct Eight<uint16_t> {
   }
 };
 
-template <class T>
+// EDGES: rows of x or of an output may end inside 8 values, or be off the 16-byte grid. Without, the program is short enough for the
+// instruction caches.
+template <class T, bool EDGES>
 __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) fp8_quantize_kernel(const QuantArgs a) {
   using V = Eight<T>;
   using P = typename V::P;
@@ -110,6 +133,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) fp8_qua
   __shared__ __align__(16) uint8_t s_t[kBlock * kBlock];
   __shared__ uint32_t s_col[kQuantThreads / 32][kBlock];
   __shared__ uint32_t s_top[kQuantThreads / 32];
+  __shared__ __align__(16) float s_inverse[kBlock];  // of the columns' scales
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int piece = threadIdx.x / 16, row8 = piece * 8, col8 = threadIdx.x % 16 * 8;  // the thread's first row and column
   dep_launch();
@@ -148,7 +172,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) fp8_qua
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + row8 + i, c = c0 + col8;
     const T* from = x + (int64_t)r * a.ld + c;
-    if (r < r_end && a.vectors && c + 8 <= a.cols) {
+    if (r < r_end && (!EDGES || (a.vectors && c + 8 <= a.cols))) {
 #pragma unroll
       for (int k = 0; k < W; k += 4) {
         const uint4 u = ld_stream_v4(reinterpret_cast<const uint32_t*>(from) + k);
@@ -157,7 +181,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) fp8_qua
     } else {
 #pragma unroll
       for (int k = 0; k < W; ++k) v[i][k] = 0;
-      if (r < r_end) {
+      if (EDGES && r < r_end) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (c + k < a.cols) V::set(v[i], k, P::template load1<false>(from + k));
@@ -200,6 +224,21 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) fp8_qua
     if (threadIdx.x == 0 && a.q != nullptr && a.tiles) a.scale[(batch * row_blocks + db) * col_blocks + cb] = s;
     if (threadIdx.x == 32 && a.qt != nullptr && a.tiles_t) a.scale_t[(batch * col_blocks + cb) * a.depth_blocks + db] = s;
   }
+  if (need_cols) {
+    if (threadIdx.x < kBlock) {
+      const int c = threadIdx.x;
+      uint32_t t = 0;
+#pragma unroll
+      for (int i = 0; i < kQuantThreads / 32; ++i) t = max(t, s_col[i][c]);
+      float inverse;
+      const float s = scale_of(t, &inverse);
+      s_inverse[c] = inverse;
+      if (!EDGES || c0 + c < a.cols) a.scale_t[(int64_t)db * a.cols + c0 + c] = s;
+    }
+    __syncthreads();
+  }
+  const bool same = a.q != nullptr && a.tiles && a.tiles_t;  // the transpose holds the same bytes
+  uint2 bytes[8];
   if (a.q != nullptr) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -218,25 +257,34 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) fp8_qua
       float y[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) y[k] = V::value(v[i], k) * inverse;
-      if (r < r_end) store_bytes(a.q + ((int64_t)batch * a.rows + r) * a.q_ld + c0 + col8, e4m3x8(y), a.cols - c0 - col8);
+      bytes[i] = e4m3x8(y);
+      if (r < r_end) store_bytes(a.q + ((int64_t)batch * a.rows + r) * a.q_ld + c0 + col8, bytes[i], EDGES ? a.cols - c0 - col8 : 8);
     }
   }
   if (a.qt == nullptr) return;
+  // eight rows of a column: 8 bytes, at another place in each group of eight columns
+  auto put = [&](int k, uint2 column) {
+    *reinterpret_cast<uint2*>(s_t + (col8 + k) * kBlock + (piece ^ (col8 / 8)) * 8) = column;
+  };
+  if (same) {
+    turn(bytes);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float inverse = tile_inverse;
-    if (!a.tiles_t) {
-      uint32_t t = 0;
+    for (int k = 0; k < 8; ++k) put(k, bytes[k]);
+  } else {
+    float inverse[8];
 #pragma unroll
-      for (int i = 0; i < kQuantThreads / 32; ++i) t = max(t, s_col[i][col8 + k]);
-      const float s = scale_of(t, &inverse);
-      if (piece == 0 && c0 + col8 + k < a.cols) a.scale_t[(int64_t)db * a.cols + c0 + col8 + k] = s;
+    for (int k = 0; k < 8; k += 4) {
+      const float4 u = a.tiles_t ? make_float4(tile_inverse, tile_inverse, tile_inverse, tile_inverse)
+                                 : *reinterpret_cast<const float4*>(s_inverse + col8 + k);
+      inverse[k] = u.x; inverse[k + 1] = u.y; inverse[k + 2] = u.z; inverse[k + 3] = u.w;
     }
-    float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = V::value(v[i], k) * inverse;
-    // eight rows of a column: 8 bytes, at another place in each group of eight columns
-    *reinterpret_cast<uint2*>(s_t + (col8 + k) * kBlock + (piece ^ (col8 / 8)) * 8) = e4m3x8(y);
+    for (int k = 0; k < 8; ++k) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = V::value(v[i], k) * inverse[k];
+      put(k, e4m3x8(y));
+    }
   }
   __syncthreads();
   // along the rows: all 128 of a group's block (zeros behind its last row), or what the matrix has
@@ -245,9 +293,9 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) fp8_qua
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = i * 16 + piece, at = threadIdx.x % 16;
-    if (c0 + c >= a.cols) break;
+    if (EDGES && c0 + c >= a.cols) break;
     const uint2 b = *reinterpret_cast<const uint2*>(s_t + c * kBlock + (at ^ (c / 8)) * 8);
-    store_bytes(a.qt + ((int64_t)batch * a.cols + c0 + c) * a.qt_ld + d0 + at * 8, b, width - at * 8);
+    store_bytes(a.qt + ((int64_t)batch * a.cols + c0 + c) * a.qt_ld + d0 + at * 8, b, EDGES ? width - at * 8 : 8);
   }
 }
 
@@ -323,8 +371,10 @@ relay_status_t relay_quantize_fp8(const relay_fp8_quantize_t* p, cudaStream_t st
     a.depth_blocks = (int32_t)dblocks;
     a.offset = p->offset;
     const dim3 grid((unsigned)cb, (unsigned)(grouped ? dblocks : rb), (unsigned)p->batch);
-    const cudaError_t e = launch_chained(p->dtype == RELAY_BF16 ? fp8_quantize_kernel<uint16_t> : fp8_quantize_kernel<float>, grid,
-                                         kQuantThreads, 0, stream, a);
+    const bool edges = !a.vectors || a.cols % kBlock != 0 || (a.qt != nullptr && !grouped && a.rows % kBlock != 0);
+    auto* kernel = p->dtype == RELAY_BF16 ? (edges ? fp8_quantize_kernel<uint16_t, true> : fp8_quantize_kernel<uint16_t, false>)
+                                          : (edges ? fp8_quantize_kernel<float, true> : fp8_quantize_kernel<float, false>);
+    const cudaError_t e = launch_chained(kernel, grid, kQuantThreads, 0, stream, a);
     if (e != cudaSuccess) return report_error(RELAY_ERR_CUDA, std::string("relay_quantize_fp8: ") + cudaGetErrorString(e));
     return RELAY_OK;
   });

@@ -35,7 +35,7 @@ def same_values(q, want):
 # ------------------------------------------------------------------------- quantization --
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (3, 130), (128, 128), (129, 257), (200, 1000), (77, 16), (300, 9)])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (3, 130), (128, 128), (129, 257), (200, 1000), (77, 16), (300, 9), (256, 384), (200, 256)])
 @pytest.mark.parametrize("tiles", [False, True])
 def test_quantize_is_exact(rows, cols, dtype, tiles):
     x = data(rows, cols, dtype)
@@ -83,7 +83,7 @@ def test_ends_of_the_range():
     assert bool(torch.isnan(st).all()) and bool(torch.isnan(qt.float()).all())
 
 
-@pytest.mark.parametrize("rows,cols,n", [(100, 200, 3), (128, 128, 1), (257, 129, 4)])
+@pytest.mark.parametrize("rows,cols,n", [(100, 200, 3), (128, 128, 1), (257, 129, 4), (256, 384, 2)])
 def test_quantize_a_batch(rows, cols, n):
     x = torch.stack([data(rows, cols, "bf16", seed=i) for i in range(n)])
     q, s = q_of(rows, cols, True, n)
@@ -103,9 +103,10 @@ def offsets(lengths, skip=0):
 
 
 @pytest.mark.parametrize("lengths", GROUPS)
+@pytest.mark.parametrize("cols", [150, 256])
 @pytest.mark.parametrize("tiles_t", [False, True])
-def test_quantize_groups(lengths, tiles_t):
-    skip, behind, cols = 3, 5, 150
+def test_quantize_groups(lengths, tiles_t, cols):
+    skip, behind = 3, 5
     rows = skip + sum(lengths) + behind
     x = data(rows, cols, "bf16")
     x[:skip] = math.nan                                   # no group's rows: not looked at
