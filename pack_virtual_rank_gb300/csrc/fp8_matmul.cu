@@ -49,7 +49,7 @@ struct Shape {
   static constexpr int kShare = NT / CTAS;     // rows of the second operand one CTA brings
   static constexpr int kFirstBytes = kHalf * kBlock, kStageBytes = kFirstBytes + kShare * kBlock;
   static constexpr int kPerSm = NT <= 64 ? 2 : 1;  // CTAs an SM holds: one's start and end under the other's products
-  static constexpr int kStages = kPair ? 6 : NT >= 128 ? 6 : NT >= 64 ? 4 : 5;
+  static constexpr int kStages = kPair ? 4 : NT >= 128 ? 6 : NT >= 64 ? 4 : 5;
   static constexpr int kAcc = NT >= 256 ? 2 : 4;          // blocks in tensor memory
   static constexpr int kTmem = kAcc * NT < 32 ? 32 : kAcc * NT;
   static constexpr int kMine = NT / 2;         // columns of the accumulator one thread finishes
@@ -57,7 +57,8 @@ struct Shape {
   static constexpr int kScales = kAScales * kBScales;
   static constexpr int kRing = kStages * kStageBytes, kScaleBytes = kScaleStages * kScales * 4;
   static constexpr int kRawBytes = (kAScales + 4) * 4;  // a block's scales as they lie, b's behind them
-  static constexpr int kStoreBytes = kPair ? 2048 : 1024;  // of a finishing warp
+  static constexpr int kStoreBytes = kPair ? 8192 : 1024;  // of a finishing warp
+  static constexpr int kFinishBytes = kFinishWarps * kStoreBytes;
   static_assert(kTmem <= 512, "tensor memory has 512 columns");
   static_assert(kStageBytes % 1024 == 0 && kFirstBytes % 1024 == 0, "operands on 1024-byte addresses");
 };
@@ -66,7 +67,7 @@ constexpr int kLaunchRegs = 168, kFeedRegs = 56, kFinishRegs = 224;
 static_assert(kFeedRegs + 2 * kFinishRegs == 3 * kLaunchRegs, "the groups' registers add up to the launch's");
 
 struct ProductArgs {
-  CUtensorMap a, b;
+  CUtensorMap a, b, c;                       // c: out, where out_map
   const float* a_scale;
   const float* b_scale;
   void* out;
@@ -75,6 +76,7 @@ struct ProductArgs {
   int32_t rows, cols, depth_blocks, groups;  // groups 1 where there are none
   int32_t by_depth, wide_out, splits;
   int32_t vectors;                           // out's rows take 16-byte stores
+  int32_t out_map;                           // and end on 16 bytes: they can be stored through a map
   int32_t extra;                             // bytes a stage waits for that no load brings (test of the bounded waits)
 };
 
@@ -300,13 +302,51 @@ __device__ __forceinline__ void store_columns(const ProductArgs& p, const Tile& 
   }
 }
 
-// A warp's 32 rows of N columns, v[j] row r0 + lane, column n + j. Through the warp's buffer, 64 bytes of each row at a time,
-// neighbouring threads get neighbouring pieces of a row.
+// A warp's 32 rows of N columns, v[j] row r0 + lane, column n + j. Where all rows are the group's they leave through a tensor map
+// while the next tile is multiplied, 128 bytes of each row to a box; else, 64 bytes of each row at a time, neighbouring
+// threads get neighbouring pieces of a row.
 template <class T, int N>
 __device__ __forceinline__ void store_rows(const ProductArgs& p, const Tile& t, int r0, int n, uint32_t buf, const float (&v)[N]) {
   constexpr int kCols = 64 / (int)sizeof(T), kPiece = 16 / (int)sizeof(T);
   const int lane = threadIdx.x % 32;
   if (n >= p.cols || r0 >= t.r_end) return;
+  auto free_buffer = [&] {  // the store before may still be reading it
+    if (lane == 0) store_wait_read<0>();
+    __syncwarp();
+  };
+  free_buffer();
+  if (p.out_map && r0 + 32 <= t.r_end) {
+    constexpr int kBox = 2 * kCols;  // columns of a box; two boxes fit the buffer
+#pragma unroll
+    for (int c = 0; c < N; c += 2 * kBox) {
+      if (c > 0) {
+        if (n + c >= p.cols) break;
+        free_buffer();
+      }
+#pragma unroll
+      for (int box = 0; box < 2; ++box)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = c + box * kBox + q * kPiece;
+            w[i] = sizeof(T) == 4 ? __float_as_uint(v[j + i]) : bf16x2_rn(v[j + 2 * i], v[j + 2 * i + 1]);
+          }
+          const uint32_t at = buf + box * 4096 + lane * 128 + ((q ^ (lane & 7)) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+        }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int y = (p.by_depth ? t.group * p.rows : 0) + r0;
+        map_store(&p.c, n + c, y, buf);
+        if (n + c + kBox < p.cols) map_store(&p.c, n + c + kBox, y, buf + 4096);
+        store_commit();
+      }
+    }
+    return;
+  }
   T* out = static_cast<T*>(p.out) + (int64_t)(p.by_depth ? t.group : 0) * p.rows * p.out_ld;
 #pragma unroll
   for (int c = 0; c < N; c += kCols) {
@@ -563,10 +603,9 @@ __global__ void __launch_bounds__(kProductThreads, Shape<CTAS, NT>::kPerSm) fp8_
   __shared__ int s_gave_up;
   const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), rank = (int)pair_rank();
   dep_launch();
-  const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u, scales = ring + S::kRing;
+  const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u, staging = ring + S::kRing, scales = staging + S::kFinishBytes;
   const uint32_t raw = scales + S::kScaleBytes;
-  const uint32_t staging = raw + kAhead * S::kRawBytes;
-  int* s_first = reinterpret_cast<int*>(smem_raw + (staging - smem_addr(smem_raw)) + kFinishWarps * S::kStoreBytes);
+  int* s_first = reinterpret_cast<int*>(smem_raw + (raw - smem_addr(smem_raw)) + kAhead * S::kRawBytes);
   Bars bar;
   bar.full = smem_addr(s_bar);
   bar.empty = bar.full + 8 * S::kStages;
@@ -596,6 +635,7 @@ __global__ void __launch_bounds__(kProductThreads, Shape<CTAS, NT>::kPerSm) fp8_
       map_prefetch(&p.a);
       map_prefetch(&p.b);
     }
+    if (S::kPair && p.out_map) map_prefetch(&p.c);
   }
   if (warp == 1) tmem_alloc<CTAS>(smem_addr(&s_tmem), S::kTmem);
   dep_wait();
@@ -658,6 +698,7 @@ __global__ void __launch_bounds__(kProductThreads, Shape<CTAS, NT>::kPerSm) fp8_
         else store_columns<uint16_t>(p, t, row, col, buf, v);
       }
     }
+    if (S::kPair && lane == 0) store_wait_all();
   }
   __syncwarp();
   tc_fence_before();
@@ -691,7 +732,17 @@ thread_local int t_extra = 0;
 
 relay_status_t bad(const std::string& msg) { return report_error(RELAY_ERR_INVALID_ARGUMENT, "relay_matmul_fp8: " + msg); }
 
-// A matrix [rows][bytes], read in boxes of box_rows by 128 bytes (128-byte swizzle).
+// out [rows][cols], written in boxes of 32 rows by 128 bytes (128-byte swizzle).
+bool out_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, bool wide) {
+  const EncodeFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * (wide ? 4 : 2)};
+  const cuuint32_t box[2] = {wide ? 32u : 64u, 32u}, unit[2] = {1, 1};
+  return fn(m, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, unit,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// A matrix [rows][bytes], read in boxes of box_rows by 128 bytes.
 bool bytes_map(CUtensorMap* m, const void* p, int64_t rows, int64_t bytes, int64_t ld, int box_rows) {
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return false;
@@ -712,7 +763,7 @@ template <int CTAS, int NT>
 cudaError_t launch(ProductArgs p, const relay_fp8_matmul_t& w, int splits, cudaStream_t s) {
   using S = Shape<CTAS, NT>;
   static thread_local int ready_device = -1;
-  constexpr int kFixed = 1024 + S::kRing + S::kScaleBytes + kAhead * S::kRawBytes + kFinishWarps * S::kStoreBytes;
+  constexpr int kFixed = 1024 + S::kRing + S::kScaleBytes + kAhead * S::kRawBytes + S::kFinishBytes;
   constexpr int kMost = kFixed + 2 * (RELAY_FP8_MAX_GROUPS + 1) * 4;
   static_assert(kMost <= 227 * 1024 - 1024, "shared memory of a CTA");
   static_assert(S::kRing >= NT * kHalf * 4 || CTAS == 2, "the ring takes the partial sums");
@@ -732,6 +783,9 @@ cudaError_t launch(ProductArgs p, const relay_fp8_matmul_t& w, int splits, cudaS
   const int64_t a_rows = w.rows, b_rows = w.by_depth ? w.cols : w.cols * std::max(w.groups, 1);
   if (w.depth > 0 && (!bytes_map(&p.a, w.a, a_rows, w.depth, w.a_stride, S::kPair ? kHalf : NT) ||
                       !bytes_map(&p.b, w.b, b_rows, w.depth, w.b_stride, kHalf)))
+    return cudaErrorInvalidValue;
+  if (S::kPair && p.out_map &&
+      !out_map(&p.c, w.out, w.by_depth ? w.rows * std::max(w.groups, 1) : w.rows, w.cols, w.out_stride, p.wide_out != 0))
     return cudaErrorInvalidValue;
   const int64_t tiles = most_tiles(w, S::kRows, S::kCols);
   if (tiles * 8 > INT_MAX) return cudaErrorInvalidConfiguration;  // 2^28 tiles: refused before
@@ -854,6 +908,8 @@ relay_status_t relay_matmul_fp8(const relay_fp8_matmul_t* w, cudaStream_t stream
     p.by_depth = w->by_depth != 0;
     p.wide_out = w->out_dtype == RELAY_F32;
     p.vectors = !off(w->out, 16) && w->out_stride * E % 16 == 0;
+    // a store through a map writes 16 bytes at a time, also where the row ends inside them
+    p.out_map = p.vectors && w->cols * E % 16 == 0;
     p.extra = t_extra;
     const Plan plan = choose(*w);
     const int64_t tiles = plan.pair ? most_tiles(*w, 256, 256) : most_tiles(*w, plan.rows, kHalf);
