@@ -795,10 +795,13 @@ cudaError_t launch(ProductArgs p, const relay_fp8_matmul_t& w, int splits, cudaS
 }
 
 // Which kernel. A round of CTAs takes `open` us and `step` us for every block of the inner dimension; the numbers are fitted to
-// products of 8 to 8192 rows by 1536 to 8192 columns of 1024 to 4096 values, and to 96 to 16384 rows in 16 and 32 groups. What it
-// decides there (us): 8 x 4096 x 4096: 16 rows split eight ways 7.3, whole 10.4, 32 rows whole 11.1; 256 x 1536 x 1024: 16 rows
-// 5.3, 32 5.5, 64 6.3, 128 6.3, pairs 8.2; 512 x 4096 x 4096: 128 rows 14.7, pairs 17.4; 1024 x 4096 x 4096: 128 rows 28.3, pairs
-// 18.5; 96 rows of 32 groups by 1408 x 2048: 16 rows 15.0, 64 18.6; 2048 rows of 32 groups: 64 rows 20.5, 16 40, pairs 29.3.
+// products of 8 to 8192 rows by 1536 to 8192 columns of 1024 to 4096 values, and to 96 to 16384 rows in 16 and 32 groups. On 35
+// sizes, 28 of them others (1 to 5000 rows, 200 to 8192 columns, 200 to 16384 values, up to 32 groups of rows or of the depth), what
+// it takes is within 8% of the best of ten, but for 512 rows in 32 groups: uneven ones take 16.0 us where 64 rows to a tile take 11.9,
+// even ones 16.2 where 64 take 18.8. What it decides (us): 8 x 4096 x 4096: 16 rows split eight ways 7.3, whole 10.4, 32 rows whole
+// 11.1; 256 x 1536 x 1024: 16 rows 5.3, 32 5.5, 64 6.3, 128 6.3, pairs 8.2; 400 x 4096 x 4096: 128 rows 14.1, pairs 17.0; 1024 x 4096
+// x 4096: 128 rows 27.4, pairs 17.2; 96 rows of 32 groups by 1408 x 2048: 16 rows 8.8, 64 10.8; 2048 rows of 32 groups: 64 rows 21.6,
+// 128 26.9, pairs 28.4.
 struct Plan {
   bool pair;
   int rows, splits;
@@ -811,7 +814,8 @@ Plan choose(const relay_fp8_matmul_t& w) {
     const double across = (double)((w.cols + cols - 1) / cols), all = (double)((w.rows + rows - 1) / rows);
     if (w.by_depth) return across * all * std::max(w.groups, 1);
     if (w.groups == 0) return across * all;
-    return across * std::max<double>((double)w.rows / rows + 0.5 * w.groups, (double)std::min<int64_t>(w.groups, w.rows));
+    // some groups have no row, and the others' last tiles are half full
+    return across * std::max((double)w.rows / rows + 0.4 * w.groups, 0.8 * (double)std::min<int64_t>(w.groups, w.rows));
   };
   Plan best{true, 256, 1};
   double least = 3.5 + std::ceil(tiles(256, 256) / (sms / 2)) * (1.5 + 0.41 * kb);
@@ -825,7 +829,8 @@ Plan choose(const relay_fp8_matmul_t& w) {
       if (splits > 1 && (o.rows > 32 || t * splits > 2 * sms)) break;
       const double rounds = t * splits / sms, step = o.step * kb / splits;
       // two CTAs an SM up to 64 rows; joining the splits costs about as much as a start
-      double cost = o.rows == 128 ? std::ceil(rounds) * (o.open + step) : o.open + step * std::max(1.0, 0.85 * rounds);
+      double cost = o.rows == 128 ? std::ceil(rounds + (w.groups > 0 && !w.by_depth ? 0.3 : 0.0)) * (o.open + step)
+                                  : std::max(1.0, std::ceil(rounds / 2)) * o.open + step * std::max(1.0, 0.85 * rounds);
       if (splits > 1) cost += 3.5;
       if (cost < least) {
         least = cost;
