@@ -7,7 +7,7 @@
 // another part of tensor memory.
 //
 // A pair of CTAs walks tiles of 256 x 256 of out: a's rows are the product's M, one to a lane of the accumulator, and a thread
-// finishes the 128 columns of one of b's tiles, so that a block's scales are one number a thread. 8192 x 8192 x 4096: 196 us, 2.8
+// finishes the 128 columns of one of b's tiles, so that a block's scales are one number a thread. 8192 x 8192 x 4096: 190 us, 2.9
 // PFLOP/s, tensor pipe 66% busy. What bounds it is the hand-over: reading the sums and the multiply-adds take about 480 cycles a
 // block, the way there and back 250, the products 512, and tensor memory holds two blocks.
 //
@@ -194,14 +194,22 @@ __host__ __device__ constexpr uint32_t fp8_desc(int m, int n) { return (1u << 4)
 // W columns of 32 lanes (lane i of the warp: row i) of tensor memory; the values are there after tmem_wait on them.
 template <int W>
 __device__ __forceinline__ void tmem_load(uint32_t tmem, float (&v)[W]) {
-  if constexpr (W == 16) {
+  if constexpr (W == 32) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+        "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(tmem)
+        : "memory");
+  } else if constexpr (W == 16) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(tmem)
         : "memory");
   } else {
-    static_assert(W == 8, "8 or 16 columns");
+    static_assert(W == 8, "8, 16 or 32 columns");
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                  : "r"(tmem)
@@ -565,7 +573,8 @@ template <int CTAS, int NT>
 __device__ __forceinline__ bool finish(const Tile& t, uint32_t& n, uint32_t scales, const Bars& bar, uint32_t tmem, int quarter, int part,
                                        volatile int* gave_up, float (&v)[Shape<CTAS, NT>::kMine]) {
   using S = Shape<CTAS, NT>;
-  constexpr int W = S::kMine <= 16 ? S::kMine : 16;  // 32 at a time: 202 us where 16 take 196 (8192 x 8192 x 4096)
+  // columns read at a time: 32 of a pair's 128 take 190 us where 16 take 196 (8192 x 8192 x 4096); 64, or a read ahead, spill
+  constexpr int W = S::kMine <= 16 ? S::kMine : NT == 64 ? 16 : 32;
   const int lane = threadIdx.x % 32;
   const uint32_t first_empty = S::kPair ? pair_addr(bar.acc_empty, 0) : bar.acc_empty;
 #pragma unroll
