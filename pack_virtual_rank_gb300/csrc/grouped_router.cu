@@ -16,7 +16,8 @@
 // by the 64-bit values of their largest. What that does not settle is chosen again in 64 bits as a whole (choose_slow). (All near rows chosen again as a whole: 99 us at
 // 65536 x 256 bf16, eight groups, where 63 us are what the rest takes.)
 //
-// Bound by instruction issue, as router.cu's choice is; the backward pass by memory.
+// Bound by instructions, most of them comparisons and selections, as router.cu's choice is (65536 x 256 bf16, 8 of 256 from 4 of 8
+// groups with a bias: 72 us, its bytes 5); the backward pass 23 us, its bytes 10.
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -168,8 +169,11 @@ __device__ __noinline__ int choose_slow(const GroupArgs& a, const T* x, bool cou
   return chosen;
 }
 
+// Blocks an SM holds (four of 8 values a lane spill and are slower; one of 16: 138 us and not 99 at 65536 x 512, eight groups).
+constexpr int resident(int values) { return values == 8 ? 3 : values == 16 ? 2 : 1; }
+
 template <class T, int N, int L, bool SIGMOID>
-__global__ void __launch_bounds__(kRouterThreads, N == 8 ? 3 : 1) grouped_forward_kernel(const GroupArgs a) {
+__global__ void __launch_bounds__(kRouterThreads, resident(N)) grouped_forward_kernel(const GroupArgs a) {
   constexpr int kRows = 32 / L;
   constexpr int kTracked = L < 32 ? 3 : 2;  // a lane's best keys kept in order: fewer lanes are chosen from more often
   extern __shared__ float s_prob[];         // [warps * kRows][experts], then the counts [experts]
@@ -625,8 +629,8 @@ relay_status_t relay_grouped_router_forward(const relay_routing_t* how, const vo
     // where all groups stay there is nothing to choose between them
     const int groups = how->kept < how->groups ? how->groups : 1, size = experts / groups;
     const Width w = width_of(groups, size, top);
-    // as many blocks as are resident at once (three an SM of 8 values a lane, one of more), within the workspace's number
-    const int blocks = (int)std::min<int64_t>(w.values > 8 ? 152 : 3 * 152, forward_blocks(tokens, kRouterWarps * (32 / std::max(w.lanes, 1))));
+    // as many blocks as are resident at once, within the workspace's number
+    const int blocks = (int)std::min<int64_t>(resident(w.values) * 152, forward_blocks(tokens, kRouterWarps * (32 / std::max(w.lanes, 1))));
     int32_t* part_count = reinterpret_cast<int32_t*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~(uintptr_t)15);
     float* part_prob = reinterpret_cast<float*>(part_count + (int64_t)blocks * experts);
     GroupArgs a{};
