@@ -40,6 +40,7 @@ constexpr int kHalf = 128;                     // rows of the product's first op
 constexpr int kFinishWarps = 8, kScaleWarps = 2;
 constexpr int kProductThreads = 128 + 32 * kFinishWarps;
 constexpr int kScaleStages = 4;                // blocks whose scales wait in shared memory
+constexpr int kMostSplits = 8;                 // CTAs of a cluster that share a tile's inner dimension
 constexpr int kAhead = 4;                      // blocks whose scales are on their way there
 
 // CTAS 2: a pair's 256 of a's rows by NT = 256 of b's. CTAS 1: 128 of b's rows by NT of a's; splits of the inner dimension are
@@ -728,8 +729,12 @@ __global__ void __launch_bounds__(kProductThreads, Shape<CTAS, NT>::kPerSm) fp8_
       const int each = NT / p.splits;
       for (int e = threadIdx.x; e < each * kHalf; e += kProductThreads) {
         const int j = rank * each + e / kHalf, row = t.r0 + j, col = t.n0 + e % kHalf;
-        float sum = 0.0f;
-        for (int s = 0; s < p.splits; ++s) sum = __fadd_rn(sum, ld_cluster(pair_addr(ring + (j * kHalf + e % kHalf) * 4, s)));
+        float part[kMostSplits], sum = 0.0f;  // all asked for before the first is added
+#pragma unroll
+        for (int s = 0; s < kMostSplits; ++s)
+          part[s] = s < p.splits ? ld_cluster(pair_addr(ring + (j * kHalf + e % kHalf) * 4, s)) : 0.0f;
+#pragma unroll
+        for (int s = 0; s < kMostSplits; ++s) sum = __fadd_rn(sum, part[s]);
         if (row < t.r_end && col < p.cols) store_out(p, t.group, row, col, sum);
       }
     }
@@ -841,7 +846,7 @@ Plan choose(const relay_fp8_matmul_t& w) {
   } one[] = {{16, 2.7, 0.23}, {32, 2.8, 0.26}, {64, 3.0, 0.40}, {128, 3.4, 0.31}};
   for (const auto& o : one) {
     const double t = tiles(o.rows, kHalf);
-    for (int splits = 1; splits <= 8; splits *= 2) {
+    for (int splits = 1; splits <= kMostSplits; splits *= 2) {
       if (splits > 1 && (o.rows > 32 || t * splits > 2 * sms)) break;
       const double rounds = t * splits / sms, step = o.step * kb / splits;
       // two CTAs an SM up to 64 rows; joining the splits costs about as much as a start
