@@ -17,7 +17,7 @@
 // 65536 x 256 bf16, eight groups, where 63 us are what the rest takes.)
 //
 // Bound by instructions, most of them comparisons and selections, as router.cu's choice is (65536 x 256 bf16, 8 of 256 from 4 of 8
-// groups with a bias: 72 us, its bytes 5); the backward pass 23 us, its bytes 10.
+// groups with a bias: 73 us, its bytes 5); the backward pass 23 us, its bytes 10.
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -169,7 +169,7 @@ __device__ __noinline__ int choose_slow(const GroupArgs& a, const T* x, bool cou
   return chosen;
 }
 
-// Blocks an SM holds (four of 8 values a lane spill and are slower; one of 16: 138 us and not 99 at 65536 x 512, eight groups).
+// Blocks an SM holds (four of 8 values a lane spill and are slower; one of 16: 138 us and not 101 at 65536 x 512, eight groups).
 constexpr int resident(int values) { return values == 8 ? 3 : values == 16 ? 2 : 1; }
 
 template <class T, int N, int L, bool SIGMOID>
@@ -348,9 +348,22 @@ __global__ void __launch_bounds__(kRouterThreads, resident(N)) grouped_forward_k
       };
       const uint32_t down = __shfl_down_sync(~0u, mine, 1, L), after = sub + 1 == a.top ? win : down;
       bool near = sub < a.top && mine != 0 && after != 0 && alike(mine, after);
+      bool same = false;  // the last one chosen and the first one left
       if (near) {  // equal ones are in the order of their experts
         const int e = key_expert(mine), f = key_expert(after);
         near = ld1(xr + e) != ld1(xr + f) || (biased && a.bias[e] != a.bias[f]);
+        same = !near && sub + 1 == a.top;
+      }
+      if (__any_sync(~0u, counted && same)) {
+        // one that is larger may stand behind equal ones
+        const uint32_t last = __shfl_sync(~0u, mine, lane0 + a.top - 1);
+        if (__shfl_sync(~0u, (int)same, lane0 + a.top - 1)) {
+          const int e = key_expert(last);
+          const float v = ld1(xr + e), b = biased ? a.bias[e] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (key[i] != 0 && key[i] < last && alike(last, key[i])) near |= ld1(xr + at.e0 + i) != v || (biased && a.bias[at.e0 + i] != b);
+        }
       }
       if (__any_sync(~0u, counted && near)) {
         if (SIGMOID || !biased) {

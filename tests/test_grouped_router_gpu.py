@@ -105,6 +105,33 @@ def test_choice_values_nearer_than_fp32_tells(groups, kept, score):
     assert torch.equal(out["counts"], want["counts"])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("experts,groups,kept,top", [(8, 1, 1, 2), (93, 1, 1, 1), (64, 8, 4, 8), (256, 8, 8, 3), (512, 1, 1, 32)])
+def test_the_best_stand_behind_equal_ones(experts, groups, kept, top, score, dtype):
+    """The choice ends among equal ones; a few nearer to them than fp32 or a key's upper bits tell, and larger, come later."""
+    g = torch.Generator().manual_seed(13)
+    x, bias = torch.ones(90, experts), torch.zeros(experts)
+    for r in range(1, 90):                                # row 0: all equal
+        some = torch.randperm(experts, generator=g)[:1 + r % 6]
+        if dtype == "f32":
+            x[r, some] += 2.0 ** -23 * (1 + r % 5)
+        x[r, torch.randperm(experts, generator=g)[:r % 3]] = 0.5
+    ends = torch.arange(max(0, experts - 3), experts)
+    x[5] = 1.0
+    if dtype == "f32":
+        x[5, ends] += 2.0 ** -22
+    raised = bias.clone()
+    raised[ends] = 2.0 ** -30
+    for b in (None, bias, raised):
+        how = dict(groups=groups, kept=kept, score=score, group_sum=2)
+        xt = x.to(DT[dtype])
+        want = ref.route(xt, top, b, **how)
+        out = run(xt, top, b, **how)
+        assert torch.equal(out["index"], want["index"])
+        assert torch.equal(out["counts"], want["counts"])
+
+
 def test_experts_that_cannot_be_chosen():
     g = torch.Generator().manual_seed(5)
     x = torch.randn(90, 32, generator=g)
