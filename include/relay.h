@@ -558,8 +558,8 @@ relay_status_t relay_router_bias_update(const int32_t* counts, const float* bias
  * Row strides are multiples of 16 (bytes), addresses of 8-bit matrices on 16-byte boundaries.
  *
  * Groups (experts): offset[groups + 1] int32 in device memory, ascending; group g holds rows offset[g] .. offset[g + 1] - 1 of
- * the rows, which stand sorted by group. A group may be empty; rows before offset[0] and from offset[groups] on are
- * neither read nor written. Offsets outside [0, rows] or out of order give unspecified results, and no access out of range.
+ * the rows, which stand sorted by group. A group may be empty; what rows before offset[0] and from offset[groups] on
+ * hold has no effect, and they are not written. Offsets outside [0, rows] or out of order give unspecified results, and no access out of range.
  *
  * relay_quantize_fp8 -- x[batch][rows][cols] (RELAY_F32 or RELAY_BF16; the batch's matrices one behind the other,
  *   rows * x_stride elements apart) to 8 bits, as it lies (q, scale), transposed (qt, scale_t), or both. Scales are powers of two,
