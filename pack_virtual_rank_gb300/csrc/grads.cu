@@ -8,8 +8,9 @@
 // and 973 us to scale out of place (6.9 TB/s).
 //
 // Sums. A thread squares and adds the values of a chunk (64 bf16, 32 fp32) in fp32, and the chunks' sums in two floats, the
-// second with what the first's roundings lost; squares that fp32 cannot hold (a sum below 2^-90 or above 2^125) are
-// summed again, scaled, into a double. Threads, then blocks join in doubles in a fixed order: equal calls give equal bits.
+// second with what the first's roundings lost; squares that fp32 cannot hold (a chunk's sum below 2^-90 or above 2^100) are
+// summed again, scaled, into a double. (A launch has 2^30 chunks and 456 blocks: with fewer than 2^22 of them a thread's sum stays
+// below 2^122.) Threads, then blocks join in doubles in a fixed order: equal calls give equal bits.
 //
 // Clipping walks the chunks from the last to the first: what the norm read last is still in L2.
 #include <math.h>
@@ -94,6 +95,9 @@ __device__ __forceinline__ float squares(const uint4 (&u)[kVectors], float by) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+// The largest sum of a chunk that `hi` takes: with all of a thread's it stays finite.
+constexpr float kMostSum = 0x1p100f;
+
 struct Sum {
   float hi = 0.0f, lo = 0.0f;
   double rare = 0.0;
@@ -113,7 +117,7 @@ __device__ __forceinline__ void sum_chunk(const void* in, int64_t n, int64_t chu
 #pragma unroll
   for (int j = 0; j < kVectors; ++j) u[j] = load_vector<T>(x, n, skip, v0 + j * kGradThreads);
   const float s = squares<T>(u, 1.0f);
-  if (s >= 0x1p-90f && s <= 0x1p125f) {
+  if (s >= 0x1p-90f && s <= kMostSum) {
     sum.add(s);
     return;
   }
@@ -280,8 +284,10 @@ int sum_blocks(int64_t chunks) { return (int)std::min<int64_t>(chunks, 3 * 152);
 int clip_blocks(int64_t chunks) { return (int)std::min<int64_t>(chunks, 40 * 152); }
 // So few chunks that one block is done before a second launch would be.
 constexpr int64_t kOneBlockChunks = 4;
+constexpr int64_t kMostChunks = 1ll << 30;  // of a launch
+static_assert((double)kMostSum * (kMostChunks / (3 * 152) + kOneBlockChunks) < 0x1p127, "a thread's sum of chunks is finite");
 
-// Tensors of one launch: a piece of the list with at most kMostTensors tensors and 2^31 - 1 chunks.
+// Tensors of one launch: a piece of the list with at most kMostTensors tensors and kMostChunks chunks.
 struct Piece {
   int lo, hi;
   int64_t chunks;
@@ -290,8 +296,8 @@ relay_status_t pieces_of(const relay_grads_t& g, std::vector<Piece>* out) {
   Piece p{0, 0, 0};
   for (int i = 0; i < g.n; ++i) {
     const int64_t c = chunks_of(g, i);
-    if (c > (1ll << 30)) return bad("a tensor is too large");
-    if (p.hi - p.lo == kMostTensors || p.chunks + c > (1ll << 30)) {
+    if (c > kMostChunks) return bad("a tensor is too large");
+    if (p.hi - p.lo == kMostTensors || p.chunks + c > kMostChunks) {
       if (p.chunks > 0) out->push_back(p);
       p = Piece{i, i, 0};
     }
