@@ -935,14 +935,12 @@ def make_grads(tensors: Sequence) -> RelayGrads:
     n = len(tensors)
     g = RelayGrads()
     g.n = n
-    g._arrays = ((ctypes.c_void_p * max(n, 1))(*[x.data_ptr() for x in tensors]),
-                 (ctypes.c_size_t * max(n, 1))(*[x.numel() for x in tensors]),
-                 (ctypes.c_int32 * max(n, 1))(*[_dtype(x, f"tensors[{i}]") for i, x in enumerate(tensors)]))
-    g.grad = ctypes.cast(g._arrays[0], ctypes.POINTER(ctypes.c_void_p))
-    g.count = ctypes.cast(g._arrays[1], ctypes.POINTER(ctypes.c_size_t))
-    g.dtype = ctypes.cast(g._arrays[2], ctypes.POINTER(ctypes.c_int32))
+    # assigned, the arrays live as long as the list; nothing here refers back to it (a cycle would hold the tensors until a
+    # garbage collection, which device memory does not bring about)
+    g.grad = (ctypes.c_void_p * max(n, 1))(*[x.data_ptr() for x in tensors])
+    g.count = (ctypes.c_size_t * max(n, 1))(*[x.numel() for x in tensors])
+    g.dtype = (ctypes.c_int32 * max(n, 1))(*[_dtype(x, f"tensors[{i}]") for i, x in enumerate(tensors)])
     g._tensors = tensors
-    g._ref = ctypes.byref(g)
     return g
 
 
@@ -961,7 +959,7 @@ def relay_grad_norm(grads: RelayGrads, norm, workspace=None, stream=None) -> Non
         _bind_torch()
     if workspace is None:
         workspace = _own_workspace(lambda: alloc_grad_workspace(grads, norm.device), stream)
-    _check(lib().relay_grad_norm(grads._ref, _array(norm, "norm", _float32, (1,)), *_space(workspace),
+    _check(lib().relay_grad_norm(ctypes.byref(grads), _array(norm, "norm", _float32, (1,)), *_space(workspace),
                                  _handle(stream)))
 
 
@@ -969,5 +967,5 @@ def relay_grad_clip(grads: RelayGrads, norm, max_norm: float, out: Optional[Rela
     """Scale every tensor by min(1, max_norm / (norm[0] + 1e-6)), in place or into the tensors of `out`."""
     if _torch is None:
         _bind_torch()
-    _check(lib().relay_grad_clip(grads._ref, None if out is None else out._ref,
+    _check(lib().relay_grad_clip(ctypes.byref(grads), None if out is None else ctypes.byref(out),
                                  _array(norm, "norm", _float32, (1,)), max_norm, _handle(stream)))
