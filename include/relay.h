@@ -520,7 +520,8 @@ relay_status_t relay_router_backward(const void* logits, int64_t row_stride, rel
  *     s. Both as relay_router_forward's: summed over ranks by relay_allreduce, taken by relay_balance_loss (counts also by
  *     relay_router_bias_update). A row that mask leaves out, or of which no expert can be chosen, has index -1 and gate 0 and is in
  *     neither.
- *   A NaN logit makes its row's gates and prob_sum NaN; index stays in range and distinct, with a NaN below what else can be chosen.
+ *   A NaN logit makes its row's gates and prob_sum NaN; index stays in range and distinct, with a NaN below what else can be chosen
+ *     (the other scores being those without it). So does a logit of +inf with softmax: the experts of +inf share the row.
  *   Scores are fp32: one below 2^-126 is 0. bias values are finite or -inf.
  *   1 <= groups <= RELAY_ROUTER_MAX_GROUPS, a divisor of experts; with kept < groups at most RELAY_ROUTER_MAX_GROUPED experts;
  *   top <= RELAY_ROUTER_MAX_TOP and the experts of the kept groups. Two launches at most. workspace: relay_router_workspace_size bytes.

@@ -99,7 +99,8 @@ __device__ __forceinline__ int groups_before(const GroupArgs& a, F value, int gr
 }
 
 // The choice of a row in 64 bits: the chosen expert of lane j, or -1. Scores that are NaN stand below all others that can be
-// chosen. Rare, and kept out of the kernel's registers.
+// chosen: a softmax is taken over the logits that are numbers, so that a NaN logit makes its own score NaN and no other's. Of
+// logits of +inf each has an equal share. Rare, and kept out of the kernel's registers.
 template <class T, int N, int L, bool SIGMOID>
 __device__ __noinline__ int choose_slow(const GroupArgs& a, const T* x, bool counted, int sub) {
   const int lane0 = threadIdx.x % 32 - sub;
@@ -111,15 +112,16 @@ __device__ __noinline__ int choose_slow(const GroupArgs& a, const T* x, bool cou
     if (!(c[i] == -INFINITY)) can |= 1u << i;
     top = fmax(top, c[i]);
   }
+  auto below = [&](double v) { return v == top ? 1.0 : exp(v - top); };  // also at +inf
   if (!SIGMOID && (a.bias != nullptr || a.group_sum > 1)) {
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) top = fmax(top, exchange(top, o));
     for (int i = 0; i < N; ++i)
-      if (can >> i & 1) sum += exp(c[i] - top);
+      if ((can >> i & 1) && c[i] == c[i]) sum += below(c[i]);
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) sum += exchange(sum, o);
   }
-  auto score = [&](double v) { return SIGMOID ? 1.0 / (1.0 + exp(-v)) : exp(v - top) / sum; };
+  auto score = [&](double v) { return SIGMOID ? 1.0 / (1.0 + exp(-v)) : below(v) / sum; };
   auto ordered = [](double v) { return v != v ? -DBL_MAX : v; };
   double one = -INFINITY, two = -INFINITY;
   for (int i = 0; i < N; ++i) {

@@ -1,0 +1,56 @@
+"""The router with scores, bias and groups on rows at the ends: NaN and infinite logits in the choice and in the
+gradients, scores next to the end of fp32's range."""
+import math
+
+import pytest
+import torch
+
+import grouped_router_ref as ref
+from test_grouped_router_gpu import F, SOFT, run
+
+pytestmark = pytest.mark.gpu
+
+GROUPINGS = [(1, 1), (4, 2), (8, 8)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("group_sum", [1, 2])
+@pytest.mark.parametrize("groups,kept", GROUPINGS)
+def test_a_nan_logit_stands_below_the_others(groups, kept, group_sum, biased, score, dtype):
+    """Where enough others can be chosen, the choice is the one without the NaN experts; and the rows beside stay."""
+    g = torch.Generator().manual_seed(5)
+    x = (torch.randn(64, 40, generator=g) * 2).to(dtype)
+    bad = torch.zeros(64, dtype=torch.bool)
+    bad[::3] = True
+    x[::3, ::4] = math.nan
+    x[3, 0], x[3, 8] = math.nan, math.nan
+    x[6, 1] = -math.inf
+    bias = torch.randn(40, generator=g) * 0.02 if biased else None
+    how = dict(groups=groups, kept=kept, group_sum=group_sum, score=score)
+    want = ref.route(torch.where(torch.isnan(x), -math.inf, x.double()), 8, bias, **how)
+    out = run(x, 8, bias, **how)
+    assert torch.equal(out["index"], want["index"])
+    assert torch.equal(out["counts"], want["counts"])
+    assert bool(torch.isnan(out["gate"][bad]).all()) and bool(torch.isfinite(out["gate"][~bad]).all())
+    assert bool(((out["gate"][~bad].double() - want["gate"][~bad]).abs() <= SOFT * want["gate"][~bad]).all())
+    assert bool(torch.isnan(out["prob_sum"]).all())
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("group_sum", [1, 2])
+@pytest.mark.parametrize("groups,kept", GROUPINGS)
+def test_infinite_logits_are_the_largest(groups, kept, group_sum, biased):
+    """Softmax: experts of +inf share the row, the others' scores are 0 (as with a logit far above the rest). The
+    row's gates show it as NaN."""
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(30, 40, generator=g)
+    x[::2, 17] = math.inf
+    x[4, 3], x[8, 39], x[8, 0] = math.inf, math.inf, -math.inf
+    bias = torch.randn(40, generator=g) * 0.02 if biased else None
+    how = dict(groups=groups, kept=kept, group_sum=group_sum, score="softmax")
+    want = ref.route(torch.where(x == math.inf, 1e4, x.double()), 8, bias, **how)
+    out = run(x, 8, bias, **how)
+    assert torch.equal(out["index"], want["index"])
+    assert bool(torch.isnan(out["gate"][::2]).all()) and bool(torch.isfinite(out["gate"][1::2]).all())
