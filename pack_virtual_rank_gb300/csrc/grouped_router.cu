@@ -122,7 +122,7 @@ __device__ __noinline__ int choose_slow(const GroupArgs& a, const T* x, bool cou
     for (int o = L / 2; o > 0; o >>= 1) sum += exchange(sum, o);
   }
   auto score = [&](double v) { return SIGMOID ? 1.0 / (1.0 + exp(-v)) : below(v) / sum; };
-  auto ordered = [](double v) { return v != v ? -DBL_MAX : v; };
+  auto ordered = [](double v) { return v != v ? -DBL_MAX / 2 : v; };  // two of them still stand above a group of which nothing can be chosen
   double one = -INFINITY, two = -INFINITY;
   for (int i = 0; i < N; ++i) {
     if (!(can >> i & 1)) continue;

@@ -38,6 +38,27 @@ def test_a_nan_logit_stands_below_the_others(groups, kept, group_sum, biased, sc
     assert bool(torch.isnan(out["prob_sum"]).all())
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("group_sum", [1, 2])
+def test_more_chosen_than_there_are_numbers(group_sum, biased, score):
+    """The NaN experts fill what is left, by their numbers; groups of nothing else stand behind all others, and before
+    one of which nothing can be chosen."""
+    x = torch.full((3, 12), math.nan)
+    x[0, [3, 7]] = torch.tensor([1.0, 2.0])
+    x[1, 4:8] = torch.tensor([0.5, -3.0, 0.5, 0.25])
+    x[2, :4] = -math.inf
+    bias = torch.zeros(12) if biased else None
+    how = dict(score=score, group_sum=group_sum)
+    out = run(x, 6, bias, **how)
+    assert out["index"][0].tolist() == [7, 3, 0, 1, 2, 4]
+    assert out["index"][1].tolist() == [4, 6, 7, 5, 0, 1]
+    assert out["index"][2].tolist() == [4, 5, 6, 7, 8, 9]
+    out = run(x, 6, bias, groups=3, kept=2, **how)
+    assert out["index"][1].tolist() == [4, 6, 7, 5, 0, 1]
+    assert out["index"][2].tolist() == [4, 5, 6, 7, 8, 9]
+
+
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("group_sum", [1, 2])
 @pytest.mark.parametrize("groups,kept", GROUPINGS)
