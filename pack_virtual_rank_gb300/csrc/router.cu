@@ -327,7 +327,8 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const B
     dot = sum_row<L>(dot) * inv;
     float extra = e * inv * dg;
     if (a.normalize) {
-      const float c = e / sum_row<L>(e), inner = sum_row<L>(c * dg);
+      // chosen scores of 0 (relay_grouped_router_forward chooses by more than the score) have gates of 0
+      const float z = sum_row<L>(e), c = z == 0.0f ? 0.0f : e / z, inner = sum_row<L>(c * dg);
       extra = c * (dg - inner);
     }
 #pragma unroll

@@ -75,3 +75,25 @@ def test_infinite_logits_are_the_largest(groups, kept, group_sum, biased):
     out = run(x, 8, bias, **how)
     assert torch.equal(out["index"], want["index"])
     assert bool(torch.isnan(out["gate"][::2]).all()) and bool(torch.isfinite(out["gate"][1::2]).all())
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_chosen_scores_of_zero(dtype, normalize):
+    """Softmax: the experts that can be chosen lie so far below drained ones that their scores are 0. Gates are 0 and have no
+    gradient; the shares' gradient is the usual one."""
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(50, 24, generator=g)
+    x[:40, :4] += 150.0
+    x = x.to(dtype)
+    bias = torch.zeros(24)
+    bias[:4] = -math.inf
+    d, dp = torch.randn(50, 3, generator=g), torch.rand(24, generator=g)
+    how = dict(score="softmax", normalize=normalize, scale=2.5)
+    out = run(x, 3, bias, None, d, dp, **how)
+    want = ref.route(x, 3, bias, d_gate=torch.where(torch.arange(50)[:, None] < 40, 0.0, d), d_prob=dp, **how)
+    assert torch.equal(out["index"], want["index"])
+    assert bool((out["gate"][:40] == 0).all()) and bool((out["gate"][40:] > 0).all())
+    unit = 2.0 ** -24 if dtype is torch.float32 else 2.0 ** -8
+    bound = 2 * SOFT * want["size"] + unit * want["d_logits"].abs() + 1e-36
+    assert bool(((out["d_logits"].double() - want["d_logits"]).abs() <= bound).all())
