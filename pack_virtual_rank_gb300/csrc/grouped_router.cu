@@ -499,20 +499,32 @@ __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) sigmoid_backwa
     sum = sum_row<L>(sum);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     dot = sum_row<L>(dot) * inv;
+    const bool small = in && sum < 0x1p-40f;
+    if (__any_sync(~0u, small)) {
+      // scores whose products with small d_prob leave fp32's range: by their shares (a slope is the score where it is small)
+      float by_share = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) by_share = fmaf(v[i] * inv, g[i], by_share);
+      by_share = sum_row<L>(by_share);
+      if (small) dot = by_share;
+    }
     float own_slope, q = dg;
     const float own_s = holds ? sigmoid_slope(own, &own_slope) : 0.0f;
     if (!holds) q = own_slope = 0.0f;
+    float gate_slope = own_slope;
     if (a.normalize) {
       // a row's only chosen expert has a share of exactly 1: its difference is 0
       const float z = sum_row<L>(own_s), zi = z == 0.0f ? 0.0f : 1.0f / z, share = own_s == z ? 1.0f : own_s * zi;
-      q = (q - sum_row<L>(share * q)) * zi;
+      q -= sum_row<L>(share * q);
+      gate_slope *= zi;
     }
+    // in this order: 1 / sum and 1 / z are up to 2^126, a slope's product with them is at most 1
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = live ? v[i] * ((g[i] - dot) * inv) : 0.0f;
+    for (int i = 0; i < N; ++i) v[i] = live ? v[i] * inv * (g[i] - dot) : 0.0f;
     T* dx = static_cast<T*>(a.d_logits) + row * a.d_ld;
     if (in) Lane<T, N>::store(dx, v, e0, a.experts, a.d_bytes);
     __syncwarp();  // orders the row's stores before the chosen experts'
-    if (in && holds) st1(dx + mine, own_slope * ((own_g - dot) * inv + q));
+    if (in && holds) st1(dx + mine, own_slope * inv * (own_g - dot) + gate_slope * q);
   }
 }
 

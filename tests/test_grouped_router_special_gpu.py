@@ -97,3 +97,23 @@ def test_chosen_scores_of_zero(dtype, normalize):
     unit = 2.0 ** -24 if dtype is torch.float32 else 2.0 ** -8
     bound = 2 * SOFT * want["size"] + unit * want["d_logits"].abs() + 1e-36
     assert bool(((out["d_logits"].double() - want["d_logits"]).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("size", [1e-7, 1.0, 1000.0, 1e15])
+@pytest.mark.parametrize("normalize", [False, True])
+def test_gradients_of_small_sigmoids(normalize, size):
+    """All scores of a row near the end of fp32's range: shares and renormalized gates are ordinary numbers, and so are their
+    gradients, for small and for large ones coming in."""
+    g = torch.Generator().manual_seed(10)
+    x = -86.0 + torch.randn(64, 24, generator=g) * 0.3
+    x[5, 7], x[6, :20] = -math.inf, -math.inf
+    x[7, 3] = 2.0
+    d, dp = torch.randn(64, 4, generator=g) * size, torch.randn(24, generator=g) * size
+    for dg, ds in ((d, dp), (d, None), (None, dp)):
+        how = dict(score="sigmoid", normalize=normalize)
+        out = run(x, 4, None, None, dg, ds, **how)
+        want = ref.route(x, 4, d_gate=dg, d_prob=ds, **how)
+        assert torch.equal(out["index"], want["index"])
+        # exp of x within (2 |x| + 6) F, in the score, the sum and the slope
+        bound = 4 * (2 * 88 + 6) * F * want["size"] + 2.0 ** -126
+        assert bool(((out["d_logits"].double() - want["d_logits"]).abs() <= bound).all())
