@@ -522,7 +522,8 @@ relay_status_t relay_router_backward(const void* logits, int64_t row_stride, rel
  *     neither.
  *   A NaN logit makes its row's gates and prob_sum NaN; index stays in range and distinct, with a NaN below what else can be chosen
  *     (the other scores being those without it). So does a logit of +inf with softmax: the experts of +inf share the row.
- *   Scores are fp32: one below 2^-126 is 0. bias values are finite or -inf.
+ *   Scores are fp32: one below 2^-126 (softmax: of the row's largest score) is 0, in gates and gradients. bias values are finite
+ *   or -inf.
  *   1 <= groups <= RELAY_ROUTER_MAX_GROUPS, a divisor of experts; with kept < groups at most RELAY_ROUTER_MAX_GROUPED experts;
  *   top <= RELAY_ROUTER_MAX_TOP and the experts of the kept groups. Two launches at most. workspace: relay_router_workspace_size bytes.
  *

@@ -402,15 +402,19 @@ __global__ void __launch_bounds__(kRouterThreads, resident(N)) grouped_forward_k
       for (int i = 0; i < N; ++i) psum[i] = SIGMOID ? fmaf(s[i], inv, psum[i]) : psum[i] + s[i];
     }
     const bool chose = chosen >= 0;
-    // the scores of the chosen, to fp32's rounding
+    // the scores of the chosen, to fp32's rounding; of a softmax before the division by its sum. What is below the normal
+    // range is 0, as in the gradient
     float own = 0.0f;
     if (chose) {
       const float v = ld1(xr + chosen);
-      own = SIGMOID ? 1.0f / (1.0f + expf(-v)) : expf(v - m) * inv;
+      own = SIGMOID ? 1.0f / (1.0f + expf(-v)) : expf(v - m);
+      if (own < FLT_MIN) own = 0.0f;
     }
     if (a.normalize) {
       const float z = sum_row<L>(own);
       own = z == 0.0f ? 0.0f : own / z;
+    } else if (!SIGMOID) {
+      own *= inv;
     }
     own *= a.scale;
     if (total != total) own = total;

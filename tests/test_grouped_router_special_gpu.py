@@ -99,6 +99,36 @@ def test_chosen_scores_of_zero(dtype, normalize):
     assert bool(((out["d_logits"].double() - want["d_logits"]).abs() <= bound).all())
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("top", [1, 4])
+@pytest.mark.parametrize("normalize", [False, True])
+def test_gates_and_gradients_agree_on_what_is_zero(normalize, top, score):
+    """Scores from 2^-110 to 2^-160 (softmax: of the row's largest): what is below fp32's normal range is 0, in the gates and
+    in their gradients, and what is above it is right to its rounding."""
+    x = -torch.linspace(110, 160, 401)[:, None] * math.log(2.0) + torch.linspace(-0.2, 0.2, 16)
+    bias = torch.zeros(16)
+    if score == "softmax":
+        x[:, 0] = 0.0
+        bias[0] = -math.inf
+    d = torch.ones(401, top) + torch.arange(top)
+    out = run(x, top, bias, None, d, None, score=score, normalize=normalize)
+    index = out["index"].long()
+    # the scores' logarithms to the base 2; the two sides' exponentials may differ next to the border
+    power = x.double().gather(1, index) / math.log(2.0)
+    below, above = power < -126.01, power > -125.99
+    assert bool((out["gate"][below] == 0).all()) and bool((out["gate"][above] > 0).all())
+    assert bool(torch.isfinite(out["d_logits"]).all())
+    chosen = out["d_logits"].gather(1, index)
+    assert bool((chosen[below] == 0).all())
+    rows = above.all(dim=1)
+    want = ref.route(x[rows], top, bias, d_gate=d[rows], score=score, normalize=normalize)
+    # exp of x within (2 |x| + 6) F for the fast exponential, |x| <= 88, both of a quotient's sides; gates by the exact one
+    off = (out["gate"][rows].double() - want["gate"]).abs()
+    assert bool((off <= 16 * F * want["gate"] + 2.0 ** -150).all())
+    off = (out["d_logits"][rows].double() - want["d_logits"]).abs()
+    assert bool((off <= 4 * (2 * 88 + 6) * F * want["size"] + 2.0 ** -126).all())
+
+
 @pytest.mark.parametrize("size", [1e-7, 1.0, 1000.0, 1e15])
 @pytest.mark.parametrize("normalize", [False, True])
 def test_gradients_of_small_sigmoids(normalize, size):
