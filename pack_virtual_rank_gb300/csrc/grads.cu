@@ -13,6 +13,7 @@
 // below 2^122.) Threads, then blocks join in doubles in a fixed order: equal calls give equal bits.
 //
 // Clipping walks the chunks from the last to the first: what the norm read last is still in L2.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -167,21 +168,27 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const double* p
   if (threadIdx.x == 0) *norm = (float)sqrt(v);
 }
 
+// factor * after: a factor that fp32 holds to its rounding, and 1, or a power of two that it leaves out.
+struct Factor {
+  float factor, after;
+};
+
 template <class T>
-__device__ __forceinline__ void clip_chunk(const void* in, void* out, int64_t n, int64_t chunk, float factor) {
+__device__ __forceinline__ void clip_chunk(const void* in, void* out, int64_t n, int64_t chunk, const Factor& by) {
   using E = typename T::Elem;
   constexpr int L = T::P::kLanes;
   const auto* x = static_cast<const E*>(in);
   auto* y = static_cast<E*>(out);
   const int skip = (int)(reinterpret_cast<uintptr_t>(in) % 16 / sizeof(E));
   const int64_t v0 = chunk * (kGradThreads * kVectors) + threadIdx.x;
-  if ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) % 16 != 0) {
-    // the two lie differently on the 16-byte grid: neighbouring threads take neighbouring elements
+  if ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) % 16 != 0 || by.after != 1.0f) {
+    // the two lie differently on the 16-byte grid, or the factor is a rare one (here alone, it costs the rest nothing:
+    // 1% otherwise): neighbouring threads take neighbouring elements
     const int64_t lo = max((int64_t)0, chunk * (kGradThreads * kVectors * L) - skip);
     const int64_t hi = min(n, (chunk + 1) * (kGradThreads * kVectors * L) - skip);
 #pragma unroll 8
     for (int64_t e = lo + threadIdx.x; e < hi; e += kGradThreads)
-      T::P::store1(y + e, __fmul_rn(T::P::template load1<true>(x + e), factor));
+      T::P::store1(y + e, __fmul_rn(__fmul_rn(T::P::template load1<true>(x + e), by.factor), by.after));
     return;
   }
   uint4 u[kVectors];
@@ -197,12 +204,12 @@ __device__ __forceinline__ void clip_chunk(const void* in, void* out, int64_t n,
       float f[L];
       T::P::unpack(u[j], f);
 #pragma unroll
-      for (int i = 0; i < L; ++i) f[i] = __fmul_rn(f[i], factor);
+      for (int i = 0; i < L; ++i) f[i] = __fmul_rn(f[i], by.factor);
       st_v4(y + at, T::P::pack(f));
     } else {
 #pragma unroll
       for (int i = 0; i < L; ++i)
-        if (at + i >= 0 && at + i < n) T::P::store1(y + at + i, __fmul_rn(T::P::template load1<true>(x + at + i), factor));
+        if (at + i >= 0 && at + i < n) T::P::store1(y + at + i, __fmul_rn(T::P::template load1<true>(x + at + i), by.factor));
     }
   }
 }
@@ -214,15 +221,16 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
   dep_launch();
   dep_wait();
   const float total = *norm;
-  float factor = max_norm / (total + 1e-6f);
+  Factor by{max_norm / (total + 1e-6f), 1.0f};
+  if (by.factor < FLT_MIN) by = Factor{max_norm * 0x1p100f / (total + 1e-6f), 0x1p-100f};  // max_norm is below 4
   // nothing to clip, or a norm that says that something is wrong: the values stay as they are
-  if (!(factor < 1.0f) || !(total < INFINITY)) factor = 1.0f;
-  if (factor == 1.0f && in_place) return;
+  if (!(by.factor < 1.0f) || !(total < INFINITY)) by = Factor{1.0f, 1.0f};
+  if (by.factor == 1.0f && in_place) return;
   for (int k = blockIdx.x; k < t.chunks; k += gridDim.x) {
     const int chunk = t.chunks - 1 - k, i = tensor_of(t, chunk);
     const int64_t n = t.count[i];
-    if (n < 0) clip_chunk<Bf16>(t.in[i], c.out[i], -n, chunk - t.first[i], factor);
-    else clip_chunk<F32>(t.in[i], c.out[i], n, chunk - t.first[i], factor);
+    if (n < 0) clip_chunk<Bf16>(t.in[i], c.out[i], -n, chunk - t.first[i], by);
+    else clip_chunk<F32>(t.in[i], c.out[i], n, chunk - t.first[i], by);
   }
 }
 
