@@ -77,6 +77,30 @@ def test_infinite_logits_are_the_largest(groups, kept, group_sum, biased):
     assert bool(torch.isnan(out["gate"][::2]).all()) and bool(torch.isfinite(out["gate"][1::2]).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("normalize", [False, True])
+def test_a_nan_logit_shows_in_its_row_of_the_gradient(normalize, score, dtype):
+    """In counted rows alone, whichever gradient comes in; masked rows are 0 and the others as they were."""
+    g = torch.Generator().manual_seed(8)
+    clean = (torch.randn(60, 40, generator=g)).to(dtype)
+    x, mask = clean.clone(), torch.ones(60, dtype=torch.bool)
+    x[::3, 5::7] = math.nan
+    mask[::6] = False
+    d, dp = torch.randn(60, 8, generator=g), torch.rand(40, generator=g)
+    how = dict(groups=4, kept=2, score=score, normalize=normalize)
+    bad = torch.zeros(60, dtype=torch.bool)
+    bad[::3] = True
+    for dg, ds in ((d, dp), (d, None), (None, dp)):
+        out = run(x, 8, None, mask, dg, ds, **how)["d_logits"]
+        base = run(clean, 8, None, mask, dg, ds, **how)["d_logits"]
+        shown = torch.isnan(out).any(dim=1)
+        assert torch.equal(shown, bad & mask)
+        assert bool((out[~mask] == 0).all()) and torch.equal(out[~bad], base[~bad])
+        if score == "softmax" or ds is not None or normalize:
+            assert bool(torch.isnan(out[bad & mask]).all(dim=1).any())
+
+
 @pytest.mark.parametrize("normalize", [False, True])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_chosen_scores_of_zero(dtype, normalize):
