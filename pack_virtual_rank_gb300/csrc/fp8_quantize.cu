@@ -99,7 +99,6 @@ template <class T>
 struct Eight;
 template <>
 struct Eight<float> {
-  using P = TF32;
   static constexpr int kWords = 8;
   static __device__ __forceinline__ uint32_t magnitude(uint32_t w) { return w & 0x7fffffffu; }
   static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
@@ -110,7 +109,6 @@ struct Eight<float> {
 };
 template <>
 struct Eight<uint16_t> {
-  using P = TBF16;
   static constexpr int kWords = 4;
   static __device__ __forceinline__ uint32_t magnitude(uint32_t w) { return w & 0x7fff7fffu; }
   static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
@@ -128,7 +126,6 @@ struct Eight<uint16_t> {
 template <class T, bool EDGES>
 __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) fp8_quantize_kernel(const QuantArgs a) {
   using V = Eight<T>;
-  using P = typename V::P;
   constexpr int W = V::kWords;
   __shared__ __align__(16) uint8_t s_t[kBlock * kBlock];
   __shared__ uint32_t s_col[kQuantThreads / 32][kBlock];
@@ -175,7 +172,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) fp8_qua
     if (r < r_end && (!EDGES || (a.vectors && c + 8 <= a.cols))) {
 #pragma unroll
       for (int k = 0; k < W; k += 4) {
-        const uint4 u = ld_stream_v4(reinterpret_cast<const uint32_t*>(from) + k);
+        const uint4 u = ld_once(reinterpret_cast<const uint32_t*>(from) + k);
         v[i][k] = u.x; v[i][k + 1] = u.y; v[i][k + 2] = u.z; v[i][k + 3] = u.w;
       }
     } else {
@@ -184,7 +181,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) fp8_qua
       if (EDGES && r < r_end) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (c + k < a.cols) V::set(v[i], k, P::template load1<false>(from + k));
+          if (c + k < a.cols) V::set(v[i], k, ld_value(from + k));
       }
     }
   }

@@ -63,10 +63,10 @@ template <class T>
 __device__ __forceinline__ uint4 load_vector(const typename T::Elem* x, int64_t n, int skip, int64_t v) {
   constexpr int L = T::P::kLanes;
   const int64_t at = v * L - skip;
-  if (at >= 0 && at + L <= n) return ld_stream_v4(x + at);
+  if (at >= 0 && at + L <= n) return ld_once(x + at);
   float f[L];
 #pragma unroll
-  for (int i = 0; i < L; ++i) f[i] = at + i >= 0 && at + i < n ? T::P::template load1<false>(x + at + i) : 0.0f;
+  for (int i = 0; i < L; ++i) f[i] = at + i >= 0 && at + i < n ? ld_value(x + at + i) : 0.0f;
   return T::P::pack(f);
 }
 struct F32 {

@@ -40,16 +40,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Streaming load of 16 bytes. Not the read-only path: a kernel here may start before the one that
-// writes what it reads has ended.
-__device__ __forceinline__ uint4 ld_once(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
-}
-
 // The three bf16 parts of an fp32 value; an infinity or NaN is its first part alone. Every part multiplies parts of
 // the other operand (six of the nine products), so what one product says about infinities the others must not
 // contradict: a logit that is -inf has to come out as -inf, not as NaN.

@@ -8,6 +8,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stdint.h>
 
 #include <utility>
 
@@ -16,6 +17,20 @@ namespace {
 
 __device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Streaming load of 16 bytes. Not the read-only path: a kernel here may start before the one that
+// writes what it reads has ended.
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+// One value, fp32 or bf16, for the same reason.
+__device__ __forceinline__ float ld_value(const float* p) { return *p; }
+__device__ __forceinline__ float ld_value(const uint32_t* p) { return __uint_as_float(*p); }
+__device__ __forceinline__ float ld_value(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
 template <class... Params, class... Args>
 cudaError_t launch_chained_clusters(void (*kernel)(Params...), int cluster, dim3 grid, int threads, size_t smem,
