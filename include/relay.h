@@ -621,17 +621,17 @@ relay_status_t relay_matmul_fp8(const relay_fp8_matmul_t* what, cudaStream_t str
  * A list of n tensors in device memory: grad[i] holds count[i] elements of dtype[i] (RELAY_F32 or RELAY_BF16), contiguous;
  * count 0 is an empty tensor. The arrays are read during the call alone.
  *
- * relay_grad_norm -- norm[0] (fp32) = sqrt of the sum of all elements' squares, 0 for an empty list. The sum is
- *   exact to fp32's rounding over the whole range of finite values, in a fixed order. A NaN or an infinity shows in norm. A tensor
- *   given twice counts twice. Norms of several lists (ranks) join by the same call over their norms.
- *   Two launches (one for up to 128 KiB) for 512 tensors, one more for each 512 beyond.
+ * relay_grad_norm -- norm[0] (fp32) = sqrt of the sum of all elements' squares, 0 for an empty list. It is within 10 x 2^-24 of
+ *   its value over the whole range of finite values (2^-149 below 2^-126, +inf where fp32 cannot hold it), summed in a fixed order. A NaN or an infinity
+ *   shows in norm. A tensor given twice counts twice. Norms of several lists (ranks) join by the same call over their norms.
+ *   Two launches for 512 tensors, one more for each 512 beyond; one for up to four pieces of 32 KiB, which never span two tensors.
  *   workspace: relay_grad_workspace_size bytes, any alignment.
  *
- * relay_grad_clip -- out[i] = grad[i] * min(1, max_norm / (norm[0] + 1e-6)), rounded once to the tensor's dtype. out NULL, or
- *   with grad[i]'s own address: in place. norm[0] is read on the device, after what precedes the call on the stream. With
- *   nothing to clip, or a norm that is NaN or infinite, the values stay as they are (the caller sees it
- *   in norm). max_norm finite and above 0. No tensor that is written may overlap another. The list is walked from its end: right after
- *   relay_grad_norm over the same list its last 100 MB are still in L2.
+ * relay_grad_clip -- out[i] = grad[i] * min(1, max_norm / (norm[0] + 1e-6)): sum, quotient and product are rounded to fp32 each, and
+ *   the product to the tensor's dtype. out NULL, or with grad[i]'s own address: in place. norm[0] is read on the device, after what
+ *   precedes the call on the stream. With nothing to clip, or a norm that is NaN or infinite, the values stay as they are (the caller
+ *   sees it in norm). max_norm finite and above 0. No tensor that is written may overlap another. The list is walked from its end:
+ *   right after relay_grad_norm over the same list its last 100 MB are still in L2.
  */
 #define RELAY_GRADS_MAX (1 << 20)
 typedef struct relay_grads {

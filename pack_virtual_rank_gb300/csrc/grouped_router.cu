@@ -13,11 +13,13 @@
 // row's largest, in steps of 2^-21 of the largest score (2 of it in all; what is further below is only known to be). Where two
 // neighbours in the choice are nearer than fp32's error allows, and not equal in logit and bias (one row in some hundred), the
 // chosen and a few candidates more are ranked by their values in 64 bits, one to a lane; groups as near to one another are compared
-// by the 64-bit values of their largest. What that does not settle is chosen again in 64 bits as a whole (choose_slow). (All near rows chosen again as a whole: 99 us at
-// 65536 x 256 bf16, eight groups, where 63 us are what the rest takes.)
+// by the 64-bit values of their largest. What that does not settle is chosen again in 64 bits as a whole (choose_slow). (All near rows
+// chosen again as a whole: 99 us at 65536 x 256 bf16, eight groups, and not 73.)
 //
-// Bound by instructions, most of them comparisons and selections, as router.cu's choice is (65536 x 256 bf16, 8 of 256 from 4 of 8
-// groups with a bias: 73 us, its bytes 5); the backward pass 23 us, its bytes 10.
+// Bound by chains of dependent instructions: a round of the choice is a maximum over the row's lanes, a vote and a selection, and 24
+// warps an SM do not hide one another's (the busiest unit is busy 59% of the time; most stalls are waits for a fixed latency). 65536
+// x 256 bf16, 8 of 256 from 4 of 8 groups with a bias: 73 us, its bytes 5. The backward pass waits for memory, the row and then its
+// chosen experts' logits, and for its sums over the row, one behind the other: 24 us, its bytes 10.
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -171,7 +173,8 @@ __device__ __noinline__ int choose_slow(const GroupArgs& a, const T* x, bool cou
   return chosen;
 }
 
-// Blocks an SM holds (four of 8 values a lane spill and are slower; one of 16: 138 us and not 101 at 65536 x 512, eight groups).
+// Blocks an SM holds. Registers that the 64-bit paths want spill at each of these bounds (60 to 140 bytes at three blocks of 8 values a
+// lane); more blocks spill more and are slower, and fewer too: one of 16 values takes 138 us and not 101 at 65536 x 512 bf16, eight groups.
 constexpr int resident(int values) { return values == 8 ? 3 : values == 16 ? 2 : 1; }
 
 template <class T, int N, int L, bool SIGMOID>
@@ -455,6 +458,8 @@ __device__ __forceinline__ float sigmoid_slope(float x, float* slope) {
   return x >= 0.0f ? r : t * r;
 }
 
+// Four blocks an SM of 8 values a lane. Of more there are as many as fit: 16 values in fp32 have 133 registers, one block (65536 x 512:
+// 93 us, its bytes 40; bf16 51), 32 values one block (32768 x 1024: 97 us, bf16 71).
 template <class T, int N, int L>
 __global__ void __launch_bounds__(kRouterThreads, N == 8 ? 4 : 1) sigmoid_backward_kernel(const SigmoidArgs a) {
   constexpr int kRows = 32 / L;
