@@ -169,9 +169,10 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const double* p
   if (threadIdx.x == 0) *norm = (float)sqrt(v);
 }
 
-// factor * after: a factor that fp32 holds to its rounding, and 1, or a power of two that it leaves out.
+// A value is multiplied by factor. Where that is below fp32's normal range: by a power of two, 2^200 times the factor, and the power
+// again, so that neither leaves the range (of a value that the first takes below it nothing is left).
 struct Factor {
-  float factor, after;
+  float factor, power;
 };
 
 template <class T>
@@ -182,14 +183,14 @@ __device__ __forceinline__ void clip_chunk(const void* in, void* out, int64_t n,
   auto* y = static_cast<E*>(out);
   const int skip = (int)(reinterpret_cast<uintptr_t>(in) % 16 / sizeof(E));
   const int64_t v0 = chunk * (kGradThreads * kVectors) + threadIdx.x;
-  if ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) % 16 != 0 || by.after != 1.0f) {
+  if ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) % 16 != 0 || by.power != 1.0f) {
     // the two lie differently on the 16-byte grid, or the factor is a rare one (here alone, it costs the rest nothing:
     // 1% otherwise): neighbouring threads take neighbouring elements
     const int64_t lo = max((int64_t)0, chunk * (kGradThreads * kVectors * L) - skip);
     const int64_t hi = min(n, (chunk + 1) * (kGradThreads * kVectors * L) - skip);
 #pragma unroll 8
     for (int64_t e = lo + threadIdx.x; e < hi; e += kGradThreads)
-      T::P::store1(y + e, __fmul_rn(__fmul_rn(T::P::template load1<true>(x + e), by.factor), by.after));
+      T::P::store1(y + e, __fmul_rn(__fmul_rn(__fmul_rn(T::P::template load1<true>(x + e), by.power), by.factor), by.power));
     return;
   }
   uint4 u[kVectors];
@@ -223,10 +224,12 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
   dep_wait();
   const float total = *norm;
   Factor by{max_norm / (total + 1e-6f), 1.0f};
-  if (by.factor < FLT_MIN) by = Factor{max_norm * 0x1p100f / (total + 1e-6f), 0x1p-100f};  // max_norm is below 4
   // nothing to clip, or a norm that says that something is wrong: the values stay as they are
-  if (!(by.factor < 1.0f) || !(total < INFINITY)) by = Factor{1.0f, 1.0f};
-  if (by.factor == 1.0f && in_place) return;
+  const bool clips = by.factor < 1.0f && total < INFINITY;
+  if (!clips && in_place) return;
+  if (!clips) by.factor = 1.0f;
+  // max_norm is below 4 here, and total above 2^-24
+  else if (by.factor < FLT_MIN) by = Factor{max_norm * 0x1p100f / ((total + 1e-6f) * 0x1p-100f), 0x1p-100f};
   for (int k = blockIdx.x; k < t.chunks; k += gridDim.x) {
     const int chunk = t.chunks - 1 - k, i = tensor_of(t, chunk);
     const int64_t n = t.count[i];
